@@ -111,6 +111,66 @@ ffn_status ffn_rmsnorm(const void *x, const void *g, void *n, int64_t rows, int6
                        float eps, ffn_dtype dtype, void *stream);
 
 /* ------------------------------------------------------------------------
+ * ffn_add_rmsnorm -- the residual's addition with the norm after it, one pass:
+ *   r[t,c] = x[t,c] + res[t,c]      (fp32 sum, rounded once to `dtype`)
+ *   n[t,c] = RMSNorm(r)[t,c] * g[c] (of the stored r; the bits of ffn_rmsnorm
+ *                                    within the rounding of the row's sum)
+ * In a pre-norm layer x is what the block before computed and res the
+ * stream it is added to; r is the stream after it.  No page describes the
+ * step.
+ *   x, res [rows x d], g [d], r and n [rows x d], all of `dtype`.  res may be
+ *   NULL (r = x), r may be NULL (not stored).  r may equal x or res, and n
+ *   may equal x or res where r does not; any other overlap of an output with
+ *   an input or an output is FFN_ERR_ALIAS.  rows >= 0, 1 <= d < 2^30.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_add_rmsnorm(const void *x, const void *res, const void *g, void *r, void *n, int64_t rows, int64_t d,
+                           float eps, ffn_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_add_rmsnorm_e4m3 -- ffn_add_rmsnorm with the norm's output in 8 bits:
+ *   v = RMSNorm(r) * g in fp32, a = max(max |v|, 2^-100) over the columns of
+ *   one scale, scales = a / 448, q = e4m3(v * (448 / a)) (nearest even), so
+ *   v is about q * scale and the largest value of a group is +-448.
+ *   group: columns per scale: 0 (one scale per row, scales [rows]), 32, 64 or
+ *   128 (scales [rows x ceil(d / group)]; the last group of a row may be
+ *   shorter).  q [rows x d]: e4m3 codes ("fn" encoding, as in ffn_fp8_weight).
+ *   A NaN in v makes its scale NaN.  q and scales overlap nothing; r as in
+ *   ffn_add_rmsnorm.  FFN_ERR_SHAPE for another group.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_add_rmsnorm_e4m3(const void *x, const void *res, const void *g, void *r, uint8_t *q, float *scales,
+                                int64_t rows, int64_t d, int64_t group, float eps, ffn_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_moe_route -- the experts of a routed feed-forward layer that each token
+ * goes to, and their weights.  With l the token's logits:
+ *   s_e = softmax(l)_e, or 1 / (1 + exp(-l_e)) with FFN_ROUTE_SIGMOID
+ *   order_e = s_e + bias_e (bias given: it steers the choice, not the weight),
+ *   else l_e
+ *   groups > 1: experts in `groups` runs of experts / groups; a group's score
+ *   is the sum of its two largest s_e + bias_e, and only the topk_groups
+ *   groups of the largest score are eligible
+ *   topk_idx[t, j]: the expert of the j-th largest order
+ *   topk_w[t, j] = s of that expert * scale, with FFN_ROUTE_RENORM divided by
+ *   max(the sum of the chosen s, 2^-100).
+ * Ties go to the lower index.  Scores and sums are fp32, but the choice is the
+ * one of the formula in 64 bits (close scores are compared again in fp64).
+ * A logit of -inf or NaN is never chosen (+inf counts as the largest finite
+ * float, |bias| as at most 1e30, a NaN bias as -1e30): a slot that no
+ * eligible expert is left for gets index -1 and weight 0, so a row of -inf
+ * (padding) chooses nothing.
+ *   logits [rows x experts] of `dtype`, bias [experts] fp32 or NULL, topk_idx
+ *   [rows x k] int32, topk_w [rows x k] fp32.  1 <= experts <= 1024, 1 <= k <=
+ *   32, 1 <= groups <= 32, experts % groups == 0, 1 <= topk_groups <= groups,
+ *   k <= topk_groups * (experts / groups); else FFN_ERR_SHAPE.  Outputs
+ *   overlap nothing.
+ * ---------------------------------------------------------------------- */
+#define FFN_ROUTE_SIGMOID 1u
+#define FFN_ROUTE_RENORM 2u
+ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_idx, float *topk_w, int64_t rows,
+                         int64_t experts, int64_t k, int64_t groups, int64_t topk_groups, float scale,
+                         ffn_dtype dtype, uint32_t flags, void *stream);
+
+/* ------------------------------------------------------------------------
  * ffn_swiglu -- h[i] = silu(gate[i]) * up[i], silu in fp32.
  * "When to hand-write a GPU kernel on Apple Silicon", Rung 1 (one pass,
  * activation upcast to fp32).

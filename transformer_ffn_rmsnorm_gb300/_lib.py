@@ -27,6 +27,7 @@ FFN_F32, FFN_F16, FFN_BF16 = 0, 1, 2
 FFN_AUTO, FFN_GATEUP_FUSED, FFN_GATEUP_UNFUSED, FFN_PATH_GEMM, FFN_PATH_GEMV = 0, 1, 2, 4, 8
 FFN_ACT_SINGLE, FFN_ACT_SPLIT, FFN_PREPARED_WEIGHTS = 16, 32, 64
 FFN_RESIDUAL, FFN_DECODE_ONE_KERNEL = 128, 256
+FFN_ROUTE_SIGMOID, FFN_ROUTE_RENORM = 1, 2
 
 
 class Q4Weight(ctypes.Structure):
@@ -44,6 +45,12 @@ class Q8Weight(ctypes.Structure):
 # name -> (restype, argtypes), in the order of include/ffn.h
 SIGNATURES = {
     "ffn_rmsnorm": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_float, c_int, c_void_p]),
+    "ffn_add_rmsnorm": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_float, c_int,
+                                c_void_p]),
+    "ffn_add_rmsnorm_e4m3": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                     c_int64, c_float, c_int, c_void_p]),
+    "ffn_moe_route": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_int64,
+                              c_float, c_int, c_uint32, c_void_p]),
     "ffn_swiglu": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p]),
     "ffn_block_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, c_int, c_uint32,
                                           ctypes.POINTER(c_size_t)]),

@@ -170,7 +170,7 @@ const char *kernel_name(int kind) {
     static const char *names[K_NUM_KINDS] = {
         "prepare", "rmsnorm", "swiglu", "simt_gateup", "simt_down", "gemv_norm",
         "gemv_gateup", "gemv_down", "gemm_gateup", "gemm_down", "selftest", "splitk_reduce",
-        "gemv_fused"};
+        "gemv_fused", "add_rmsnorm", "moe_route", "moe_plan", "moe_gateup", "moe_down", "moe_combine"};
     return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : "unknown";
 }
 
@@ -252,6 +252,69 @@ ffn_status ffn_rmsnorm(const void *x, const void *g, void *n, int64_t rows, int6
     if (overlaps(rn, rg)) return FFN_ERR_ALIAS;
     if (rows == 0) return FFN_OK;
     return from_cuda(launch_rmsnorm(x, g, n, rows, d, eps, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+static ffn_status add_rmsnorm(const void *x, const void *res, const void *g, void *r, void *out, size_t out_es,
+                              float *scales, int64_t rows, int64_t d, int64_t group, float eps, ffn_dtype dtype,
+                              bool quant, void *stream) {
+    if (!g || (rows != 0 && (!x || !out || (quant && !scales)))) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    if (rows < 0 || d < 1 || rows > INT32_MAX || d > (INT32_MAX >> 1)) return FFN_ERR_SHAPE;
+    if (quant && group != 0 && group != 32 && group != 64 && group != 128) return FFN_ERR_SHAPE;
+    if (rows == 0) return FFN_OK;
+    for (const void *p : {x, res, g, static_cast<const void *>(r), static_cast<const void *>(out),
+                          static_cast<const void *>(scales)})
+        if (!aligned16(p)) return FFN_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(rows) * d, es = dtype_size(dtype);
+    const size_t ng = quant ? static_cast<size_t>(rows) * (group ? (d + group - 1) / group : 1) : 0;
+    const Range rx{x, n * es}, rres{res, n * es}, rg{g, static_cast<size_t>(d) * es}, rr{r, n * es},
+        ro{out, n * out_es}, rs{scales, ng * 4};
+    // r may take x's or res's place, and n that of either unless r does; a
+    // row is read before any of it is written
+    for (const Range &in : {rx, rres}) {
+        if (r != in.p && overlaps(rr, in)) return FFN_ERR_ALIAS;
+        if ((quant || out != in.p) && overlaps(ro, in)) return FFN_ERR_ALIAS;
+        if (overlaps(rs, in)) return FFN_ERR_ALIAS;
+    }
+    for (const Range &o : {rr, ro, rs})
+        if (overlaps(o, rg)) return FFN_ERR_ALIAS;
+    if (overlaps(rr, ro) || overlaps(rr, rs) || overlaps(ro, rs)) return FFN_ERR_ALIAS;
+    return from_cuda(launch_add_rmsnorm(x, res, g, r, out, scales, rows, d, group, eps, dtype, quant,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+ffn_status ffn_add_rmsnorm(const void *x, const void *res, const void *g, void *r, void *n, int64_t rows, int64_t d,
+                           float eps, ffn_dtype dtype, void *stream) {
+    return add_rmsnorm(x, res, g, r, n, valid_dtype(dtype) ? dtype_size(dtype) : 0, nullptr, rows, d, 0, eps, dtype,
+                       false, stream);
+}
+
+ffn_status ffn_add_rmsnorm_e4m3(const void *x, const void *res, const void *g, void *r, uint8_t *q, float *scales,
+                                int64_t rows, int64_t d, int64_t group, float eps, ffn_dtype dtype, void *stream) {
+    return add_rmsnorm(x, res, g, r, q, 1, scales, rows, d, group, eps, dtype, true, stream);
+}
+
+ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_idx, float *topk_w, int64_t rows,
+                         int64_t experts, int64_t k, int64_t groups, int64_t topk_groups, float scale,
+                         ffn_dtype dtype, uint32_t flags, void *stream) {
+    if (rows != 0 && (!logits || !topk_idx || !topk_w)) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    if (flags & ~(FFN_ROUTE_SIGMOID | FFN_ROUTE_RENORM)) return FFN_ERR_FLAGS;
+    if (rows < 0 || rows > INT32_MAX || experts < 1 || experts > 1024 || k < 1 || k > 32) return FFN_ERR_SHAPE;
+    if (groups < 1 || groups > 32 || experts % groups || topk_groups < 1 || topk_groups > groups) return FFN_ERR_SHAPE;
+    if (k > topk_groups * (experts / groups)) return FFN_ERR_SHAPE;
+    if (rows == 0) return FFN_OK;
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w)) return FFN_ERR_ALIGN;
+    const Range rl{logits, static_cast<size_t>(rows) * experts * dtype_size(dtype)},
+        rb{bias, static_cast<size_t>(experts) * 4}, ri{topk_idx, static_cast<size_t>(rows) * k * 4},
+        rw{topk_w, static_cast<size_t>(rows) * k * 4};
+    for (const Range &o : {ri, rw})
+        if (overlaps(o, rl) || overlaps(o, rb)) return FFN_ERR_ALIAS;
+    if (overlaps(ri, rw)) return FFN_ERR_ALIAS;
+    return from_cuda(launch_moe_route(logits, bias, topk_idx, topk_w, rows, static_cast<int>(experts),
+                                      static_cast<int>(k), static_cast<int>(groups), static_cast<int>(topk_groups),
+                                      scale, (flags & FFN_ROUTE_SIGMOID) != 0, (flags & FFN_ROUTE_RENORM) != 0, dtype,
+                                      static_cast<cudaStream_t>(stream)));
 }
 
 ffn_status ffn_swiglu(const void *gate, const void *up, void *h, int64_t count, ffn_dtype dtype,

@@ -29,6 +29,12 @@ enum KernelKind : int {
     K_SELFTEST,
     K_SPLITK_REDUCE,
     K_GEMV_FUSED,
+    K_ADD_RMSNORM,
+    K_MOE_ROUTE,
+    K_MOE_PLAN,
+    K_MOE_GATEUP,
+    K_MOE_DOWN,
+    K_MOE_COMBINE,
     K_NUM_KINDS
 };
 const char *kernel_name(int kind);
@@ -83,6 +89,15 @@ cudaError_t launch_rmsnorm_split(const void *x, const void *g, void *n_hi, void 
 // 16-bit x and g of type dt_in, n written as fp16 (operand of fp16 tensor ops).
 cudaError_t launch_rmsnorm_to_f16(const void *x, const void *g, void *n, int64_t rows, int64_t d,
                                   float eps, int dt_in, cudaStream_t s, const float *ss_in = nullptr);
+// r = x + res (res may be null; r may be null: not stored), then the norm of
+// r: as n in the storage type (quant false), or as e4m3 with a scale for each
+// `group` columns (0: for each row).
+cudaError_t launch_add_rmsnorm(const void *x, const void *res, const void *g, void *r, void *out, float *scales,
+                               int64_t rows, int64_t d, int64_t group, float eps, int dt, bool quant, cudaStream_t s);
+// Each row's k experts and weights (moe_route.cu); experts <= 1024, k <= 32.
+cudaError_t launch_moe_route(const void *logits, const float *bias, int32_t *idx, float *w, int64_t rows, int experts,
+                             int k, int groups, int topk_groups, float scale, bool sigmoid, bool renorm, int dt,
+                             cudaStream_t s);
 // dst[i] = fp16(src[i] * 2^8) for 16-bit src of type dt; out-of-range values
 // set DEVERR_RANGE in the device status word.
 cudaError_t launch_prepare_weights(const void *src, void *dst, int64_t count, int dt, cudaStream_t s);

@@ -18,6 +18,7 @@ from . import _lib
 from ._lib import (FFN_AUTO, FFN_BF16, FFN_F16, FFN_F32, FFN_GATEUP_FUSED,  # noqa: F401
                    FFN_GATEUP_UNFUSED, FFN_ACT_SINGLE, FFN_ACT_SPLIT, FFN_PATH_GEMM,
                    FFN_PATH_GEMV, FFN_PREPARED_WEIGHTS, FFN_RESIDUAL, FFN_DECODE_ONE_KERNEL,
+                   FFN_ROUTE_RENORM, FFN_ROUTE_SIGMOID,
                    Fp8Weight, Q4Weight, Q8Weight)
 
 _DT = {torch.float32: FFN_F32, torch.float16: FFN_F16, torch.bfloat16: FFN_BF16}
@@ -58,6 +59,118 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _expect(name: str, t, shape, dtype, device):
+    """A tensor the C side cannot look into: its sizes, type and place."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of the input")
+
+
+def _launch(fn, where: str, device: int, stream, *args):
+    """fn(*args, stream) with `device` current; the current stream by default."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(fn, where, device, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    status = fn(*args, s)
+    if status != 0:
+        raise FFNError(status, where)
+
+
+def _rows_of(x: torch.Tensor):
+    """(rows, d, device index) of a [..., d] input tensor."""
+    dev = x.get_device()
+    if dev < 0 or not x.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    d = x.shape[-1]
+    return (x.numel() // d if d else 0), d, dev
+
+
+def ffn_add_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
+                    r_out: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """(r, n): r = x + res (x itself without `res`) and n = RMSNorm(r) * g.
+
+    `r_out` may be x or res (in place); without it a new tensor takes r."""
+    rows, d, dev = _rows_of(x)
+    dt, shape = x.dtype, x.shape
+    code = _dtype(x)
+    _expect("g", g, (d,), dt, dev)
+    if res is not None:
+        _expect("res", res, shape, dt, dev)
+        if r_out is None:
+            r_out = torch.empty_like(x)
+    if r_out is not None:
+        _expect("r_out", r_out, shape, dt, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _expect("out", out, shape, dt, dev)
+    _launch(_LIB.ffn_add_rmsnorm, "ffn_add_rmsnorm", dev, stream, x.data_ptr(),
+            None if res is None else res.data_ptr(), g.data_ptr(), None if r_out is None else r_out.data_ptr(),
+            out.data_ptr(), rows, d, eps, code)
+    return (x if r_out is None else r_out), out
+
+
+def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
+                         group: int = 0, r_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         scales: torch.Tensor | None = None, stream=None):
+    """(r, q, scales): as ffn_add_rmsnorm with the norm's output as
+    torch.float8_e4m3fn codes and fp32 scales, one per row (group 0, shape
+    [rows, 1]) or per `group` columns (32, 64 or 128; [rows, ceil(d / group)]):
+    RMSNorm(r) * g is about q * scale."""
+    rows, d, dev = _rows_of(x)
+    dt, shape = x.dtype, x.shape
+    code = _dtype(x)
+    _expect("g", g, (d,), dt, dev)
+    if res is not None:
+        _expect("res", res, shape, dt, dev)
+        if r_out is None:
+            r_out = torch.empty_like(x)
+    if r_out is not None:
+        _expect("r_out", r_out, shape, dt, dev)
+    sshape = (*shape[:-1], -(-d // group) if group > 0 else 1)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _expect("out", out, shape, torch.float8_e4m3fn, dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
+    else:
+        _expect("scales", scales, sshape, torch.float32, dev)
+    _launch(_LIB.ffn_add_rmsnorm_e4m3, "ffn_add_rmsnorm_e4m3", dev, stream, x.data_ptr(),
+            None if res is None else res.data_ptr(), g.data_ptr(), None if r_out is None else r_out.data_ptr(),
+            out.data_ptr(), scales.data_ptr(), rows, d, group, eps, code)
+    return (x if r_out is None else r_out), out, scales
+
+
+def ffn_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, groups: int = 1,
+                  topk_groups: int = 1, scale: float = 1.0, flags: int = 0, idx: torch.Tensor | None = None,
+                  weights: torch.Tensor | None = None, stream=None):
+    """(idx int32 [rows, k], weights fp32 [rows, k]) of a [rows, experts] tensor
+    of router logits; flags: FFN_ROUTE_SIGMOID, FFN_ROUTE_RENORM.  A slot
+    that no eligible expert is left for has index -1 and weight 0."""
+    rows, experts, dev = _rows_of(logits)
+    code = _dtype(logits)
+    if bias is not None:
+        _expect("bias", bias, (experts,), torch.float32, dev)
+    shape = (*logits.shape[:-1], k)
+    if idx is None:
+        idx = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    else:
+        _expect("idx", idx, shape, torch.int32, dev)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _expect("weights", weights, shape, torch.float32, dev)
+    _launch(_LIB.ffn_moe_route, "ffn_moe_route", dev, stream, logits.data_ptr(),
+            None if bias is None else bias.data_ptr(), idx.data_ptr(), weights.data_ptr(), rows, experts, k, groups,
+            topk_groups, scale, code, flags)
+    return idx, weights
 
 
 def ffn_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, out: torch.Tensor | None = None,
