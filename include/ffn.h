@@ -171,6 +171,41 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
                          ffn_dtype dtype, uint32_t flags, void *stream);
 
 /* ------------------------------------------------------------------------
+ * ffn_moe_forward -- the routed feed-forward block: for every token the SwiGLU
+ * blocks of its k experts, weighted and added ("Unfusing a Kernel Made It
+ * 1.63x Faster", Finding 1, describes one such block; no page describes the
+ * routed form):
+ *   y_t = [res_t +] sum_j topk_w[t,j] * W_down[e] ( silu(W_gate[e] x_t) * (W_up[e] x_t) ),
+ *   e = topk_idx[t,j]
+ *   x [rows x d] (the layer's normalised input), topk_idx and topk_w [rows x
+ *   k] as ffn_moe_route writes them, w_gate and w_up [experts x ffn x d],
+ *   w_down [experts x d x ffn], res [rows x d] or NULL, y [rows x d].  A slot
+ *   whose index is not in 0 .. experts - 1 is skipped (its weight is not
+ *   read), an expert may appear twice in a row; a token without an expert
+ *   gets y = res, or 0.  y may equal res and overlaps nothing else.
+ *   dtype: FFN_F16 or FFN_BF16 (x, weights, res, y).  With
+ *   FFN_PREPARED_WEIGHTS the weights are ffn_prepare_weights output (fp16 of
+ *   w * 2^8) and the products run on fp16 operands: a bf16 x must lie in
+ *   fp16's range (a finite value beyond it becomes infinite and records
+ *   FFN_ERR_RANGE in the device status word), and |h| below 1.6e7.  No other flag.
+ *   h = silu(G) * U is rounded once to the operand type; everything else is
+ *   fp32, results are added in slot order and rounded once.
+ *   d % 8 == 0, ffn % 8 == 0, 1 <= experts <= 1024, 1 <= k <= 32; rows * k,
+ *   experts * d and experts * ffn at most 2^30.  rows == 0 launches nothing.
+ *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned (sorted
+ *   positions, h, one fp32 row per (token, slot) pair); not shared by calls
+ *   that may run at the same time.  The whole call is on `stream` and never
+ *   waits for the device: it can be captured in a graph, and which experts
+ *   are used is read when it runs.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_moe_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, ffn_dtype dtype,
+                                   uint32_t flags, size_t *bytes);
+ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *topk_w, const void *w_gate,
+                           const void *w_up, const void *w_down, const void *res, void *y, int64_t rows, int64_t d,
+                           int64_t ffn, int64_t experts, int64_t k, ffn_dtype dtype, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * ffn_swiglu -- h[i] = silu(gate[i]) * up[i], silu in fp32.
  * "When to hand-write a GPU kernel on Apple Silicon", Rung 1 (one pass,
  * activation upcast to fp32).

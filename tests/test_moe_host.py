@@ -80,3 +80,39 @@ def test_wrappers_refuse_what_the_library_cannot_see():
         ffn.ffn_add_rmsnorm_e4m3(x, x[0], 1e-6)
     with pytest.raises(ValueError):
         ffn.ffn_moe_route(x, 2)
+
+
+def test_moe_forward_refusals(lib):
+    x, idx, w, wg, wu, wd, res, y, ws = ptrs(9)
+    B = _lib.FFN_BF16
+
+    def need(rows=4, d=64, ffn=128, experts=8, k=2, dtype=B, flags=0):
+        out = ctypes.c_size_t(0)
+        return lib.ffn_moe_workspace_bytes(rows, d, ffn, experts, k, dtype, flags, ctypes.byref(out)), out.value
+
+    def call(x=x, idx=idx, w=w, wg=wg, wu=wu, wd=wd, res=res, y=y, rows=4, d=64, ffn=128, experts=8, k=2, dtype=B,
+             flags=0, ws=ws, bytes_=1 << 27):
+        return lib.ffn_moe_forward(x, idx, w, wg, wu, wd, res, y, rows, d, ffn, experts, k, dtype, flags, ws, bytes_,
+                                   None)
+
+    assert need()[0] == _lib.FFN_OK and need()[1] >= 8 * (128 * 2 + 64 * 4)
+    assert need(flags=_lib.FFN_PREPARED_WEIGHTS)[1] > need()[1]
+    assert need(rows=0) == (_lib.FFN_OK, 0)
+    for name in ("x", "idx", "w", "wg", "wu", "wd", "y"):
+        assert call(**{name: None}) == _lib.FFN_ERR_NULL, name
+    for bad in ({"dtype": _lib.FFN_F32}, {"dtype": 5}):
+        assert call(**bad) == _lib.FFN_ERR_DTYPE and need(**bad)[0] == _lib.FFN_ERR_DTYPE
+    for flags in (_lib.FFN_RESIDUAL, _lib.FFN_PATH_GEMV, 1 << 20):
+        assert call(flags=flags) == _lib.FFN_ERR_FLAGS
+    for bad in ({"rows": -1}, {"d": 0}, {"d": 68}, {"ffn": 100}, {"experts": 0}, {"experts": 1025}, {"k": 0},
+                {"k": 33}, {"rows": 1 << 30}, {"experts": 1024, "ffn": 1 << 21}, {"experts": 1024, "d": 1 << 21}):
+        assert call(**bad) == _lib.FFN_ERR_SHAPE and need(**bad)[0] == _lib.FFN_ERR_SHAPE, bad
+    n = need()[1]
+    assert call(bytes_=n - 1) == _lib.FFN_ERR_WORKSPACE
+    assert call(ws=None) == _lib.FFN_ERR_WORKSPACE
+    for name, p in (("x", x), ("wg", wg), ("res", res), ("ws", ws)):
+        assert call(**{name: ctypes.c_void_p(p.value + 8)}) == _lib.FFN_ERR_ALIGN, name
+    for bad in (x, wd, w, ctypes.c_void_p(res.value + 16), ctypes.c_void_p(ws.value + 256)):
+        assert call(y=bad) == _lib.FFN_ERR_ALIAS
+    assert call(ws=wu) == _lib.FFN_ERR_ALIAS
+    assert call(rows=0) == _lib.FFN_OK

@@ -51,6 +51,11 @@ SIGNATURES = {
                                      c_int64, c_float, c_int, c_void_p]),
     "ffn_moe_route": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_int64,
                               c_float, c_int, c_uint32, c_void_p]),
+    "ffn_moe_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, c_int64, c_int64, c_int, c_uint32,
+                                        ctypes.POINTER(c_size_t)]),
+    "ffn_moe_forward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                c_int64, c_int64, c_int64, c_int64, c_int64, c_int, c_uint32, c_void_p, c_size_t,
+                                c_void_p]),
     "ffn_swiglu": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p]),
     "ffn_block_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, c_int, c_uint32,
                                           ctypes.POINTER(c_size_t)]),

@@ -16,6 +16,7 @@
 
 #include "../../include/ffn.h"
 #include "ffn_internal.cuh"
+#include "moe.cuh"
 
 __device__ unsigned g_ffn_status_word;
 
@@ -315,6 +316,114 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
                                       static_cast<int>(k), static_cast<int>(groups), static_cast<int>(topk_groups),
                                       scale, (flags & FFN_ROUTE_SIGMOID) != 0, (flags & FFN_ROUTE_RENORM) != 0, dtype,
                                       static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// what the routed block's entries share: sizes, and the workspace's parts
+struct MoePlan {
+    int64_t pairs;
+    size_t plan, x16, h, part;   // bytes, in this order
+    size_t total() const { return plan + x16 + h + part; }
+};
+
+ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, int64_t step, int tile,
+                    bool x16, MoePlan *m) {
+    if (rows < 0 || d < 1 || ffn < 1 || experts < 1 || experts > moe::kMaxExperts || k < 1 || k > 32)
+        return FFN_ERR_SHAPE;
+    if (d % step || ffn % step) return FFN_ERR_SHAPE;
+    // sorted rows, weight rows and units of work are 32-bit
+    const int64_t most = int64_t{1} << 30;
+    if (rows > most || d > most || ffn > most || rows * k > most) return FFN_ERR_SHAPE;
+    if (experts * d > most || experts * ffn > most) return FFN_ERR_SHAPE;
+    m->pairs = rows * k;
+    if (moe::max_tiles(m->pairs, experts, tile) * ((std::max(d, ffn) + 127) / 128) > most) return FFN_ERR_SHAPE;
+    const size_t p = static_cast<size_t>(m->pairs);
+    m->plan = rows ? moe_plan_bytes(m->pairs, experts, tile) : 0;
+    m->x16 = x16 ? align256(static_cast<size_t>(rows) * d * 2) : 0;
+    m->h = align256(p * ffn * 2);
+    m->part = align256(p * d * 4);
+    return FFN_OK;
+}
+
+// the checks that follow the sizes: pointers given, their alignment, overlaps
+ffn_status check_moe(const void *x, const int32_t *idx, const float *w, const Range *weights, int nweights,
+                     const void *res, const void *y, int64_t rows, int64_t d, int64_t k, const MoePlan &m,
+                     void *workspace, size_t workspace_bytes) {
+    if (!workspace || workspace_bytes < m.total()) return FFN_ERR_WORKSPACE;
+    for (const void *p : {x, static_cast<const void *>(idx), static_cast<const void *>(w), res, y,
+                          static_cast<const void *>(workspace)})
+        if (!aligned16(p)) return FFN_ERR_ALIGN;
+    const size_t xb = static_cast<size_t>(rows) * d * 2, ib = static_cast<size_t>(rows) * k * 4;
+    const Range ry{y, xb}, rws{workspace, m.total()};
+    for (int i = 0; i < nweights; ++i) {
+        if (!aligned16(weights[i].p)) return FFN_ERR_ALIGN;
+        if (overlaps(ry, weights[i]) || overlaps(rws, weights[i])) return FFN_ERR_ALIAS;
+    }
+    for (const Range &in : {Range{x, xb}, Range{idx, ib}, Range{w, ib}})
+        if (overlaps(ry, in) || overlaps(rws, in)) return FFN_ERR_ALIAS;
+    const Range rr{res, xb};   // y may take res's place
+    if ((y != res && overlaps(ry, rr)) || overlaps(rws, rr) || overlaps(ry, rws)) return FFN_ERR_ALIAS;
+    return FFN_OK;
+}
+
+ffn_status plan_moe16(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, ffn_dtype dtype,
+                      uint32_t flags, MoePlan *m) {
+    if (dtype != FFN_F16 && dtype != FFN_BF16) return FFN_ERR_DTYPE;
+    if (flags & ~FFN_PREPARED_WEIGHTS) return FFN_ERR_FLAGS;
+    return plan_moe(rows, d, ffn, experts, k, 8, kMoeTile, (flags & FFN_PREPARED_WEIGHTS) && dtype == FFN_BF16, m);
+}
+
+}  // namespace
+
+extern "C" {
+
+ffn_status ffn_moe_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, ffn_dtype dtype,
+                                   uint32_t flags, size_t *bytes) {
+    if (!bytes) return FFN_ERR_NULL;
+    MoePlan m;
+    const ffn_status st = plan_moe16(rows, d, ffn, experts, k, dtype, flags, &m);
+    if (st != FFN_OK) return st;
+    *bytes = m.total();
+    return FFN_OK;
+}
+
+ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *topk_w, const void *w_gate,
+                           const void *w_up, const void *w_down, const void *res, void *y, int64_t rows, int64_t d,
+                           int64_t ffn, int64_t experts, int64_t k, ffn_dtype dtype, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    if (!w_gate || !w_up || !w_down || (rows != 0 && (!x || !topk_idx || !topk_w || !y))) return FFN_ERR_NULL;
+    MoePlan m;
+    ffn_status st = plan_moe16(rows, d, ffn, experts, k, dtype, flags, &m);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    const size_t wb = static_cast<size_t>(experts) * ffn * d * 2;
+    const Range weights[3] = {{w_gate, wb}, {w_up, wb}, {w_down, wb}};
+    st = check_moe(x, topk_idx, topk_w, weights, 3, res, y, rows, d, k, m, workspace, workspace_bytes);
+    if (st != FFN_OK) return st;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, kMoeTile);
+    void *x16 = m.x16 ? ws + m.plan : nullptr;
+    void *h = ws + m.plan + m.x16;
+    float *part = reinterpret_cast<float *>(ws + m.plan + m.x16 + m.h);
+    // prepared weights: fp16 operands; the weights' 2^8 is undone on G and U,
+    // h is stored times 2^-8 and the two cancel in the down product
+    const bool prepared = (flags & FFN_PREPARED_WEIGHTS) != 0;
+    const int op = prepared ? static_cast<int>(DT_F16) : static_cast<int>(dtype);
+    const float w_unscale = prepared ? 1.f / kPreparedScale : 1.f, h_scale = prepared ? 1.f / 256.f : 1.f;
+    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), kMoeTile, plan, x,
+                                    x16, d, dtype, false, s);
+    if (e == cudaSuccess)
+        e = launch_moe_gateup(op, plan, x16 ? x16 : x, w_gate, w_up, h, rows, m.pairs, d, ffn, experts, w_unscale,
+                              h_scale, s);
+    if (e == cudaSuccess)
+        e = launch_moe_down(op, plan, h, w_down, part, m.pairs, d, ffn, experts, w_unscale / h_scale, s);
+    if (e == cudaSuccess) e = launch_moe_combine(plan, topk_w, part, res, y, rows, static_cast<int>(k), d, dtype, s);
+    return from_cuda(e);
 }
 
 ffn_status ffn_swiglu(const void *gate, const void *up, void *h, int64_t count, ffn_dtype dtype,

@@ -1,0 +1,423 @@
+// moe_gemm.cu -- the routed block's two products with 16-bit weights, on the
+// 5th-generation tensor cores.
+//
+//   gate/up:  h[r, f]    = silu(W_gate[e] x_t)_f * (W_up[e] x_t)_f   for sorted row r, its token t
+//   down:     part[r, o] = (W_down[e] h_r)_o                         (fp32)
+//
+// CTA pairs (tcgen05 .cta_group::2): a unit of work is 256 weight rows (128
+// in each CTA) against one token tile of n <= 256 columns of one expert.  The
+// weights are the M operand, loaded by TMA as 128 x 64 boxes; the tokens are
+// the N operand, each CTA holding half of the columns.  The gate/up product
+// gathers the tokens' rows of x straight into shared memory (tile::gather4
+// TMA loads of four rows, one per lane), so no sorted copy of x is made; the down
+// product reads the sorted rows of h in boxes of eight.
+//
+// What bounds it: with few tokens the stream of weights (the ring keeps
+// 130-190 KB of loads in flight per SM); with many the tensor pipe.  Why the
+// tile is 256 x 256: per 64 k values a CTA takes 32 KB of gate and up rows and 16 KB of
+// tokens for 1024 cycles of MMAs, 48 bytes a cycle from L2; with 128 columns
+// it would be 80.  The price is tensor memory: gate and up together fill its
+// 512 columns, so a wide gate/up tile's epilogue does not overlap the next
+// tile's MMAs.  Where every tile of the call is at most 128 wide (plan.header[1]) there are two accumulators
+// and it does; the down product always has two.
+//
+// Roles: warp 0 loads (all lanes: one gather or box each), warp 1 issues the
+// MMAs (one thread of the even CTA), warps 2-9 read the accumulators (lane =
+// weight row, column = token): for a fixed column a warp's 32 lanes store 32
+// neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "moe.cuh"
+
+namespace ffn {
+namespace {
+
+using moe::Plan;
+using moe::Unit;
+
+constexpr int kBM = 128, kBK = 64, kTile = kMoeTile;
+constexpr uint32_t kABytes = kBM * kBK * 2;                // one CTA's weight rows of a k block
+constexpr uint32_t kBBytes = (kTile / 2) * kBK * 2;        // room for its half of the tokens
+constexpr uint32_t kTmemCols = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+enum Mode { GATEUP = 0, DOWN = 1 };
+
+// A stage holds KSUB blocks of 64 k values: gate rows, up rows, tokens, or
+// (two such blocks) down rows, tokens.
+template <int MODE> struct Ring {
+    static constexpr int NMAT = MODE == GATEUP ? 2 : 1;
+    static constexpr int KSUB = MODE == GATEUP ? 1 : 2;
+    static constexpr uint32_t SUB_BYTES = NMAT * kABytes + kBBytes;
+    static constexpr uint32_t STAGE_BYTES = KSUB * SUB_BYTES;
+    static constexpr int STAGES = static_cast<int>((225u * 1024u) / STAGE_BYTES);
+    static constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+    static_assert(STAGES >= 3 && SMEM_BYTES > 114 * 1024, "one CTA per SM: each allocates all of tensor memory");
+};
+
+struct Params {
+    const int *header;
+    const int4 *tiles;
+    const int *row_token;
+    int nf;            // feature tiles of 256 rows
+    int wrows;         // weight rows of an expert (ffn or d)
+    int nkb;           // 64-wide k blocks
+    void *out;         // h (operand type) or part (fp32), [pairs x wrows]
+    float acc_scale, out_scale;
+    unsigned *err;
+};
+
+__device__ __forceinline__ void gather4_pair(uint32_t dst, const void *map, uint32_t bar, int x, int r0, int r1, int r2,
+                                             int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+
+template <int MODE, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+                    const __grid_constant__ CUtensorMap map_b, const Params p) {
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    using RG = Ring<MODE>;
+    constexpr int STAGES = RG::STAGES, KSUB = RG::KSUB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
+    __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
+    __shared__ uint32_t s_tmem_base;
+    __shared__ int s_abort, s_never;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    auto sA = [&](int s, int j, int m) { return base + s * RG::STAGE_BYTES + j * RG::SUB_BYTES + m * kABytes; };
+    auto sB = [&](int s, int j) { return base + s * RG::STAGE_BYTES + j * RG::SUB_BYTES + RG::NMAT * kABytes; };
+    auto full = [&](int s) { return ptx::smem_u32(&bar_full[s]); };
+    auto empty = [&](int s) { return ptx::smem_u32(&bar_empty[s]); };
+    auto tfull = [&](int a) { return ptx::smem_u32(&bar_tfull[a]); };
+    auto tempty = [&](int a) { return ptx::smem_u32(&bar_tempty[a]); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(tfull(a), 1);
+            ptx::mbar_init(tempty(a), 2 * kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
+        s_abort = 0;
+        s_never = 0;
+        ptx::fence_mbar_init();
+        ptx::tma_prefetch_map(&map_w0);
+        if (MODE == GATEUP) ptx::tma_prefetch_map(&map_w1);
+        ptx::tma_prefetch_map(&map_b);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(&s_tmem_base), kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();   // both CTAs' barriers are initialised before either reports to the other
+    ptx::tc_fence_after();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = s_tmem_base;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    auto lead = [&](uint32_t bar) { return ptx::mapa_shared(bar, 0); };   // the pair's barriers live in the even CTA
+    volatile int *abort_flag = &s_abort;
+    volatile int *never = &s_never;
+    const int nst = (p.nkb + KSUB - 1) / KSUB;
+    const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+    uint32_t produced = 0;
+
+    ptx::griddep_wait();   // the plan, x, h: all written by kernels before this one
+    const int units = __ldcg(p.header) * p.nf;
+    // two accumulators where gate and up of the widest tile fit in half of tensor memory
+    const bool two = MODE == DOWN || __ldcg(p.header + 1) <= 128;
+    const uint32_t up_off = two ? 128u : 256u;
+    auto tile_a = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf)); };
+    auto tile_b = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf) + 1); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer
+        bool ok = true;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = moe::unit_of(u, p.nf, tile_a(u), tile_b(u));
+            const int half = t.n >> 1;   // this CTA's columns, a multiple of 8
+            const int wrow = t.expert * p.wrows + t.f * 256 + static_cast<int>(rank) * kBM;
+            // gate/up: the token rows of this lane's four columns (columns
+            // past the tile's last row repeat it; nobody reads them)
+            int g[4] = {0, 0, 0, 0};
+            const bool mine = MODE == GATEUP ? 4 * lane < half : 8 * lane < half;
+            if (MODE == GATEUP && mine) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    g[i] = __ldcg(p.row_token + t.row0 + min(static_cast<int>(rank) * half + 4 * lane + i, t.valid - 1));
+            }
+            const int hrow = t.row0 + static_cast<int>(rank) * half + 8 * lane;
+            for (int ks = 0; ks < nst; ++ks) {
+                const bool got = ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (leader)
+                        ptx::mbar_arrive_expect_tx(full(s), KSUB * (2 * RG::NMAT * kABytes + t.n * (kBK * 2)));
+#pragma unroll
+                    for (int j = 0; j < KSUB; ++j) {
+                        const int k0 = (ks * KSUB + j) * kBK;   // a block past K is zero fill
+                        ptx::tma_load_2d_pair(sA(s, j, 0), &map_w0, lead(full(s)), k0, wrow);
+                        if (MODE == GATEUP) ptx::tma_load_2d_pair(sA(s, j, 1), &map_w1, lead(full(s)), k0, wrow);
+                    }
+                }
+                __syncwarp();
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < KSUB; ++j) {
+                        const int k0 = (ks * KSUB + j) * kBK;
+                        if (MODE == GATEUP)
+                            gather4_pair(sB(s, j) + lane * 512, &map_b, lead(full(s)), k0, g[0], g[1], g[2], g[3]);
+                        else
+                            ptx::tma_load_2d_pair(sB(s, j) + lane * 1024, &map_b, lead(full(s)), k0, hrow);
+                    }
+                }
+                ++produced;
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // -------------------------------------------------------- MMA issuer
+        bool ok = true;
+        int s = 0, acc = 0;
+        uint32_t ph = 0, acc_ph = 0;
+        int4 na = make_int4(0, 0, 1, 0), nb = na;
+        if (u0 < units) {
+            na = tile_a(u0);
+            nb = tile_b(u0);
+        }
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = moe::unit_of(u, p.nf, na, nb);
+            if (u + ustep < units) {   // the next unit's tile, under this one's MMAs
+                na = tile_a(u + ustep);
+                nb = tile_b(u + ustep);
+            }
+            const uint32_t idesc = ptx::idesc_f16(256, t.n, BF16);
+            if (!ptx::mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, kWaitNs)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t d0 = tmem + acc * 256;
+            for (int ks = 0; ks < nst; ++ks) {
+                if (!ptx::mbar_wait(full(s), ph, abort_flag, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < KSUB; ++j) {
+                    const uint64_t bd = ptx::sdesc_k_sw128(sB(s, j));
+#pragma unroll
+                    for (int m = 0; m < RG::NMAT; ++m) {
+                        const uint64_t ad = ptx::sdesc_k_sw128(sA(s, j, m));
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)   // 32 bytes of k further: 2 in the address field
+                            ptx::tc_mma_f16_pair(d0 + m * up_off, ad + 2 * k, bd + 2 * k, idesc, (ks | j | k) != 0);
+                    }
+                }
+                ptx::tc_commit_pair(empty(s), 0x3);
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            ptx::tc_commit_pair(tfull(acc), 0x3);
+            if (!two || ++acc == 2) {
+                acc = 0;
+                acc_ph ^= 1u;
+            }
+        }
+        if (!ok) {
+            atomicOr(p.err, DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        ptx::tc_commit_pair(ptx::smem_u32(&bar_drain), 0x1);   // every MMA ends before TMEM is freed
+        ptx::mbar_wait(ptx::smem_u32(&bar_drain), 0, never, kWaitNs);
+    } else if (warp >= 2) {
+        // ---------------------------------------------------------- epilogue
+        const int q = warp & 3;                 // this warp may read TMEM lanes 32q .. 32q+31
+        const int part = (warp - 2) >> 2;       // which 16-column chunks of every 32
+        bool ok = true;
+        int acc = 0;
+        uint32_t acc_ph = 0;
+        for (int u = u0; u < units; u += ustep) {
+            const Unit t = moe::unit_of(u, p.nf, tile_a(u), tile_b(u));
+            const bool got = ptx::mbar_wait(tfull(acc), acc_ph, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const int f = t.f * 256 + static_cast<int>(rank) * kBM + q * 32 + lane;
+            const bool live = f < p.wrows;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+            const int64_t at = static_cast<int64_t>(t.row0) * p.wrows + f;
+            for (int c = part * 16; c < t.n; c += 32) {
+                if constexpr (MODE == GATEUP) {
+                    uint32_t rg[16], ru[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + c, rg);
+                    ptx::tmem_ld_32x32b_x16(taddr + up_off + c, ru);
+                    ptx::tmem_ld_wait();
+                    T *dst = static_cast<T *>(p.out) + at + static_cast<int64_t>(c) * p.wrows;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        // h feeds the next product: one rounding to its operand type
+                        const float hv = silu_f32(__uint_as_float(rg[i]) * p.acc_scale) *
+                                         (__uint_as_float(ru[i]) * p.acc_scale) * p.out_scale;
+                        if (live && c + i < t.valid) dst[static_cast<int64_t>(i) * p.wrows] = from_f32<T>(hv);
+                    }
+                } else {
+                    uint32_t r[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                    ptx::tmem_ld_wait();
+                    float *dst = static_cast<float *>(p.out) + at + static_cast<int64_t>(c) * p.wrows;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (live && c + i < t.valid)
+                            dst[static_cast<int64_t>(i) * p.wrows] = __uint_as_float(r[i]) * p.acc_scale;
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) ptx::mbar_arrive(tempty(acc));
+                else ptx::mbar_arrive_cluster(lead(tempty(acc)));
+            }
+            if (!two || ++acc == 2) {
+                acc = 0;
+                acc_ph ^= 1u;
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+
+    __syncthreads();
+    if (warp == 0 && lane == 0 && leader) {
+        // loads still in flight (only after an abandoned wait) land before shared memory is released
+        for (uint32_t s = 0; s < STAGES; ++s)
+            if (produced > s)
+                ptx::mbar_wait(full(s), ((produced - s + STAGES - 1) / STAGES - 1) & 1u, never, kWaitNs);
+    }
+    __syncthreads();
+    ptx::cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+bool map_16(CUtensorMap *m, const void *ptr, bool bf16, int64_t inner, int64_t rows, uint32_t box_rows) {
+    return encode_tma_2d(m, ptr, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner,
+                         rows, inner * 2, kBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int MODE, bool BF16>
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &b, int64_t pairs,
+                   int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, float out_scale,
+                   cudaStream_t s) {
+    using RG = Ring<MODE>;
+    const auto kern = &moe_gemm_kernel<MODE, BF16>;
+    static int configured_device = -1, slots = 0;   // co-resident CTA pairs
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = RG::SMEM_BYTES;
+    cfg.attrs = attr;
+    if (configured_device != dev) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(RG::SMEM_BYTES));
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&slots, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (slots < 1) return cudaErrorLaunchOutOfResources;
+        configured_device = dev;
+    }
+    Params p{};
+    p.header = plan.header;
+    p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
+    p.row_token = plan.row_token;
+    p.nf = static_cast<int>((wrows + 255) / 256);
+    p.wrows = static_cast<int>(wrows);
+    p.nkb = static_cast<int>((K + kBK - 1) / kBK);
+    p.out = out;
+    p.acc_scale = acc_scale;
+    p.out_scale = out_scale;
+    p.err = device_status_word();
+    if (!p.err) return cudaErrorUnknown;
+    const int64_t most = moe::max_tiles(pairs, experts, kTile) * p.nf;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(slots, most)));
+    cfg.stream = s;
+    cfg.numAttrs = 2;
+    LaunchScope scope(MODE == GATEUP ? K_MOE_GATEUP : K_MOE_DOWN, s);
+    e = cudaLaunchKernelEx(&cfg, kern, w0, w1, b, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *x, const void *wg, const void *wu, void *h,
+                              int64_t rows, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                              float out_scale, cudaStream_t s) {
+    const bool bf = op == DT_BF16;
+    CUtensorMap w0, w1, b;
+    if (!map_16(&w0, wg, bf, d, experts * ffn, kBM) || !map_16(&w1, wu, bf, d, experts * ffn, kBM) ||
+        !map_16(&b, x, bf, d, rows, 1))   // gathered rows: a box one row high
+        return cudaErrorInvalidValue;
+    return bf ? launch<GATEUP, true>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s)
+              : launch<GATEUP, false>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s);
+}
+
+cudaError_t launch_moe_down(int op, const Plan &plan, const void *h, const void *wd, float *part, int64_t pairs,
+                            int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s) {
+    const bool bf = op == DT_BF16;
+    CUtensorMap w, b;
+    if (!map_16(&w, wd, bf, ffn, experts * d, kBM) || !map_16(&b, h, bf, ffn, pairs, 8)) return cudaErrorInvalidValue;
+    return bf ? launch<DOWN, true>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s)
+              : launch<DOWN, false>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+}
+
+}  // namespace ffn

@@ -10,6 +10,7 @@ every step of the computation runs in the library's own kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 import torch
@@ -71,15 +72,27 @@ def _expect(name: str, t, shape, dtype, device):
         raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of the input")
 
 
-def _launch(fn, where: str, device: int, stream, *args):
-    """fn(*args, stream) with `device` current; the current stream by default."""
+def _launch(fn, where: str, device: int, *args):
+    """fn(*args, stream) on the current stream of `device`, with it current."""
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _launch(fn, where, device, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    status = fn(*args, s)
+            return _launch(fn, where, device, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if status != 0:
         raise FFNError(status, where)
+
+
+def _on_stream(f):
+    """Runs f under its `stream` argument, so that outputs and workspaces made
+    in the call come from that stream's memory (memory of another stream may
+    still be in use there)."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def _rows_of(x: torch.Tensor):
@@ -91,8 +104,9 @@ def _rows_of(x: torch.Tensor):
     return (x.numel() // d if d else 0), d, dev
 
 
+@_on_stream
 def ffn_add_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
-                    r_out: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+                    r_out: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """(r, n): r = x + res (x itself without `res`) and n = RMSNorm(r) * g.
 
     `r_out` may be x or res (in place); without it a new tensor takes r."""
@@ -110,15 +124,16 @@ def ffn_add_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Ten
         out = torch.empty_like(x)
     else:
         _expect("out", out, shape, dt, dev)
-    _launch(_LIB.ffn_add_rmsnorm, "ffn_add_rmsnorm", dev, stream, x.data_ptr(),
+    _launch(_LIB.ffn_add_rmsnorm, "ffn_add_rmsnorm", dev, x.data_ptr(),
             None if res is None else res.data_ptr(), g.data_ptr(), None if r_out is None else r_out.data_ptr(),
             out.data_ptr(), rows, d, eps, code)
     return (x if r_out is None else r_out), out
 
 
+@_on_stream
 def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
                          group: int = 0, r_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                         scales: torch.Tensor | None = None, stream=None):
+                         scales: torch.Tensor | None = None):
     """(r, q, scales): as ffn_add_rmsnorm with the norm's output as
     torch.float8_e4m3fn codes and fp32 scales, one per row (group 0, shape
     [rows, 1]) or per `group` columns (32, 64 or 128; [rows, ceil(d / group)]):
@@ -142,15 +157,16 @@ def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torc
         scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
     else:
         _expect("scales", scales, sshape, torch.float32, dev)
-    _launch(_LIB.ffn_add_rmsnorm_e4m3, "ffn_add_rmsnorm_e4m3", dev, stream, x.data_ptr(),
+    _launch(_LIB.ffn_add_rmsnorm_e4m3, "ffn_add_rmsnorm_e4m3", dev, x.data_ptr(),
             None if res is None else res.data_ptr(), g.data_ptr(), None if r_out is None else r_out.data_ptr(),
             out.data_ptr(), scales.data_ptr(), rows, d, group, eps, code)
     return (x if r_out is None else r_out), out, scales
 
 
+@_on_stream
 def ffn_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, groups: int = 1,
                   topk_groups: int = 1, scale: float = 1.0, flags: int = 0, idx: torch.Tensor | None = None,
-                  weights: torch.Tensor | None = None, stream=None):
+                  weights: torch.Tensor | None = None):
     """(idx int32 [rows, k], weights fp32 [rows, k]) of a [rows, experts] tensor
     of router logits; flags: FFN_ROUTE_SIGMOID, FFN_ROUTE_RENORM.  A slot
     that no eligible expert is left for has index -1 and weight 0."""
@@ -167,10 +183,58 @@ def ffn_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
     else:
         _expect("weights", weights, shape, torch.float32, dev)
-    _launch(_LIB.ffn_moe_route, "ffn_moe_route", dev, stream, logits.data_ptr(),
+    _launch(_LIB.ffn_moe_route, "ffn_moe_route", dev, logits.data_ptr(),
             None if bias is None else bias.data_ptr(), idx.data_ptr(), weights.data_ptr(), rows, experts, k, groups,
             topk_groups, scale, code, flags)
     return idx, weights
+
+
+def ffn_moe_workspace_bytes(rows: int, d: int, ffn: int, experts: int, k: int, dtype: torch.dtype,
+                            flags: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_LIB.ffn_moe_workspace_bytes(rows, d, ffn, experts, k, _DT[dtype], flags, ctypes.byref(out)),
+           "ffn_moe_workspace_bytes")
+    return out.value
+
+
+def _moe_inputs(x, idx, weights, res, out):
+    """Checks what both routed blocks take; (rows, d, k, device index)."""
+    rows, d, dev = _rows_of(x)
+    k = idx.shape[-1]
+    shape = (*x.shape[:-1], k)
+    _expect("idx", idx, shape, torch.int32, dev)
+    _expect("weights", weights, shape, torch.float32, dev)
+    if res is not None:
+        _expect("res", res, x.shape, x.dtype, dev)
+    if out is not None:
+        _expect("out", out, x.shape, x.dtype, dev)
+    return rows, d, k, dev
+
+
+@_on_stream
+def ffn_moe_forward(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor,
+                    w_up: torch.Tensor, w_down: torch.Tensor, res: torch.Tensor | None = None, flags: int = 0,
+                    out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The routed block: y = [res +] sum over a token's slots of weight * the
+    chosen expert's SwiGLU block of x.  idx, weights: ffn_moe_route's [rows, k];
+    w_gate, w_up [experts, ffn, d], w_down [experts, d, ffn] of x's type, or
+    ffn_prepare_weights output with FFN_PREPARED_WEIGHTS."""
+    rows, d, k, dev = _moe_inputs(x, idx, weights, res, out)
+    code = _dtype(x)
+    experts, ffn = w_gate.shape[0], w_gate.shape[1]
+    wt = torch.float16 if flags & FFN_PREPARED_WEIGHTS else x.dtype
+    _expect("w_gate", w_gate, (experts, ffn, d), wt, dev)
+    _expect("w_up", w_up, (experts, ffn, d), wt, dev)
+    _expect("w_down", w_down, (experts, d, ffn), wt, dev)
+    y = torch.empty_like(x) if out is None else out
+    if ws is None:   # (a passed workspace is checked against the need by the C side)
+        ws = workspace(ffn_moe_workspace_bytes(rows, d, ffn, experts, k, x.dtype, flags), x.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous CUDA tensor on the device of the input")
+    _launch(_LIB.ffn_moe_forward, "ffn_moe_forward", dev, x.data_ptr(), idx.data_ptr(), weights.data_ptr(),
+            w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), None if res is None else res.data_ptr(),
+            y.data_ptr(), rows, d, ffn, experts, k, code, flags, ws.data_ptr(), ws.numel() * ws.element_size())
+    return y
 
 
 def ffn_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, out: torch.Tensor | None = None,
