@@ -333,6 +333,26 @@ typedef struct {
 ffn_status ffn_block_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, size_t *bytes);
 
 /* ------------------------------------------------------------------------
+ * ffn_moe_forward_q4 -- ffn_moe_forward with Q4 weights: at decode each expert
+ * is a few matrix-vector products with 4-bit weights and a scale for every
+ * 32 of them, at a quarter of the 16-bit stream; prompts take the same entry.
+ *   x, res, y [rows x d] bf16; w_gate and w_up [experts x ffn] rows of d
+ *   weights, w_down [experts x d] rows of ffn weights in the device layout
+ *   above (an expert's rows follow those of the expert before).  d % 32 == 0,
+ *   ffn % 32 == 0; the other limits, the skipped slots, y = res in place and
+ *   the workspace (ffn_moe_q4_workspace_bytes) as in ffn_moe_forward.
+ *   The products run on fp16 operands: w = (u - 8) * s rounded once to fp16
+ *   (|8 s| must be finite in fp16), x rounded to fp16 (beyond its range:
+ *   FFN_ERR_RANGE in the device status word), h stored times 2^-8 (|h| below
+ *   1.6e7); accumulation in fp32.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, size_t *bytes);
+ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const float *topk_w, ffn_q4_weight w_gate,
+                              ffn_q4_weight w_up, ffn_q4_weight w_down, const void *res, void *y, int64_t rows,
+                              int64_t d, int64_t ffn, int64_t experts, int64_t k, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * ffn_block_forward_q4 -- the block with Q4 weights, dequantised in registers.
  * "Megakernels on Mac: What Fusion Saves and What It Costs", section "Threadgroup staging" (stream Q4 weights
  * to registers; staging through shared memory lost).

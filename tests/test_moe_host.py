@@ -116,3 +116,32 @@ def test_moe_forward_refusals(lib):
         assert call(y=bad) == _lib.FFN_ERR_ALIAS
     assert call(ws=wu) == _lib.FFN_ERR_ALIAS
     assert call(rows=0) == _lib.FFN_OK
+
+
+def test_moe_forward_q4_refusals(lib):
+    x, idx, w, a, b, c, res, y, ws = ptrs(9)
+    sa, sb, sc = (ctypes.c_void_p((i + 20) << 28) for i in range(3))
+
+    def q4(q, s):
+        return _lib.Q4Weight(q.value if q else None, s.value if s else None)
+
+    def need(rows=4, d=64, ffn=128, experts=8, k=2):
+        out = ctypes.c_size_t(0)
+        return lib.ffn_moe_q4_workspace_bytes(rows, d, ffn, experts, k, ctypes.byref(out)), out.value
+
+    def call(x=x, idx=idx, w=w, a=a, b=b, c=c, sa=sa, sb=sb, sc=sc, res=res, y=y, rows=4, d=64, ffn=128, experts=8,
+             k=2, ws=ws, bytes_=1 << 27):
+        return lib.ffn_moe_forward_q4(x, idx, w, q4(a, sa), q4(b, sb), q4(c, sc), res, y, rows, d, ffn, experts, k, ws,
+                                      bytes_, None)
+
+    assert need()[0] == _lib.FFN_OK and need()[1] >= 8 * (128 * 2 + 64 * 4) + 4 * 64 * 2
+    for name in ("x", "idx", "w", "a", "b", "c", "sa", "sb", "sc", "y"):
+        assert call(**{name: None}) == _lib.FFN_ERR_NULL, name
+    for bad in ({"d": 48}, {"ffn": 72}, {"rows": -1}, {"experts": 0}, {"experts": 2000}, {"k": 0}, {"k": 40},
+                {"rows": 1 << 30}):
+        assert call(**bad) == _lib.FFN_ERR_SHAPE and need(**bad)[0] == _lib.FFN_ERR_SHAPE, bad
+    assert call(bytes_=need()[1] - 1) == _lib.FFN_ERR_WORKSPACE
+    assert call(sb=ctypes.c_void_p(sb.value + 2)) == _lib.FFN_ERR_ALIGN
+    for bad in (x, c, sc, ctypes.c_void_p(res.value + 16)):
+        assert call(y=bad) == _lib.FFN_ERR_ALIAS
+    assert call(rows=0) == _lib.FFN_OK and need(rows=0) == (_lib.FFN_OK, 0)

@@ -56,6 +56,9 @@ SIGNATURES = {
     "ffn_moe_forward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                 c_int64, c_int64, c_int64, c_int64, c_int64, c_int, c_uint32, c_void_p, c_size_t,
                                 c_void_p]),
+    "ffn_moe_q4_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, c_int64, c_int64, ctypes.POINTER(c_size_t)]),
+    "ffn_moe_forward_q4": (c_int, [c_void_p, c_void_p, c_void_p, Q4Weight, Q4Weight, Q4Weight, c_void_p, c_void_p,
+                                   c_int64, c_int64, c_int64, c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
     "ffn_swiglu": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p]),
     "ffn_block_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, c_int, c_uint32,
                                           ctypes.POINTER(c_size_t)]),

@@ -426,6 +426,51 @@ ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *
     return from_cuda(e);
 }
 
+ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k,
+                                      size_t *bytes) {
+    if (!bytes) return FFN_ERR_NULL;
+    MoePlan m;
+    const ffn_status st = plan_moe(rows, d, ffn, experts, k, 32, kMoeQ4Tile, true, &m);
+    if (st != FFN_OK) return st;
+    *bytes = m.total();
+    return FFN_OK;
+}
+
+ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const float *topk_w, ffn_q4_weight w_gate,
+                              ffn_q4_weight w_up, ffn_q4_weight w_down, const void *res, void *y, int64_t rows,
+                              int64_t d, int64_t ffn, int64_t experts, int64_t k, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    if (!w_gate.qs || !w_gate.scales || !w_up.qs || !w_up.scales || !w_down.qs || !w_down.scales ||
+        (rows != 0 && (!x || !topk_idx || !topk_w || !y)))
+        return FFN_ERR_NULL;
+    MoePlan m;
+    ffn_status st = plan_moe(rows, d, ffn, experts, k, 32, kMoeQ4Tile, true, &m);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    const size_t gd = static_cast<size_t>(experts) * ffn * q4_groups(d), gf = static_cast<size_t>(experts) * d * q4_groups(ffn);
+    const Range weights[6] = {{w_gate.qs, gd * 64}, {w_up.qs, gd * 64}, {w_down.qs, gf * 64},
+                              {w_gate.scales, gd * 8}, {w_up.scales, gd * 8}, {w_down.scales, gf * 8}};
+    st = check_moe(x, topk_idx, topk_w, weights, 6, res, y, rows, d, k, m, workspace, workspace_bytes);
+    if (st != FFN_OK) return st;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, kMoeQ4Tile);
+    void *x16 = ws + m.plan, *h = ws + m.plan + m.x16;
+    float *part = reinterpret_cast<float *>(ws + m.plan + m.x16 + m.h);
+    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), kMoeQ4Tile, plan,
+                                    x, x16, d, DT_BF16, true, s);
+    // h is stored times 2^-8, which keeps it clear of fp16 overflow
+    if (e == cudaSuccess)
+        e = launch_moe_gateup_q4(plan, x16, w_gate.qs, w_gate.scales, w_up.qs, w_up.scales, h, rows, m.pairs, d, ffn,
+                                 experts, 1.f / 256.f, s);
+    if (e == cudaSuccess)
+        e = launch_moe_down_q4(plan, h, w_down.qs, w_down.scales, part, m.pairs, d, ffn, experts, 256.f, s);
+    if (e == cudaSuccess)
+        e = launch_moe_combine(plan, topk_w, part, res, y, rows, static_cast<int>(k), d, DT_BF16, s);
+    return from_cuda(e);
+}
+
 ffn_status ffn_swiglu(const void *gate, const void *up, void *h, int64_t count, ffn_dtype dtype,
                       void *stream) {
     if (count != 0 && (!gate || !up || !h)) return FFN_ERR_NULL;

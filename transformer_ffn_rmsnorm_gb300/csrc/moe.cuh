@@ -78,4 +78,14 @@ cudaError_t launch_moe_gateup(int op, const moe::Plan &plan, const void *x, cons
 cudaError_t launch_moe_down(int op, const moe::Plan &plan, const void *h, const void *wd, float *part, int64_t pairs,
                             int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s);
 
+// The products with Q4 weights (moe_gemm_q4.cu): x16 is x in fp16, columns 1
+// and 2 of every four exchanged; h is written in the same order.
+constexpr int kMoeQ4Tile = 128;
+cudaError_t launch_moe_gateup_q4(const moe::Plan &plan, const void *x16, const uint8_t *qg, const uint16_t *sg,
+                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t rows, int64_t pairs, int64_t d,
+                                 int64_t ffn, int64_t experts, float out_scale, cudaStream_t s);
+cudaError_t launch_moe_down_q4(const moe::Plan &plan, const void *h, const uint8_t *qd, const uint16_t *sd, float *part,
+                               int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                               cudaStream_t s);
+
 }  // namespace ffn

@@ -1,0 +1,576 @@
+// moe_gemm_q4.cu -- the routed block's two products with Q4 weights, on the
+// 5th-generation tensor cores with the weights dequantised into tensor memory.
+//
+//   gate/up:  h[r, f]    = silu(W_gate[e] x_t)_f * (W_up[e] x_t)_f    w = (u - 8) s
+//   down:     part[r, o] = (W_down[e] h_r)_o                          (fp32)
+//
+// A unit of work is 128 weight rows (gate/up: 64 rows of W_gate and the same
+// 64 of W_up) of one expert against one token tile of n <= 128 columns, the
+// weights on the M side as in moe_gemm.cu.  The weights travel HBM -> shared
+// memory as 4 bits (TMA, 64 bytes of a row per 128 values; their scales, whose
+// row pitch need not be a multiple of 16 bytes, by 8-byte cp.async), from
+// there through registers, where eight warps turn them into fp16, into tensor
+// memory (tcgen05.st), and tcgen05.mma takes its A operand from there.  Through
+// shared memory the fp16 form would cost 4 bytes a weight (stored and read
+// back) beside the 0.6 of the 4-bit form; so it costs none.
+//
+// What bounds it: few tokens: HBM, if the eight warps keep up -- per 128
+// values of 128 rows (9 KB, 430 cycles of this SM's share of HBM) each issues
+// about 140 instructions, two warps to a scheduler; more tokens: the
+// activations from L2 (32 KB a stage at 128 columns), then the tensor pipe.
+//
+// Arithmetic: a nibble pair becomes fp16 1024 + u (or 1024 + 16 u, the high
+// nibbles where they stand), u - 8 exactly by one subtraction (one fma), and
+// (u - 8) s by one product, rounded once to fp16 (11 bits of the at most 14;
+// exact where it is subnormal).  The nibbles of bytes 0 and 2, and 1 and 3,
+// come out as pairs, so the operands' k order within every four is 0, 2, 1, 3:
+// the plan writes x and the gate/up epilogue writes h in that order.
+//
+// Roles: warp 0 loads nibbles, warp 3 scales, warp 2 tokens; warp 1 issues the
+// MMAs; warps 4-11 dequantise (warp w fills TMEM lanes 32 (w % 4) .. and one
+// 64-value half of the stage); warps 12-15 are the epilogue.  Every wait is
+// bounded (1 s) as in gemm_tcgen05.cu.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "moe.cuh"
+
+namespace ffn {
+namespace {
+
+using moe::Plan;
+using moe::Unit;
+
+constexpr int kRows = 128, kK = 128, kTile = kMoeQ4Tile;
+constexpr uint32_t kRawBytes = kRows * 64, kScaleBytes = kRows * 8;   // a stage's nibbles and scales
+constexpr uint32_t kBBytes = kTile * kK * 2;                          // room for its tokens
+constexpr int kRawStages = 12, kBStages = 3, kAStages = 4;
+constexpr uint32_t kRawOff = kBStages * kBBytes;
+constexpr uint32_t kScaleOff = kRawOff + kRawStages * kRawBytes;
+constexpr size_t kSmemBytes = kScaleOff + kRawStages * kScaleBytes + 1024;
+static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
+              "one CTA per SM (each allocates all of tensor memory), beside 8 KB of static shared memory");
+constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
+constexpr int kDequantWarps = 8, kEpiWarps = 4;
+constexpr int kThreads = 32 * (4 + kDequantWarps + kEpiWarps);
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+enum Mode { GATEUP = 0, DOWN = 1 };
+
+struct Params {
+    const int *header;
+    const int4 *tiles;
+    const int *row_token;
+    const uint16_t *s0, *s1;   // scales of W_gate and W_up, or of W_down
+    int nf;                    // feature tiles of 64 (gate/up) or 128 rows
+    int wrows;                 // weight rows of an expert (ffn or d)
+    int ngrp;                  // 128-value groups of a row: the stages of a unit
+    void *out;
+    float acc_scale, out_scale;
+    unsigned *err;
+};
+
+__device__ __forceinline__ void gather4(uint32_t dst, const void *map, uint32_t bar, int x, int r0, int r1, int r2,
+                                        int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// arrives on bar once this thread's cp.async so far have landed (the barrier counts the arrival)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Eight nibbles (a word of the device layout) as (u - 8) s in fp16 pairs:
+// o[0], o[1] bytes 0/2 and 1/3 of the low nibbles, o[2], o[3] of the high ones.
+__device__ __forceinline__ void dequant_word(uint32_t w, __half2 s, uint32_t (&o)[4]) {
+    const __half2 lo8 = __half2half2(__ushort_as_half(0x6408));        // 1032
+    const __half2 hi_m = __half2half2(__ushort_as_half(0x2C00));       // 1/16
+    const __half2 hi_a = __half2half2(__ushort_as_half(0xD480));       // -72
+    const uint32_t v = w >> 8;
+    uint32_t r[4];
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(r[0]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(r[1]) : "r"(v));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(r[2]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(r[3]) : "r"(v));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __half2 h = *reinterpret_cast<__half2 *>(&r[i]);
+        h = i < 2 ? __hsub2(h, lo8) : __hfma2(h, hi_m, hi_a);
+        h = __hmul2(h, s);
+        o[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_gemm_q4_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+                       const __grid_constant__ CUtensorMap map_b, const Params p) {
+    constexpr int kFRows = MODE == GATEUP ? 64 : 128;   // features of a unit
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_rfull[kRawStages], bar_rempty[kRawStages];
+    __shared__ __align__(8) uint64_t bar_bfull[kBStages], bar_bempty[kBStages];
+    __shared__ __align__(8) uint64_t bar_afull[kAStages], bar_aempty[kAStages];
+    __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
+    __shared__ float s_swap[MODE == GATEUP ? 2 : 1][2][8][MODE == GATEUP ? 64 : 1];
+    __shared__ uint32_t s_tmem_base;
+    __shared__ int s_abort, s_never;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    auto bar = [](uint64_t *b) { return ptx::smem_u32(b); };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRawStages; ++s) {
+            ptx::mbar_init(bar(&bar_rfull[s]), 1 + 32);        // the nibbles' bytes, the scale warp's lanes
+            ptx::mbar_init(bar(&bar_rempty[s]), kDequantWarps);
+        }
+        for (int s = 0; s < kBStages; ++s) {
+            ptx::mbar_init(bar(&bar_bfull[s]), 1);
+            ptx::mbar_init(bar(&bar_bempty[s]), 1);
+        }
+        for (int s = 0; s < kAStages; ++s) {
+            ptx::mbar_init(bar(&bar_afull[s]), kDequantWarps);
+            ptx::mbar_init(bar(&bar_aempty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(bar(&bar_tfull[a]), 1);
+            ptx::mbar_init(bar(&bar_tempty[a]), kEpiWarps);
+        }
+        ptx::mbar_init(bar(&bar_drain), 1);
+        s_abort = 0;
+        s_never = 0;
+        ptx::fence_mbar_init();
+        ptx::tma_prefetch_map(&map_w0);
+        if (MODE == GATEUP) ptx::tma_prefetch_map(&map_w1);
+        ptx::tma_prefetch_map(&map_b);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&s_tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = s_tmem_base;
+    volatile int *abort_flag = &s_abort;
+    volatile int *never = &s_never;
+    const int u0 = blockIdx.x, ustep = gridDim.x;
+    uint32_t produced = 0;   // stages whose loads this warp issued (warps 0 and 2)
+    bool ok = true;
+
+    ptx::griddep_wait();   // the plan, x, h: written by kernels before this one
+    const int units = __ldcg(p.header) * p.nf;
+    auto unit_at = [&](int u) {
+        const int4 *t = p.tiles + 2 * (u / p.nf);
+        return moe::unit_of(u, p.nf, __ldcg(t), __ldcg(t + 1));
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------------- nibbles
+            int s = 0;
+            uint32_t ph = 0;
+            for (int u = u0; u < units && ok; u += ustep) {
+                const Unit t = unit_at(u);
+                const int wrow = t.expert * p.wrows + t.f * kFRows;
+                for (int g = 0; g < p.ngrp; ++g) {
+                    if (!ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = bar(&bar_rfull[s]), dst = base + kRawOff + s * kRawBytes;
+                    ptx::mbar_arrive_expect_tx(full, kRawBytes);
+                    ptx::tma_load_2d(dst, &map_w0, full, g * 64, wrow);
+                    if (MODE == GATEUP) ptx::tma_load_2d(dst + kRawBytes / 2, &map_w1, full, g * 64, wrow);
+                    ++produced;
+                    if (++s == kRawStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------ scales
+        int s = 0;
+        uint32_t ph = 0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = unit_at(u);
+            const uint16_t *src[4];   // of this lane's rows lane, lane + 32, ...
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int f = t.f * kFRows + (MODE == GATEUP ? 32 * (i & 1) : 32 * i) + lane;
+                const uint16_t *m = MODE == GATEUP && i >= 2 ? p.s1 : p.s0;
+                src[i] = m + (static_cast<int64_t>(t.expert) * p.wrows + min(f, p.wrows - 1)) * (4 * p.ngrp);
+            }
+            for (int g = 0; g < p.ngrp; ++g) {
+                const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = base + kScaleOff + s * kScaleBytes + lane * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cp_async8(dst + i * 256, src[i] + 4 * g);
+                cp_async_arrive(bar(&bar_rfull[s]));
+                if (++s == kRawStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 2) {
+        // ------------------------------------------------------ tokens
+        int s = 0;
+        uint32_t ph = 0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = unit_at(u);
+            int gr[4] = {0, 0, 0, 0};
+            const bool mine = MODE == GATEUP ? 4 * lane < t.n : 8 * lane < t.n;
+            if (MODE == GATEUP && mine) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gr[i] = __ldcg(p.row_token + t.row0 + min(4 * lane + i, t.valid - 1));
+            }
+            for (int g = 0; g < p.ngrp; ++g) {
+                const bool got = ptx::mbar_wait(bar(&bar_bempty[s]), ph ^ 1u, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = bar(&bar_bfull[s]);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
+                __syncwarp();
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {   // 64 values each; past the row's end zero fill
+                        const uint32_t dst = base + s * kBBytes + j * (kBBytes / 2);
+                        if (MODE == GATEUP)
+                            gather4(dst + lane * 512, &map_b, full, g * kK + j * 64, gr[0], gr[1], gr[2], gr[3]);
+                        else
+                            ptx::tma_load_2d(dst + lane * 1024, &map_b, full, g * kK + j * 64, t.row0 + 8 * lane);
+                    }
+                }
+                ++produced;
+                if (++s == kBStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // -------------------------------------------------- MMA issuer
+            int sa = 0, sb = 0, acc = 0;
+            uint32_t pa = 0, pb = 0, pacc = 0;
+            int4 na = make_int4(0, 0, 1, 0), nb = na;
+            auto fetch = [&](int u) {
+                na = __ldcg(p.tiles + 2 * (u / p.nf));
+                nb = __ldcg(p.tiles + 2 * (u / p.nf) + 1);
+            };
+            if (u0 < units) fetch(u0);
+            for (int u = u0; u < units && ok; u += ustep) {
+                const Unit t = moe::unit_of(u, p.nf, na, nb);
+                if (u + ustep < units) fetch(u + ustep);
+                const uint32_t idesc = ptx::idesc_f16(128, t.n, false);
+                if (!ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t d = tmem + acc * 128;
+                for (int g = 0; g < p.ngrp; ++g) {
+                    if (!ptx::mbar_wait(bar(&bar_bfull[sb]), pb, abort_flag, kWaitNs) ||
+                        !ptx::mbar_wait(bar(&bar_afull[sa]), pa, abort_flag, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a = tmem + kACol + sa * kAColsPerStage;
+#pragma unroll
+                    for (int k = 0; k < kK / 16; ++k) {
+                        const uint64_t bd = ptx::sdesc_k_sw128(base + sb * kBBytes + (k >> 2) * (kBBytes / 2)) + 2 * (k & 3);
+                        mma_ts(d, a + 8 * k, bd, idesc, (g | k) != 0);
+                    }
+                    ptx::tc_commit(bar(&bar_bempty[sb]));
+                    ptx::tc_commit(bar(&bar_aempty[sa]));
+                    if (++sb == kBStages) {
+                        sb = 0;
+                        pb ^= 1u;
+                    }
+                    if (++sa == kAStages) {
+                        sa = 0;
+                        pa ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                ptx::tc_commit(bar(&bar_tfull[acc]));
+                if (++acc == 2) {
+                    acc = 0;
+                    pacc ^= 1u;
+                }
+            }
+            ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
+            ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
+        }
+    } else if (warp < 4 + kDequantWarps) {
+        // ------------------------------------------------------ dequantisation
+        const int q = warp & 3, hv = (warp - 4) >> 2;   // rows 32q .. 32q + 31; values 64 hv .. 64 hv + 63
+        const int row = 32 * q + lane;
+        const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
+        int s = 0, sa = 0;
+        uint32_t ph = 0, pa = 0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            for (int g = 0; g < p.ngrp; ++g) {
+                bool got = ptx::mbar_wait(bar(&bar_rfull[s]), ph, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = base + kRawOff + s * kRawBytes + row * 64 + hv * 8;
+                uint2 w[4];   // this half's two blocks: words of canonical bytes 4t .. 4t + 3
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(w[t].x), "=r"(w[t].y)
+                                 : "r"(src + ((t ^ swz) << 4)));
+                uint32_t sc;
+                asm volatile("ld.shared.u32 %0, [%1];"
+                             : "=r"(sc)
+                             : "r"(base + kScaleOff + s * kScaleBytes + row * 8 + hv * 4));
+                uint32_t o[32];
+                const __half2 sp = *reinterpret_cast<const __half2 *>(&sc);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const __half2 s2 = b ? __high2half2(sp) : __low2half2(sp);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        uint32_t v[4];
+                        dequant_word(b ? w[t].y : w[t].x, s2, v);
+                        o[16 * b + 2 * t] = v[0];
+                        o[16 * b + 2 * t + 1] = v[1];
+                        o[16 * b + 8 + 2 * t] = v[2];
+                        o[16 * b + 8 + 2 * t + 1] = v[3];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(&bar_rempty[s]));
+                if (++s == kRawStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                got = ptx::mbar_wait(bar(&bar_aempty[sa]), pa ^ 1u, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                tmem_st_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + kACol + sa * kAColsPerStage + 32 * hv, o);
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(&bar_afull[sa]));
+                if (++sa == kAStages) {
+                    sa = 0;
+                    pa ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue
+        const int q = warp & 3;
+        int acc = 0;
+        uint32_t pacc = 0;
+        for (int u = u0; u < units; u += ustep) {
+            const Unit t = unit_at(u);
+            const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
+            // (with the exchange below the four warps stay or leave together:
+            // the vote is over all of them)
+            __syncwarp();
+            bool stay;
+            if constexpr (MODE == GATEUP) {
+                int all;
+                asm volatile(
+                    "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, 1, 128, a;\n\t"
+                    "selp.b32 %0, 1, 0, b;\n\t}"
+                    : "=r"(all)
+                    : "r"(got ? 1 : 0)
+                    : "memory");
+                stay = all != 0;
+            } else {
+                stay = __all_sync(0xffffffffu, got);
+            }
+            if (!stay) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 128;
+            if constexpr (MODE == GATEUP) {
+                // lanes 0-63 hold gate, 64-127 up of the same 64 features: of
+                // every 16 columns the gate warps take the first eight and
+                // the up warps the others, and hand over what the other side needs
+                const int fl = 32 * (q & 1) + lane, mat = q >> 1;
+                const int f = t.f * kFRows + fl;
+                const int fp = (f & ~3) | ((f & 1) << 1) | ((f >> 1) & 1);   // its place in h
+                const bool live = f < p.wrows;
+                __half *dst = static_cast<__half *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + fp;
+                for (int c = 0, pp = 0; c < t.n; c += 16, pp ^= 1) {
+                    uint32_t r[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s_swap[pp][mat][i][fl] = __uint_as_float(mat ? r[i] : r[8 + i]);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float other = s_swap[pp][mat ^ 1][i][fl];
+                        const float mine = __uint_as_float(mat ? r[8 + i] : r[i]);
+                        const float gate = mat ? other : mine, up = mat ? mine : other;
+                        const float hv = silu_f32(gate * p.acc_scale) * (up * p.acc_scale) * p.out_scale;
+                        const int col = c + 8 * mat + i;
+                        // h feeds the next product: one rounding to fp16
+                        if (live && col < t.valid) dst[static_cast<int64_t>(col) * p.wrows] = __float2half_rn(hv);
+                    }
+                }
+            } else {
+                const int f = t.f * kFRows + 32 * q + lane;
+                const bool live = f < p.wrows;
+                float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + f;
+                for (int c = 0; c < t.n; c += 16) {
+                    uint32_t r[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (live && c + i < t.valid)
+                            dst[static_cast<int64_t>(c + i) * p.wrows] = __uint_as_float(r[i]) * p.acc_scale;
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(&bar_tempty[acc]));
+            if (++acc == 2) {
+                acc = 0;
+                pacc ^= 1u;
+            }
+        }
+    }
+    if (!ok && (lane == 0 || warp >= 2)) {
+        if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    }
+
+    __syncthreads();
+    // loads still in flight (only after an abandoned wait) land before shared memory is released
+    if (warp == 0 && lane == 0)
+        for (uint32_t s = 0; s < kRawStages; ++s)
+            if (produced > s)
+                ptx::mbar_wait(bar(&bar_rfull[s]), ((produced - s + kRawStages - 1) / kRawStages - 1) & 1u, never,
+                               kWaitNs);
+    if (warp == 2 && lane == 0)
+        for (uint32_t s = 0; s < kBStages; ++s)
+            if (produced > s)
+                ptx::mbar_wait(bar(&bar_bfull[s]), ((produced - s + kBStages - 1) / kBStages - 1) & 1u, never, kWaitNs);
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int MODE>
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &b,
+                   const uint16_t *s0, const uint16_t *s1, int64_t pairs, int64_t experts, int64_t wrows, int64_t K,
+                   void *out, float acc_scale, float out_scale, cudaStream_t s) {
+    const auto kern = &moe_gemm_q4_kernel<MODE>;
+    static int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (configured_device != dev) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    constexpr int kFRows = MODE == GATEUP ? 64 : 128;
+    Params p{};
+    p.header = plan.header;
+    p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
+    p.row_token = plan.row_token;
+    p.s0 = s0;
+    p.s1 = s1;
+    p.nf = static_cast<int>((wrows + kFRows - 1) / kFRows);
+    p.wrows = static_cast<int>(wrows);
+    p.ngrp = static_cast<int>((K + kK - 1) / kK);
+    p.out = out;
+    p.acc_scale = acc_scale;
+    p.out_scale = out_scale;
+    p.err = device_status_word();
+    if (!p.err) return cudaErrorUnknown;
+    const int64_t grid = std::min<int64_t>(sm_count(), moe::max_tiles(pairs, experts, kTile) * p.nf);
+    LaunchScope scope(MODE == GATEUP ? K_MOE_GATEUP : K_MOE_DOWN, s);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, w0, w1, b, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// nibbles: 64 bytes of box_rows rows, rows of whole 128-value groups
+bool map_q4(CUtensorMap *m, const uint8_t *qs, int64_t K, int64_t rows, uint32_t box_rows) {
+    const int64_t pitch = 64 * ((K + kK - 1) / kK);
+    return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 64, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool map_f16(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows) {
+    return encode_tma_2d(m, ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner, rows, inner * 2, 64, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gateup_q4(const Plan &plan, const void *x16, const uint8_t *qg, const uint16_t *sg,
+                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t rows, int64_t pairs, int64_t d,
+                                 int64_t ffn, int64_t experts, float out_scale, cudaStream_t s) {
+    CUtensorMap w0, w1, b;
+    if (!map_q4(&w0, qg, d, experts * ffn, 64) || !map_q4(&w1, qu, d, experts * ffn, 64) ||
+        !map_f16(&b, x16, d, rows, 1))
+        return cudaErrorInvalidValue;
+    return launch<GATEUP>(plan, w0, w1, b, sg, su, pairs, experts, ffn, d, h, 1.f, out_scale, s);
+}
+
+cudaError_t launch_moe_down_q4(const Plan &plan, const void *h, const uint8_t *qd, const uint16_t *sd, float *part,
+                               int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                               cudaStream_t s) {
+    CUtensorMap w, b;
+    if (!map_q4(&w, qd, ffn, experts * d, 128) || !map_f16(&b, h, ffn, pairs, 8)) return cudaErrorInvalidValue;
+    return launch<DOWN>(plan, w, w, b, sd, sd, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+}
+
+}  // namespace ffn

@@ -237,6 +237,47 @@ def ffn_moe_forward(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w
     return y
 
 
+def ffn_moe_q4_workspace_bytes(rows: int, d: int, ffn: int, experts: int, k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_LIB.ffn_moe_q4_workspace_bytes(rows, d, ffn, experts, k, ctypes.byref(out)), "ffn_moe_q4_workspace_bytes")
+    return out.value
+
+
+def _moe_q4_weight(name, w, experts, out, inn, dev):
+    qs, sc = w
+    groups = -(-inn // 128)
+    _expect(name + " qs", qs, (experts, out, 64 * groups), torch.uint8, dev)
+    if sc.element_size() != 2:
+        raise TypeError(f"{name} scales must be fp16 or their 16-bit patterns")
+    _expect(name + " scales", sc, (experts, out, 4 * groups), sc.dtype, dev)
+    return Q4Weight(qs.data_ptr(), sc.data_ptr())
+
+
+@_on_stream
+def ffn_moe_forward_q4(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_gate, w_up, w_down, ffn: int,
+                       res: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None) -> torch.Tensor:
+    """ffn_moe_forward (bf16) with Q4 weights: ``w_*`` are (qs uint8 [experts,
+    rows, 64 ceil(in/128)], scales [experts, rows, 4 ceil(in/128)] fp16 or
+    their bits) pairs in the device layout of include/ffn.h."""
+    rows, d, k, dev = _moe_inputs(x, idx, weights, res, out)
+    if x.dtype is not torch.bfloat16:
+        raise TypeError("x must be torch.bfloat16")
+    experts = w_gate[0].shape[0]
+    wg = _moe_q4_weight("w_gate", w_gate, experts, ffn, d, dev)
+    wu = _moe_q4_weight("w_up", w_up, experts, ffn, d, dev)
+    wd = _moe_q4_weight("w_down", w_down, experts, d, ffn, dev)
+    y = torch.empty_like(x) if out is None else out
+    if ws is None:
+        ws = workspace(ffn_moe_q4_workspace_bytes(rows, d, ffn, experts, k), x.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous CUDA tensor on the device of the input")
+    _launch(_LIB.ffn_moe_forward_q4, "ffn_moe_forward_q4", dev, x.data_ptr(), idx.data_ptr(), weights.data_ptr(),
+            wg, wu, wd, None if res is None else res.data_ptr(), y.data_ptr(), rows, d, ffn, experts, k,
+            ws.data_ptr(), ws.numel() * ws.element_size())
+    return y
+
+
 def ffn_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     _need_cuda(x, g, out)
