@@ -106,7 +106,7 @@ def test_shapes(env, rows, d, f, experts, k, dtype, prepared):
     run(env, args, residual=rows % 2 == 1, prepared=prepared)
 
 
-@pytest.mark.parametrize("rows", [31, 32, 33, 127, 128, 129, 255, 256, 257, 300, 513, 1025])
+@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 64, 65, 80, 127, 128, 129, 255, 256, 257, 300, 513, 1025])
 def test_tile_edges(env, rows):
     """Every token to expert 1 and every third one to expert 3 as well: token
     tiles that end at, before and after their limits; two experts unused."""

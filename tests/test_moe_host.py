@@ -96,7 +96,7 @@ def test_moe_forward_refusals(lib):
                                    None)
 
     assert need()[0] == _lib.FFN_OK and need()[1] >= 8 * (128 * 2 + 64 * 4)
-    assert need(flags=_lib.FFN_PREPARED_WEIGHTS)[1] > need()[1]
+    assert need(flags=_lib.FFN_PREPARED_WEIGHTS)[1] >= need()[1]
     assert need(rows=0) == (_lib.FFN_OK, 0)
     for name in ("x", "idx", "w", "wg", "wu", "wd", "y"):
         assert call(**{name: None}) == _lib.FFN_ERR_NULL, name

@@ -325,26 +325,35 @@ namespace {
 // what the routed block's entries share: sizes, and the workspace's parts
 struct MoePlan {
     int64_t pairs;
-    size_t plan, x16, h, part;   // bytes, in this order
-    size_t total() const { return plan + x16 + h + part; }
+    moe::Cut cut;
+    int splits;                  // of the down product's reduction
+    size_t plan, xs, h, part;    // bytes, in this order
+    size_t total() const { return plan + xs + h + part; }
 };
 
-ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, int64_t step, int tile,
-                    bool x16, MoePlan *m) {
+// Rows an expert has on average (of those in use, at most) up to which 16-bit
+// weights stream through single CTAs.
+constexpr int64_t kMoeStreamRows = 32;
+
+ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, bool q4, MoePlan *m) {
     if (rows < 0 || d < 1 || ffn < 1 || experts < 1 || experts > moe::kMaxExperts || k < 1 || k > 32)
         return FFN_ERR_SHAPE;
+    const int64_t step = q4 ? 32 : 8;
     if (d % step || ffn % step) return FFN_ERR_SHAPE;
     // sorted rows, weight rows and units of work are 32-bit
     const int64_t most = int64_t{1} << 30;
     if (rows > most || d > most || ffn > most || rows * k > most) return FFN_ERR_SHAPE;
     if (experts * d > most || experts * ffn > most) return FFN_ERR_SHAPE;
     m->pairs = rows * k;
-    if (moe::max_tiles(m->pairs, experts, tile) * ((std::max(d, ffn) + 127) / 128) > most) return FFN_ERR_SHAPE;
+    const bool stream = !q4 && m->pairs <= kMoeStreamRows * std::min(m->pairs, experts);
+    m->cut = q4 ? kMoeCutQ4 : stream ? kMoeCutStream : kMoeCutPair;
+    m->splits = q4 || stream ? moe_down_splits(m->pairs, experts, d, ffn) : 1;
+    if (moe::max_tiles(m->pairs, experts, m->cut.tile) * ((std::max(d, ffn) + 63) / 64) > most / 8) return FFN_ERR_SHAPE;
     const size_t p = static_cast<size_t>(m->pairs);
-    m->plan = rows ? moe_plan_bytes(m->pairs, experts, tile) : 0;
-    m->x16 = x16 ? align256(static_cast<size_t>(rows) * d * 2) : 0;
+    m->plan = rows ? moe_plan_bytes(m->pairs, experts, m->cut.tile) : 0;
+    m->xs = align256(p * d * 2);
     m->h = align256(p * ffn * 2);
-    m->part = align256(p * d * 4);
+    m->part = align256(p * d * 4 * m->splits);
     return FFN_OK;
 }
 
@@ -373,7 +382,7 @@ ffn_status plan_moe16(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int
                       uint32_t flags, MoePlan *m) {
     if (dtype != FFN_F16 && dtype != FFN_BF16) return FFN_ERR_DTYPE;
     if (flags & ~FFN_PREPARED_WEIGHTS) return FFN_ERR_FLAGS;
-    return plan_moe(rows, d, ffn, experts, k, 8, kMoeTile, (flags & FFN_PREPARED_WEIGHTS) && dtype == FFN_BF16, m);
+    return plan_moe(rows, d, ffn, experts, k, false, m);
 }
 
 }  // namespace
@@ -406,23 +415,30 @@ ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, kMoeTile);
-    void *x16 = m.x16 ? ws + m.plan : nullptr;
-    void *h = ws + m.plan + m.x16;
-    float *part = reinterpret_cast<float *>(ws + m.plan + m.x16 + m.h);
+    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, m.cut.tile);
+    void *xs = ws + m.plan, *h = ws + m.plan + m.xs;
+    float *part = reinterpret_cast<float *>(ws + m.plan + m.xs + m.h);
     // prepared weights: fp16 operands; the weights' 2^8 is undone on G and U,
     // h is stored times 2^-8 and the two cancel in the down product
     const bool prepared = (flags & FFN_PREPARED_WEIGHTS) != 0;
     const int op = prepared ? static_cast<int>(DT_F16) : static_cast<int>(dtype);
     const float w_unscale = prepared ? 1.f / kPreparedScale : 1.f, h_scale = prepared ? 1.f / 256.f : 1.f;
-    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), kMoeTile, plan, x,
-                                    x16, d, dtype, false, s);
+    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), m.cut, plan, x, xs,
+                                    d, dtype, op != static_cast<int>(dtype), false, s);
+    if (m.cut.tile == kMoeCutStream.tile) {
+        if (e == cudaSuccess)
+            e = launch_moe_gateup_stream(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale, s);
+        if (e == cudaSuccess)
+            e = launch_moe_down_stream(op, plan, h, w_down, part, m.splits, m.pairs, d, ffn, experts,
+                                       w_unscale / h_scale, s);
+    } else {
+        if (e == cudaSuccess)
+            e = launch_moe_gateup(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale, s);
+        if (e == cudaSuccess)
+            e = launch_moe_down(op, plan, h, w_down, part, m.pairs, d, ffn, experts, w_unscale / h_scale, s);
+    }
     if (e == cudaSuccess)
-        e = launch_moe_gateup(op, plan, x16 ? x16 : x, w_gate, w_up, h, rows, m.pairs, d, ffn, experts, w_unscale,
-                              h_scale, s);
-    if (e == cudaSuccess)
-        e = launch_moe_down(op, plan, h, w_down, part, m.pairs, d, ffn, experts, w_unscale / h_scale, s);
-    if (e == cudaSuccess) e = launch_moe_combine(plan, topk_w, part, res, y, rows, static_cast<int>(k), d, dtype, s);
+        e = launch_moe_combine(plan, topk_w, part, m.splits, res, y, rows, static_cast<int>(k), d, dtype, s);
     return from_cuda(e);
 }
 
@@ -430,7 +446,7 @@ ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int6
                                       size_t *bytes) {
     if (!bytes) return FFN_ERR_NULL;
     MoePlan m;
-    const ffn_status st = plan_moe(rows, d, ffn, experts, k, 32, kMoeQ4Tile, true, &m);
+    const ffn_status st = plan_moe(rows, d, ffn, experts, k, true, &m);
     if (st != FFN_OK) return st;
     *bytes = m.total();
     return FFN_OK;
@@ -444,7 +460,7 @@ ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const floa
         (rows != 0 && (!x || !topk_idx || !topk_w || !y)))
         return FFN_ERR_NULL;
     MoePlan m;
-    ffn_status st = plan_moe(rows, d, ffn, experts, k, 32, kMoeQ4Tile, true, &m);
+    ffn_status st = plan_moe(rows, d, ffn, experts, k, true, &m);
     if (st != FFN_OK) return st;
     if (rows == 0) return FFN_OK;
     const size_t gd = static_cast<size_t>(experts) * ffn * q4_groups(d), gf = static_cast<size_t>(experts) * d * q4_groups(ffn);
@@ -455,19 +471,19 @@ ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const floa
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, kMoeQ4Tile);
-    void *x16 = ws + m.plan, *h = ws + m.plan + m.x16;
-    float *part = reinterpret_cast<float *>(ws + m.plan + m.x16 + m.h);
-    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), kMoeQ4Tile, plan,
-                                    x, x16, d, DT_BF16, true, s);
+    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, m.cut.tile);
+    void *xs = ws + m.plan, *h = ws + m.plan + m.xs;
+    float *part = reinterpret_cast<float *>(ws + m.plan + m.xs + m.h);
+    cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), m.cut, plan, x, xs,
+                                    d, DT_BF16, true, true, s);
     // h is stored times 2^-8, which keeps it clear of fp16 overflow
     if (e == cudaSuccess)
-        e = launch_moe_gateup_q4(plan, x16, w_gate.qs, w_gate.scales, w_up.qs, w_up.scales, h, rows, m.pairs, d, ffn,
-                                 experts, 1.f / 256.f, s);
+        e = launch_moe_gateup_q4(plan, xs, w_gate.qs, w_gate.scales, w_up.qs, w_up.scales, h, m.pairs, d, ffn, experts,
+                                 1.f / 256.f, s);
     if (e == cudaSuccess)
-        e = launch_moe_down_q4(plan, h, w_down.qs, w_down.scales, part, m.pairs, d, ffn, experts, 256.f, s);
+        e = launch_moe_down_q4(plan, h, w_down.qs, w_down.scales, part, m.splits, m.pairs, d, ffn, experts, 256.f, s);
     if (e == cudaSuccess)
-        e = launch_moe_combine(plan, topk_w, part, res, y, rows, static_cast<int>(k), d, DT_BF16, s);
+        e = launch_moe_combine(plan, topk_w, part, m.splits, res, y, rows, static_cast<int>(k), d, DT_BF16, s);
     return from_cuda(e);
 }
 

@@ -2,15 +2,16 @@
 //
 //   y_t = [res_t +] sum_j w_tj * W_down[e] ( silu(W_gate[e] x_t) * (W_up[e] x_t) ),  e = idx_tj
 //
-// One call is four kernels: the plan sorts the (token, slot) pairs by expert;
-// the gate/up and the down product run over the experts' tiles; the last one
-// adds each token's weighted results in slot order.
+// One call: the plan sorts the (token, slot) pairs by expert and copies their
+// rows of x in that order; the gate/up and the down product run over the
+// experts' tiles; the last kernel adds each token's weighted results in slot
+// order.
 //
 // The products put the WEIGHT rows on the M side of the tensor-core
 // instruction and an expert's tokens on its N side.  N may be any multiple of
-// 32, so an expert with c tokens wastes fewer than 32 columns where tokens on
-// the M side would waste up to a whole 256-row tile, and the same kernel runs
-// from one token (a stream of weights) to long prompts.
+// 32 (16 without CTA pairs), so an expert with c tokens wastes fewer than 32
+// columns where tokens on the M side would waste up to a whole 256-row tile,
+// and the same scheme runs from one token (a stream of weights) to long prompts.
 #pragma once
 
 #include "ffn_internal.cuh"
@@ -27,10 +28,16 @@ struct Tile {
 };
 
 struct Plan {
-    int *header;       // [0] token tiles, [1] columns of the widest tile
+    int *header;       // [0] token tiles, [1] columns of the widest tile, [2] sorted rows
     Tile *tiles;
     int *row_token;    // token of each sorted row
     int *pos;          // sorted row of pair (token, slot), or -1 (no expert)
+};
+
+// How a product cuts its work: token tiles of at most `tile` columns, ending
+// on multiples of `gran`.
+struct Cut {
+    int tile, gran;
 };
 
 constexpr int kMaxExperts = 1024;
@@ -45,6 +52,7 @@ __host__ __device__ constexpr int64_t max_tiles(int64_t pairs, int64_t experts, 
 struct Unit {
     int expert, f, row0, valid, n;
 };
+template <int GRAN>
 __device__ __forceinline__ Unit unit_of(int u, int nf, const int4 &a, const int4 &b) {
     Unit r;
     const int local = u - a.y * nf;
@@ -53,39 +61,133 @@ __device__ __forceinline__ Unit unit_of(int u, int nf, const int4 &a, const int4
     const int tt = local - r.f * a.z;
     r.row0 = b.x + tt * a.w;
     r.valid = min(a.w, b.y - tt * a.w);
-    r.n = (r.valid + 31) & ~31;
+    r.n = (r.valid + GRAN - 1) & ~(GRAN - 1);
     return r;
+}
+
+// The sorted rows a tile reads, loaded in boxes of 128, 64, 32 and 16 rows
+// (a copy engine's request costs about 80 cycles whatever its size, so few
+// large ones: boxes of eight rows, or four gathered rows a request, had the
+// products wait 2400 to 2800 cycles for a stage whose MMAs take 1024).
+struct RowMaps {
+    CUtensorMap m[4];
+};
+// This lane's box for `rows` rows (a multiple of 16, at most 128): its first
+// row, or -1 if it has none; lanes 0 .. 3 take the boxes of 128 >> lane rows.
+__device__ __forceinline__ int row_box(int rows, int lane) {
+    const int size = 128 >> lane;
+    return lane < 4 && (rows & size) ? (rows & ~(2 * size - 1)) : -1;
+}
+
+// ---- epilogues of the single-CTA products (four warps, q = warp % 4, lane:
+// weight row 32 q + lane of the unit; columns are the tile's rows)
+
+constexpr int kSwapFloats = 2 * 2 * 8 * 64;   // shared memory of swiglu_epilogue
+
+// Lanes 0-63 of the accumulator hold gate, 64-127 up of the same 64 features.
+// Of every 16 columns the gate warps finish the first eight and the up warps
+// the others; each side hands over what the other needs.  PERM: h's columns 1
+// and 2 of every four exchanged.  h feeds the next product: one rounding to
+// its operand type.
+template <typename T, bool PERM>
+__device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane, const Unit &t, int wrows, T *h,
+                                                float (*swap)[2][8][64], float acc_scale, float out_scale) {
+    const int fl = 32 * (q & 1) + lane, mat = q >> 1;
+    const int f = t.f * 64 + fl;
+    const int at = PERM ? (f & ~3) | ((f & 1) << 1) | ((f >> 1) & 1) : f;
+    const bool live = f < wrows;
+    T *dst = h + static_cast<int64_t>(t.row0) * wrows + at;
+    for (int c = 0, pp = 0; c < t.n; c += 16, pp ^= 1) {
+        uint32_t r[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c, r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) swap[pp][mat][i][fl] = __uint_as_float(mat ? r[i] : r[8 + i]);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float other = swap[pp][mat ^ 1][i][fl];
+            const float mine = __uint_as_float(mat ? r[8 + i] : r[i]);
+            const float hv = silu_f32((mat ? other : mine) * acc_scale) * ((mat ? mine : other) * acc_scale) * out_scale;
+            const int col = c + 8 * mat + i;
+            if (live && col < t.valid) dst[static_cast<int64_t>(col) * wrows] = from_f32<T>(hv);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_epilogue(uint32_t taddr, int q, int lane, const Unit &t, int wrows, float *part,
+                                               float acc_scale) {
+    const int f = t.f * 128 + 32 * q + lane;
+    float *dst = part + static_cast<int64_t>(t.row0) * wrows + f;
+    for (int c = 0; c < t.n; c += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld_32x32b_x16(taddr + c, r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (f < wrows && c + i < t.valid) dst[static_cast<int64_t>(c + i) * wrows] = __uint_as_float(r[i]) * acc_scale;
+    }
+}
+
+// Whether all four epilogue warps passed their wait (they leave together).
+__device__ __forceinline__ bool epilogue_vote(bool got) {
+    int all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, 1, 128, a;\n\t"
+        "selp.b32 %0, 1, 0, b;\n\t}"
+        : "=r"(all)
+        : "r"(got ? 1 : 0)
+        : "memory");
+    return all != 0;
 }
 
 }  // namespace moe
 
 size_t moe_plan_bytes(int64_t pairs, int64_t experts, int tile);
 moe::Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile);
-// Sorts the pairs of idx [rows x k] into token tiles of at most `tile`
-// columns (a multiple of 32) and, with x16, writes x (bf16 or fp16, type dt)
-// as fp16 there; perm: columns 1 and 2 of every four exchanged.
-cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts, int tile, const moe::Plan &plan,
-                            const void *x, void *x16, int64_t d, int dt, bool perm, cudaStream_t s);
-// y = [res +] sum over slots of w * part[pos]; part fp32 [pairs x d].
-cudaError_t launch_moe_combine(const moe::Plan &plan, const float *w, const float *part, const void *res, void *y,
-                               int64_t rows, int k, int64_t d, int dt, cudaStream_t s);
+// Sorts the pairs of idx [rows x k] into token tiles and writes their rows of
+// x [rows x d] (type dt) in sorted order to xs [pairs x d]: as they are, or as
+// fp16 (to_f16), there with columns 1 and 2 of every four exchanged (perm).
+cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts, moe::Cut cut, const moe::Plan &plan,
+                            const void *x, void *xs, int64_t d, int dt, bool to_f16, bool perm, cudaStream_t s);
+// y = [res +] sum over slots of w * (sum over splits of part[split][pos]);
+// part fp32 [splits x pairs x d].
+cudaError_t launch_moe_combine(const moe::Plan &plan, const float *w, const float *part, int splits, const void *res,
+                               void *y, int64_t rows, int k, int64_t d, int dt, cudaStream_t s);
 
-// The products with 16-bit weights (moe_gemm.cu); op: the operands' type.
-constexpr int kMoeTile = 256;
-cudaError_t launch_moe_gateup(int op, const moe::Plan &plan, const void *x, const void *wg, const void *wu, void *h,
-                              int64_t rows, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
-                              float out_scale, cudaStream_t s);
+// 16-bit weights (op: the operands' type), many tokens: CTA pairs (moe_gemm.cu).
+constexpr moe::Cut kMoeCutPair = {256, 32};
+cudaError_t launch_moe_gateup(int op, const moe::Plan &plan, const void *xs, const void *wg, const void *wu, void *h,
+                              int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale, float out_scale,
+                              cudaStream_t s);
 cudaError_t launch_moe_down(int op, const moe::Plan &plan, const void *h, const void *wd, float *part, int64_t pairs,
                             int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s);
 
-// The products with Q4 weights (moe_gemm_q4.cu): x16 is x in fp16, columns 1
-// and 2 of every four exchanged; h is written in the same order.
-constexpr int kMoeQ4Tile = 128;
-cudaError_t launch_moe_gateup_q4(const moe::Plan &plan, const void *x16, const uint8_t *qg, const uint16_t *sg,
-                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t rows, int64_t pairs, int64_t d,
-                                 int64_t ffn, int64_t experts, float out_scale, cudaStream_t s);
+// 16-bit weights, few tokens: single CTAs streaming weights (moe_stream.cu).
+constexpr moe::Cut kMoeCutStream = {64, 16};
+cudaError_t launch_moe_gateup_stream(int op, const moe::Plan &plan, const void *xs, const void *wg, const void *wu,
+                                     void *h, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                                     float out_scale, cudaStream_t s);
+cudaError_t launch_moe_down_stream(int op, const moe::Plan &plan, const void *h, const void *wd, float *part,
+                                   int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts,
+                                   float acc_scale, cudaStream_t s);
+
+// Q4 weights (moe_gemm_q4.cu): xs is fp16 with perm; h is written in the same order.
+constexpr moe::Cut kMoeCutQ4 = {128, 16};
+cudaError_t launch_moe_gateup_q4(const moe::Plan &plan, const void *xs, const uint8_t *qg, const uint16_t *sg,
+                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t pairs, int64_t d, int64_t ffn,
+                                 int64_t experts, float out_scale, cudaStream_t s);
 cudaError_t launch_moe_down_q4(const moe::Plan &plan, const void *h, const uint8_t *qd, const uint16_t *sd, float *part,
-                               int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                               int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
                                cudaStream_t s);
+
+// Splits of the down product's reduction on the single-CTA kernels (units of
+// 128 weight rows, stages of 128 values): with few experts in use the units
+// rarely fill whole waves of multiprocessors, and shorter ones waste less of
+// the last wave.  A function of the sizes alone, so that the workspace query
+// and the call agree: the fewest splits within 2 % of the least waves / splits,
+// at most 8 and none shorter than 4 stages.
+int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn);
 
 }  // namespace ffn

@@ -6,14 +6,11 @@
 //
 // CTA pairs (tcgen05 .cta_group::2): a unit of work is 256 weight rows (128
 // in each CTA) against one token tile of n <= 256 columns of one expert.  The
-// weights are the M operand, loaded by TMA as 128 x 64 boxes; the tokens are
-// the N operand, each CTA holding half of the columns.  The gate/up product
-// gathers the tokens' rows of x straight into shared memory (tile::gather4
-// TMA loads of four rows, one per lane), so no sorted copy of x is made; the down
-// product reads the sorted rows of h in boxes of eight.
+// weights are the M operand, loaded by TMA as 128 x 64 boxes; the tokens'
+// sorted rows (of x or of h) are the N operand, each CTA holding half of the
+// columns in boxes of 128, 64, 32 and 16 rows.
 //
-// What bounds it: with few tokens the stream of weights (the ring keeps
-// 130-190 KB of loads in flight per SM); with many the tensor pipe.  Why the
+// What bounds it: the tensor pipe.  Why the
 // tile is 256 x 256: per 64 k values a CTA takes 32 KB of gate and up rows and 16 KB of
 // tokens for 1024 cycles of MMAs, 48 bytes a cycle from L2; with 128 columns
 // it would be 80.  The price is tensor memory: gate and up together fill its
@@ -21,7 +18,7 @@
 // tile's MMAs.  Where every tile of the call is at most 128 wide (plan.header[1]) there are two accumulators
 // and it does; the down product always has two.
 //
-// Roles: warp 0 loads (all lanes: one gather or box each), warp 1 issues the
+// Roles: warp 0 loads (lane 0 weights, lanes 0-3 a box of tokens each), warp 1 issues the
 // MMAs (one thread of the even CTA), warps 2-9 read the accumulators (lane =
 // weight row, column = token): for a fixed column a warp's 32 lanes store 32
 // neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
@@ -38,7 +35,7 @@ namespace {
 using moe::Plan;
 using moe::Unit;
 
-constexpr int kBM = 128, kBK = 64, kTile = kMoeTile;
+constexpr int kBM = 128, kBK = 64, kTile = kMoeCutPair.tile;
 constexpr uint32_t kABytes = kBM * kBK * 2;                // one CTA's weight rows of a k block
 constexpr uint32_t kBBytes = (kTile / 2) * kBK * 2;        // room for its half of the tokens
 constexpr uint32_t kTmemCols = 512;
@@ -63,7 +60,6 @@ template <int MODE> struct Ring {
 struct Params {
     const int *header;
     const int4 *tiles;
-    const int *row_token;
     int nf;            // feature tiles of 256 rows
     int wrows;         // weight rows of an expert (ffn or d)
     int nkb;           // 64-wide k blocks
@@ -72,19 +68,10 @@ struct Params {
     unsigned *err;
 };
 
-__device__ __forceinline__ void gather4_pair(uint32_t dst, const void *map, uint32_t bar, int x, int r0, int r1, int r2,
-                                             int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
-}
-
 template <int MODE, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
-                    const __grid_constant__ CUtensorMap map_b, const Params p) {
+                    const __grid_constant__ moe::RowMaps maps_b, const Params p) {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     using RG = Ring<MODE>;
     constexpr int STAGES = RG::STAGES, KSUB = RG::KSUB;
@@ -118,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_mbar_init();
         ptx::tma_prefetch_map(&map_w0);
         if (MODE == GATEUP) ptx::tma_prefetch_map(&map_w1);
-        ptx::tma_prefetch_map(&map_b);
+        for (int i = 0; i < 4; ++i) ptx::tma_prefetch_map(&maps_b.m[i]);
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(ptx::smem_u32(&s_tmem_base), kTmemCols);
@@ -153,19 +140,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of(u, p.nf, tile_a(u), tile_b(u));
-            const int half = t.n >> 1;   // this CTA's columns, a multiple of 8
+            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
+            const int half = t.n >> 1;   // this CTA's columns, a multiple of 16
             const int wrow = t.expert * p.wrows + t.f * 256 + static_cast<int>(rank) * kBM;
-            // gate/up: the token rows of this lane's four columns (columns
-            // past the tile's last row repeat it; nobody reads them)
-            int g[4] = {0, 0, 0, 0};
-            const bool mine = MODE == GATEUP ? 4 * lane < half : 8 * lane < half;
-            if (MODE == GATEUP && mine) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    g[i] = __ldcg(p.row_token + t.row0 + min(static_cast<int>(rank) * half + 4 * lane + i, t.valid - 1));
-            }
-            const int hrow = t.row0 + static_cast<int>(rank) * half + 8 * lane;
+            const int box = moe::row_box(half, lane);
+            const int brow = t.row0 + static_cast<int>(rank) * half + box;
             for (int ks = 0; ks < nst; ++ks) {
                 const bool got = ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -183,15 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (mine) {
+                if (box >= 0) {
 #pragma unroll
-                    for (int j = 0; j < KSUB; ++j) {
-                        const int k0 = (ks * KSUB + j) * kBK;
-                        if (MODE == GATEUP)
-                            gather4_pair(sB(s, j) + lane * 512, &map_b, lead(full(s)), k0, g[0], g[1], g[2], g[3]);
-                        else
-                            ptx::tma_load_2d_pair(sB(s, j) + lane * 1024, &map_b, lead(full(s)), k0, hrow);
-                    }
+                    for (int j = 0; j < KSUB; ++j)
+                        ptx::tma_load_2d_pair(sB(s, j) + box * 128, &maps_b.m[lane], lead(full(s)),
+                                              (ks * KSUB + j) * kBK, brow);
                 }
                 ++produced;
                 if (++s == STAGES) {
@@ -215,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             nb = tile_b(u0);
         }
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of(u, p.nf, na, nb);
+            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, na, nb);
             if (u + ustep < units) {   // the next unit's tile, under this one's MMAs
                 na = tile_a(u + ustep);
                 nb = tile_b(u + ustep);
@@ -271,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t acc_ph = 0;
         for (int u = u0; u < units; u += ustep) {
-            const Unit t = moe::unit_of(u, p.nf, tile_a(u), tile_b(u));
+            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
             const bool got = ptx::mbar_wait(tfull(acc), acc_ph, abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
@@ -346,7 +321,7 @@ bool map_16(CUtensorMap *m, const void *ptr, bool bf16, int64_t inner, int64_t r
 }
 
 template <int MODE, bool BF16>
-cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &b, int64_t pairs,
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const moe::RowMaps &b, int64_t pairs,
                    int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, float out_scale,
                    cudaStream_t s) {
     using RG = Ring<MODE>;
@@ -379,7 +354,6 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     Params p{};
     p.header = plan.header;
     p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
-    p.row_token = plan.row_token;
     p.nf = static_cast<int>((wrows + 255) / 256);
     p.wrows = static_cast<int>(wrows);
     p.nkb = static_cast<int>((K + kBK - 1) / kBK);
@@ -397,15 +371,22 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+bool map_rows(moe::RowMaps *m, const void *ptr, bool bf16, int64_t inner, int64_t rows) {
+    for (int i = 0; i < 4; ++i)
+        if (!map_16(&m->m[i], ptr, bf16, inner, rows, 128u >> i)) return false;
+    return true;
+}
+
 }  // namespace
 
-cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *x, const void *wg, const void *wu, void *h,
-                              int64_t rows, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
-                              float out_scale, cudaStream_t s) {
+cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *xs, const void *wg, const void *wu, void *h,
+                              int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale, float out_scale,
+                              cudaStream_t s) {
     const bool bf = op == DT_BF16;
-    CUtensorMap w0, w1, b;
+    CUtensorMap w0, w1;
+    moe::RowMaps b;
     if (!map_16(&w0, wg, bf, d, experts * ffn, kBM) || !map_16(&w1, wu, bf, d, experts * ffn, kBM) ||
-        !map_16(&b, x, bf, d, rows, 1))   // gathered rows: a box one row high
+        !map_rows(&b, xs, bf, d, pairs))
         return cudaErrorInvalidValue;
     return bf ? launch<GATEUP, true>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s)
               : launch<GATEUP, false>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s);
@@ -414,8 +395,9 @@ cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *x, const voi
 cudaError_t launch_moe_down(int op, const Plan &plan, const void *h, const void *wd, float *part, int64_t pairs,
                             int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s) {
     const bool bf = op == DT_BF16;
-    CUtensorMap w, b;
-    if (!map_16(&w, wd, bf, ffn, experts * d, kBM) || !map_16(&b, h, bf, ffn, pairs, 8)) return cudaErrorInvalidValue;
+    CUtensorMap w;
+    moe::RowMaps b;
+    if (!map_16(&w, wd, bf, ffn, experts * d, kBM) || !map_rows(&b, h, bf, ffn, pairs)) return cudaErrorInvalidValue;
     return bf ? launch<DOWN, true>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s)
               : launch<DOWN, false>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
 }

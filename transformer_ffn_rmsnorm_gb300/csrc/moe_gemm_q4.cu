@@ -42,7 +42,7 @@ namespace {
 using moe::Plan;
 using moe::Unit;
 
-constexpr int kRows = 128, kK = 128, kTile = kMoeQ4Tile;
+constexpr int kRows = 128, kK = 128, kTile = kMoeCutQ4.tile, kGran = kMoeCutQ4.gran;
 constexpr uint32_t kRawBytes = kRows * 64, kScaleBytes = kRows * 8;   // a stage's nibbles and scales
 constexpr uint32_t kBBytes = kTile * kK * 2;                          // room for its tokens
 constexpr int kRawStages = 12, kBStages = 3, kAStages = 4;
@@ -61,24 +61,17 @@ enum Mode { GATEUP = 0, DOWN = 1 };
 struct Params {
     const int *header;
     const int4 *tiles;
-    const int *row_token;
     const uint16_t *s0, *s1;   // scales of W_gate and W_up, or of W_down
     int nf;                    // feature tiles of 64 (gate/up) or 128 rows
     int wrows;                 // weight rows of an expert (ffn or d)
-    int ngrp;                  // 128-value groups of a row: the stages of a unit
+    int ngrp;                  // 128-value groups of a row: stages of 128 values
+    int splits;                // of the reduction (down)
+    int64_t split_stride;      // floats from one split of part to the next
     void *out;
     float acc_scale, out_scale;
     unsigned *err;
 };
 
-__device__ __forceinline__ void gather4(uint32_t dst, const void *map, uint32_t bar, int x, int r0, int r1, int r2,
-                                        int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
-}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -132,14 +125,14 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s, uint32_t (&o
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_gemm_q4_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
-                       const __grid_constant__ CUtensorMap map_b, const Params p) {
+                       const __grid_constant__ moe::RowMaps maps_b, const Params p) {
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;   // features of a unit
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_rfull[kRawStages], bar_rempty[kRawStages];
     __shared__ __align__(8) uint64_t bar_bfull[kBStages], bar_bempty[kBStages];
     __shared__ __align__(8) uint64_t bar_afull[kAStages], bar_aempty[kAStages];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
-    __shared__ float s_swap[MODE == GATEUP ? 2 : 1][2][8][MODE == GATEUP ? 64 : 1];
+    __shared__ float s_swap[MODE == GATEUP ? 2 : 1][2][8][64];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort, s_never;
 
@@ -169,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_mbar_init();
         ptx::tma_prefetch_map(&map_w0);
         if (MODE == GATEUP) ptx::tma_prefetch_map(&map_w1);
-        ptx::tma_prefetch_map(&map_b);
+        for (int i = 0; i < 4; ++i) ptx::tma_prefetch_map(&maps_b.m[i]);
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem_base), 512);
@@ -187,10 +180,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     ptx::griddep_wait();   // the plan, x, h: written by kernels before this one
-    const int units = __ldcg(p.header) * p.nf;
-    auto unit_at = [&](int u) {
+    // unit v is split v % splits of tile unit v / splits: stages [lo, hi)
+    const int units = __ldcg(p.header) * p.nf * p.splits;
+    auto lo_of = [&](int v) { return p.ngrp * (v % p.splits) / p.splits; };
+    auto hi_of = [&](int v) { return p.ngrp * (v % p.splits + 1) / p.splits; };
+    auto unit_at = [&](int v) {
+        const int u = v / p.splits;
         const int4 *t = p.tiles + 2 * (u / p.nf);
-        return moe::unit_of(u, p.nf, __ldcg(t), __ldcg(t + 1));
+        return moe::unit_of<kGran>(u, p.nf, __ldcg(t), __ldcg(t + 1));
     };
 
     if (warp == 0) {
@@ -201,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = u0; u < units && ok; u += ustep) {
                 const Unit t = unit_at(u);
                 const int wrow = t.expert * p.wrows + t.f * kFRows;
-                for (int g = 0; g < p.ngrp; ++g) {
+                for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                     if (!ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs)) {
                         ok = false;
                         break;
@@ -231,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint16_t *m = MODE == GATEUP && i >= 2 ? p.s1 : p.s0;
                 src[i] = m + (static_cast<int64_t>(t.expert) * p.wrows + min(f, p.wrows - 1)) * (4 * p.ngrp);
             }
-            for (int g = 0; g < p.ngrp; ++g) {
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -254,13 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = unit_at(u);
-            int gr[4] = {0, 0, 0, 0};
-            const bool mine = MODE == GATEUP ? 4 * lane < t.n : 8 * lane < t.n;
-            if (MODE == GATEUP && mine) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) gr[i] = __ldcg(p.row_token + t.row0 + min(4 * lane + i, t.valid - 1));
-            }
-            for (int g = 0; g < p.ngrp; ++g) {
+            const int box = moe::row_box(t.n, lane);
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_bempty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -269,15 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t full = bar(&bar_bfull[s]);
                 if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
                 __syncwarp();
-                if (mine) {
+                if (box >= 0) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {   // 64 values each; past the row's end zero fill
-                        const uint32_t dst = base + s * kBBytes + j * (kBBytes / 2);
-                        if (MODE == GATEUP)
-                            gather4(dst + lane * 512, &map_b, full, g * kK + j * 64, gr[0], gr[1], gr[2], gr[3]);
-                        else
-                            ptx::tma_load_2d(dst + lane * 1024, &map_b, full, g * kK + j * 64, t.row0 + 8 * lane);
-                    }
+                    for (int j = 0; j < 2; ++j)   // 64 values each; past the row's end zero fill
+                        ptx::tma_load_2d(base + s * kBBytes + j * (kBBytes / 2) + box * 128, &maps_b.m[lane], full,
+                                         g * kK + j * 64, t.row0 + box);
                 }
                 ++produced;
                 if (++s == kBStages) {
@@ -292,13 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int sa = 0, sb = 0, acc = 0;
             uint32_t pa = 0, pb = 0, pacc = 0;
             int4 na = make_int4(0, 0, 1, 0), nb = na;
-            auto fetch = [&](int u) {
-                na = __ldcg(p.tiles + 2 * (u / p.nf));
-                nb = __ldcg(p.tiles + 2 * (u / p.nf) + 1);
+            auto fetch = [&](int v) {
+                na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
+                nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
             };
             if (u0 < units) fetch(u0);
             for (int u = u0; u < units && ok; u += ustep) {
-                const Unit t = moe::unit_of(u, p.nf, na, nb);
+                const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
                 if (u + ustep < units) fetch(u + ustep);
                 const uint32_t idesc = ptx::idesc_f16(128, t.n, false);
                 if (!ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs)) {
@@ -306,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t d = tmem + acc * 128;
-                for (int g = 0; g < p.ngrp; ++g) {
+                const int g0 = lo_of(u);
+                for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                     if (!ptx::mbar_wait(bar(&bar_bfull[sb]), pb, abort_flag, kWaitNs) ||
                         !ptx::mbar_wait(bar(&bar_afull[sa]), pa, abort_flag, kWaitNs)) {
                         ok = false;
@@ -317,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kK / 16; ++k) {
                         const uint64_t bd = ptx::sdesc_k_sw128(base + sb * kBBytes + (k >> 2) * (kBBytes / 2)) + 2 * (k & 3);
-                        mma_ts(d, a + 8 * k, bd, idesc, (g | k) != 0);
+                        mma_ts(d, a + 8 * k, bd, idesc, g != g0 || k != 0);
                     }
                     ptx::tc_commit(bar(&bar_bempty[sb]));
                     ptx::tc_commit(bar(&bar_aempty[sa]));
@@ -348,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, sa = 0;
         uint32_t ph = 0, pa = 0;
         for (int u = u0; u < units && ok; u += ustep) {
-            for (int g = 0; g < p.ngrp; ++g) {
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 bool got = ptx::mbar_wait(bar(&bar_rfull[s]), ph, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -411,69 +400,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units; u += ustep) {
             const Unit t = unit_at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
-            // (with the exchange below the four warps stay or leave together:
-            // the vote is over all of them)
-            __syncwarp();
-            bool stay;
-            if constexpr (MODE == GATEUP) {
-                int all;
-                asm volatile(
-                    "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, 1, 128, a;\n\t"
-                    "selp.b32 %0, 1, 0, b;\n\t}"
-                    : "=r"(all)
-                    : "r"(got ? 1 : 0)
-                    : "memory");
-                stay = all != 0;
-            } else {
-                stay = __all_sync(0xffffffffu, got);
-            }
+            const bool stay = moe::epilogue_vote(got);
             if (!stay) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 128;
-            if constexpr (MODE == GATEUP) {
-                // lanes 0-63 hold gate, 64-127 up of the same 64 features: of
-                // every 16 columns the gate warps take the first eight and
-                // the up warps the others, and hand over what the other side needs
-                const int fl = 32 * (q & 1) + lane, mat = q >> 1;
-                const int f = t.f * kFRows + fl;
-                const int fp = (f & ~3) | ((f & 1) << 1) | ((f >> 1) & 1);   // its place in h
-                const bool live = f < p.wrows;
-                __half *dst = static_cast<__half *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + fp;
-                for (int c = 0, pp = 0; c < t.n; c += 16, pp ^= 1) {
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s_swap[pp][mat][i][fl] = __uint_as_float(mat ? r[i] : r[8 + i]);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float other = s_swap[pp][mat ^ 1][i][fl];
-                        const float mine = __uint_as_float(mat ? r[8 + i] : r[i]);
-                        const float gate = mat ? other : mine, up = mat ? mine : other;
-                        const float hv = silu_f32(gate * p.acc_scale) * (up * p.acc_scale) * p.out_scale;
-                        const int col = c + 8 * mat + i;
-                        // h feeds the next product: one rounding to fp16
-                        if (live && col < t.valid) dst[static_cast<int64_t>(col) * p.wrows] = __float2half_rn(hv);
-                    }
-                }
-            } else {
-                const int f = t.f * kFRows + 32 * q + lane;
-                const bool live = f < p.wrows;
-                float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + f;
-                for (int c = 0; c < t.n; c += 16) {
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (live && c + i < t.valid)
-                            dst[static_cast<int64_t>(c + i) * p.wrows] = __uint_as_float(r[i]) * p.acc_scale;
-                }
-            }
+            if constexpr (MODE == GATEUP)
+                moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, p.wrows, static_cast<__half *>(p.out), s_swap,
+                                                   p.acc_scale, p.out_scale);
+            else
+                moe::store_epilogue(taddr, q, lane, t, p.wrows,
+                                    static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(&bar_tempty[acc]));
@@ -508,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int MODE>
-cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &b,
-                   const uint16_t *s0, const uint16_t *s1, int64_t pairs, int64_t experts, int64_t wrows, int64_t K,
-                   void *out, float acc_scale, float out_scale, cudaStream_t s) {
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const moe::RowMaps &b,
+                   const uint16_t *s0, const uint16_t *s1, int splits, int64_t pairs, int64_t experts, int64_t wrows,
+                   int64_t K, void *out, float acc_scale, float out_scale, cudaStream_t s) {
     const auto kern = &moe_gemm_q4_kernel<MODE>;
     static int configured_device = -1;
     int dev = 0;
@@ -525,18 +464,19 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     Params p{};
     p.header = plan.header;
     p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
-    p.row_token = plan.row_token;
     p.s0 = s0;
     p.s1 = s1;
     p.nf = static_cast<int>((wrows + kFRows - 1) / kFRows);
     p.wrows = static_cast<int>(wrows);
     p.ngrp = static_cast<int>((K + kK - 1) / kK);
+    p.splits = splits;
+    p.split_stride = pairs * wrows;
     p.out = out;
     p.acc_scale = acc_scale;
     p.out_scale = out_scale;
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
-    const int64_t grid = std::min<int64_t>(sm_count(), moe::max_tiles(pairs, experts, kTile) * p.nf);
+    const int64_t grid = std::min<int64_t>(sm_count(), moe::max_tiles(pairs, experts, kTile) * p.nf * splits);
     LaunchScope scope(MODE == GATEUP ? K_MOE_GATEUP : K_MOE_DOWN, s);
     e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, w0, w1, b, p);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -548,29 +488,34 @@ bool map_q4(CUtensorMap *m, const uint8_t *qs, int64_t K, int64_t rows, uint32_t
     return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 64, box_rows,
                          CU_TENSOR_MAP_SWIZZLE_64B);
 }
-bool map_f16(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows) {
-    return encode_tma_2d(m, ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner, rows, inner * 2, 64, box_rows,
-                         CU_TENSOR_MAP_SWIZZLE_128B);
+bool map_rows(moe::RowMaps *m, const void *ptr, int64_t inner, int64_t rows) {
+    for (int i = 0; i < 4; ++i)
+        if (!encode_tma_2d(&m->m[i], ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner, rows, inner * 2, 64, 128u >> i,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+            return false;
+    return true;
 }
 
 }  // namespace
 
-cudaError_t launch_moe_gateup_q4(const Plan &plan, const void *x16, const uint8_t *qg, const uint16_t *sg,
-                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t rows, int64_t pairs, int64_t d,
-                                 int64_t ffn, int64_t experts, float out_scale, cudaStream_t s) {
-    CUtensorMap w0, w1, b;
+cudaError_t launch_moe_gateup_q4(const Plan &plan, const void *xs, const uint8_t *qg, const uint16_t *sg,
+                                 const uint8_t *qu, const uint16_t *su, void *h, int64_t pairs, int64_t d, int64_t ffn,
+                                 int64_t experts, float out_scale, cudaStream_t s) {
+    CUtensorMap w0, w1;
+    moe::RowMaps b;
     if (!map_q4(&w0, qg, d, experts * ffn, 64) || !map_q4(&w1, qu, d, experts * ffn, 64) ||
-        !map_f16(&b, x16, d, rows, 1))
+        !map_rows(&b, xs, d, pairs))
         return cudaErrorInvalidValue;
-    return launch<GATEUP>(plan, w0, w1, b, sg, su, pairs, experts, ffn, d, h, 1.f, out_scale, s);
+    return launch<GATEUP>(plan, w0, w1, b, sg, su, 1, pairs, experts, ffn, d, h, 1.f, out_scale, s);
 }
 
 cudaError_t launch_moe_down_q4(const Plan &plan, const void *h, const uint8_t *qd, const uint16_t *sd, float *part,
-                               int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
+                               int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
                                cudaStream_t s) {
-    CUtensorMap w, b;
-    if (!map_q4(&w, qd, ffn, experts * d, 128) || !map_f16(&b, h, ffn, pairs, 8)) return cudaErrorInvalidValue;
-    return launch<DOWN>(plan, w, w, b, sd, sd, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+    CUtensorMap w;
+    moe::RowMaps b;
+    if (!map_q4(&w, qd, ffn, experts * d, 128) || !map_rows(&b, h, ffn, pairs)) return cudaErrorInvalidValue;
+    return launch<DOWN>(plan, w, w, b, sd, sd, splits, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
 }
 
 }  // namespace ffn

@@ -1,14 +1,14 @@
 // moe_plan.cu -- the two ends of the routed block: sorting the (token, slot)
 // pairs by expert, and adding each token's weighted results.
 //
-// The plan is one CTA: it counts the pairs of each expert in shared memory,
-// scans the counts, cuts every expert's rows into token tiles of equal width
-// (rounded to the 32 columns a tile can end on) and deals the sorted
-// positions out.  Equal lanes of a warp count once (match_any), so a few
-// popular experts cost no serialised atomics.  The order of an expert's rows depends
-// on the order of the warps, the results do not: every column of a product
-// is computed the same way wherever it stands.  Other CTAs of the same launch
-// write the 16-bit activations of the products where those are not x itself.
+// The plan counts the pairs of each expert in shared memory, scans the
+// counts, cuts every expert's rows into token tiles of equal width and deals
+// the sorted positions out.  Up to 256 pairs (decode) every CTA of one
+// launch does that for itself and copies a share of x's rows to their sorted
+// places; more pairs are sorted by one CTA and copied by a second kernel (a
+// launch is then small beside the products).  In the large form the order of an expert's
+// rows depends on the order of the warps; the results do not: every column
+// of a product is computed the same way wherever it stands.
 //
 // The combination adds a token's k fp32 rows in slot order with fp32 weights
 // and rounds once.  Bound by reading those rows.
@@ -24,14 +24,17 @@ using moe::Tile;
 
 constexpr int kPlanThreads = 1024;
 
+constexpr int kSmallPairs = 256;   // up to here one launch plans and copies
+
 struct PlanParams {
     const int32_t *idx;
-    int pairs, k, experts, tile;
+    int pairs, k, experts;
+    moe::Cut cut;
     Plan plan;
     const void *x;
-    void *x16;
-    int64_t nvec;   // 8-element vectors of x
-    bool perm;
+    void *xs;
+    int nvec;   // 8-element vectors of a row of x
+    bool to_f16, perm;
     unsigned *err;
 };
 
@@ -77,97 +80,207 @@ __device__ __forceinline__ void scan2(int &a, int &b, int (*s_warp)[32], int &to
     total_b = s_warp[2][1];
 }
 
+// One 8-element vector of x as the products read it.
 template <typename T>
-__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const PlanParams p) {
+__device__ __forceinline__ uint4 convert_vec(const PlanParams &p, const uint4 &v, bool &bad) {
+    if (!p.to_f16) return v;
+    float f[8];
+    Vec16<T>::unpack(v, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bad |= fabsf(f[e]) > 65504.f && fabsf(f[e]) < INFINITY;
+    if (p.perm) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const float t = f[e + 1];
+            f[e + 1] = f[e + 2];
+            f[e + 2] = t;
+        }
+    }
+    return Vec16<__half>::pack(f);
+}
+
+struct PlanShared {
+    int count[moe::kMaxExperts], first[moe::kMaxExperts], row0[moe::kMaxExperts];
+    int warp[3][32];
+    int widest;
+};
+
+// From the experts' counts in sh.count: first tiles and first rows; with
+// `write` also the tables.  Returns the number of sorted rows.
+__device__ __forceinline__ int plan_tables(const PlanParams &p, PlanShared &sh, bool write) {
+    const int c = sh.count[threadIdx.x];
+    const int nt = (c + p.cut.tile - 1) / p.cut.tile;
+    int row0 = c, first = nt, total, ntiles;
+    scan2(row0, first, sh.warp, total, ntiles);
+    sh.first[threadIdx.x] = first;
+    sh.row0[threadIdx.x] = row0;
+    auto width = [&](int rows, int tiles) {
+        return ((rows + tiles - 1) / tiles + p.cut.gran - 1) / p.cut.gran * p.cut.gran;
+    };
+    if (write && nt) atomicMax(&sh.widest, width(c, nt));
+    __syncthreads();
+    if (write) {
+        if (threadIdx.x == 0) {
+            p.plan.header[0] = ntiles;
+            p.plan.header[1] = sh.widest;
+            p.plan.header[2] = total;
+        }
+        for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
+            // the last expert whose first tile is at or before q (one without
+            // tiles shares its first with the next one)
+            int lo = 0, hi = p.experts - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (sh.first[mid] <= q) lo = mid;
+                else hi = mid - 1;
+            }
+            Tile t;
+            t.expert = lo;
+            t.first = sh.first[lo];
+            t.rows = sh.count[lo];
+            t.count = (t.rows + p.cut.tile - 1) / p.cut.tile;
+            t.cols = width(t.rows, t.count);
+            t.row0 = sh.row0[lo];
+            t.pad0 = t.pad1 = 0;
+            p.plan.tiles[q] = t;
+        }
+    }
+    return total;
+}
+
+// Few pairs: every CTA sorts them for itself (a row's place is the number of
+// equal experts before it, so all CTAs agree) and copies its share of the
+// rows; the first one writes the tables.
+template <typename T>
+__global__ void __launch_bounds__(kPlanThreads) moe_plan_small_kernel(const PlanParams p) {
+    __shared__ PlanShared sh;
+    __shared__ __align__(16) int s_e[kSmallPairs];
+    __shared__ int s_token[kSmallPairs];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    if (blockIdx.x > 0) {
-        // fp16 copy of x
-        const uint4 *src = static_cast<const uint4 *>(p.x);
-        uint4 *dst = static_cast<uint4 *>(p.x16);
-        bool bad = false;
-        const int64_t step = static_cast<int64_t>(gridDim.x - 1) * kPlanThreads;
-        for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < p.nvec; i += step) {
-            float f[8];
-            Vec16<T>::unpack(src[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) bad |= fabsf(f[e]) > 65504.f && fabsf(f[e]) < INFINITY;
-            if (p.perm) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float t = f[e + 1];
-                    f[e + 1] = f[e + 2];
-                    f[e + 2] = t;
-                }
-            }
-            dst[i] = Vec16<__half>::pack(f);
+    const int i = threadIdx.x;
+    int e = i < p.pairs ? p.idx[i] : -1;
+    if (e >= p.experts) e = -1;
+    sh.count[i] = 0;
+    if (i < kSmallPairs) s_e[i] = e;
+    if (i == 0) sh.widest = 0;
+    __syncthreads();
+    int rank = 0;
+    if (e >= 0) {
+        atomicAdd(&sh.count[e], 1);
+        const int4 *v = reinterpret_cast<const int4 *>(s_e);
+        for (int j = 0; 4 * j < i; ++j) {
+            const int4 o = v[j];
+            rank += (o.x == e) + (o.y == e && 4 * j + 1 < i) + (o.z == e && 4 * j + 2 < i) + (o.w == e && 4 * j + 3 < i);
         }
-        if (bad) atomicOr(p.err, DEVERR_RANGE);
-        return;
     }
-    __shared__ int s_count[moe::kMaxExperts], s_first[moe::kMaxExperts], s_row0[moe::kMaxExperts];
-    __shared__ int s_warp[3][32];
-    __shared__ int s_widest;
+    __syncthreads();
+    const int total = plan_tables(p, sh, blockIdx.x == 0);
+    if (i < p.pairs) {
+        const int at = e >= 0 ? sh.row0[e] + rank : -1;
+        if (e >= 0) s_token[at] = i / p.k;
+        if (blockIdx.x == 0) {
+            p.plan.pos[i] = at;
+            if (e >= 0) p.plan.row_token[at] = i / p.k;
+        }
+    }
+    __syncthreads();
+    const uint4 *src = static_cast<const uint4 *>(p.x);
+    uint4 *dst = static_cast<uint4 *>(p.xs);
+    bool bad = false;
+    const int64_t n = static_cast<int64_t>(total) * p.nvec;
+    for (int64_t v = blockIdx.x * kPlanThreads + threadIdx.x; v < n; v += gridDim.x * kPlanThreads) {
+        const int r = static_cast<int>(v / p.nvec), c = static_cast<int>(v - static_cast<int64_t>(r) * p.nvec);
+        dst[v] = convert_vec<T>(p, src[static_cast<int64_t>(s_token[r]) * p.nvec + c], bad);
+    }
+    if (bad) atomicOr(p.err, DEVERR_RANGE);
+}
+
+// Many pairs: one CTA.  A pair's rank among its expert's is the counter's
+// value when it came (a few experts: counted by warp ballots, so that the
+// counters are not hit 32 times a warp).
+__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const PlanParams p) {
+    __shared__ PlanShared sh;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    constexpr int kBatch = 8;   // index loads in flight a thread
     const int lane = threadIdx.x & 31;
-    s_count[threadIdx.x] = 0;
-    if (threadIdx.x == 0) s_widest = 0;
+    sh.count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.widest = 0;
     __syncthreads();
-    const int rounds = (p.pairs + kPlanThreads - 1) / kPlanThreads;
-    for (int r = 0; r < rounds; ++r) {
-        const int i = r * kPlanThreads + threadIdx.x;
+    auto load = [&](int i) {
         const int e = i < p.pairs ? p.idx[i] : -1;
-        const bool ok = e >= 0 && e < p.experts;
-        const unsigned same = __match_any_sync(0xffffffffu, ok ? e : -1);
-        if (ok && __ffs(same) - 1 == lane) atomicAdd(&s_count[e], __popc(same));
-    }
-    __syncthreads();
-    const int c = s_count[threadIdx.x];
-    const int nt = (c + p.tile - 1) / p.tile;
-    int row0 = c, first = nt, total, ntiles;
-    scan2(row0, first, s_warp, total, ntiles);
-    s_first[threadIdx.x] = first;
-    s_row0[threadIdx.x] = row0;
-    if (nt) atomicMax(&s_widest, (((c + nt - 1) / nt) + 31) & ~31);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        p.plan.header[0] = ntiles;
-        p.plan.header[1] = s_widest;
-    }
-    for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
-        // the last expert whose first tile is at or before q and that has tiles
-        int lo = 0, hi = p.experts - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_first[mid] <= q) lo = mid;
-            else hi = mid - 1;
+        return e < p.experts ? e : -1;
+    };
+    for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x) < p.pairs; i0 += kBatch * kPlanThreads) {
+        int e[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) e[b] = load(i0 + b * kPlanThreads);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kPlanThreads;
+            int rank = 0;
+            if (p.experts <= 16) {
+                for (int x = 0; x < p.experts; ++x) {
+                    const unsigned m = __ballot_sync(0xffffffffu, e[b] == x);
+                    int base = 0;
+                    if (m && lane == 0) base = atomicAdd(&sh.count[x], __popc(m));
+                    base = __shfl_sync(0xffffffffu, base, 0);
+                    if (e[b] == x) rank = base + __popc(m & ((1u << lane) - 1u));
+                }
+            } else if (e[b] >= 0) {
+                rank = atomicAdd(&sh.count[e[b]], 1);
+            }
+            if (i < p.pairs) p.plan.pos[i] = e[b] >= 0 ? rank : -1;
         }
-        const int ce = s_count[lo], n = (ce + p.tile - 1) / p.tile;
-        Tile t;
-        t.expert = lo;
-        t.first = s_first[lo];
-        t.count = n;
-        t.cols = (((ce + n - 1) / n) + 31) & ~31;
-        t.row0 = s_row0[lo];
-        t.rows = ce;
-        t.pad0 = t.pad1 = 0;
-        p.plan.tiles[q] = t;
     }
     __syncthreads();
-    s_count[threadIdx.x] = row0;   // next free row of each expert
-    __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-        const int i = r * kPlanThreads + threadIdx.x;
-        const int e = i < p.pairs ? p.idx[i] : -1;
-        const bool ok = e >= 0 && e < p.experts;
-        const unsigned same = __match_any_sync(0xffffffffu, ok ? e : -1);
-        const int leader = __ffs(same) - 1;
-        int base = 0;
-        if (ok && leader == lane) base = atomicAdd(&s_count[e], __popc(same));
-        base = __shfl_sync(0xffffffffu, base, leader);
-        const int at = base + __popc(same & ((1u << lane) - 1u));
-        if (i < p.pairs) p.plan.pos[i] = ok ? at : -1;
-        if (ok) p.plan.row_token[at] = i / p.k;
+    plan_tables(p, sh, true);
+    for (int i0 = threadIdx.x; i0 < p.pairs; i0 += kBatch * kPlanThreads) {
+        int e[kBatch], rank[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kPlanThreads;
+            e[b] = load(i);
+            rank[b] = i < p.pairs ? p.plan.pos[i] : -1;   // written by this thread above
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kPlanThreads;
+            if (i >= p.pairs || e[b] < 0) continue;
+            const int at = sh.row0[e[b]] + rank[b];
+            p.plan.pos[i] = at;
+            p.plan.row_token[at] = i / p.k;
+        }
     }
+}
+
+// The sorted copy of x's rows, after moe_plan_kernel.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_gather_kernel(const PlanParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const uint4 *src = static_cast<const uint4 *>(p.x);
+    uint4 *dst = static_cast<uint4 *>(p.xs);
+    bool bad = false;
+    const int64_t n = static_cast<int64_t>(p.plan.header[2]) * p.nvec, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v0 < n; v0 += 4 * step) {
+        uint4 a[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int64_t v = v0 + b * step;
+            if (v < n) {
+                const int64_t r = v / p.nvec, c = v - r * p.nvec;
+                a[b] = src[static_cast<int64_t>(p.plan.row_token[r]) * p.nvec + c];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int64_t v = v0 + b * step;
+            if (v < n) dst[v] = convert_vec<T>(p, a[b], bad);
+        }
+    }
+    if (bad) atomicOr(p.err, DEVERR_RANGE);
 }
 
 struct CombineParams {
@@ -176,7 +289,8 @@ struct CombineParams {
     const void *res;
     void *y;
     int64_t rows, nvec;   // nvec: 8-element vectors of a row
-    int k;
+    int64_t split_stride; // floats from one split of part to the next
+    int k, splits;
 };
 
 template <typename T>
@@ -202,9 +316,22 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p)
             const int at = p.pos[t * p.k + j];
             if (at < 0) continue;
             const float w = p.w[t * p.k + j];
-            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(at) * p.nvec + c) * 2;
-            const float4 a = __ldcs(src), b = __ldcs(src + 1);
-            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const float *src = p.part + (static_cast<int64_t>(at) * p.nvec + c) * 8;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            for (int sp = 0; sp < p.splits; ++sp, src += p.split_stride) {
+                const float4 a = __ldcs(reinterpret_cast<const float4 *>(src)),
+                             b = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
+                v[0] += a.x;
+                v[1] += a.y;
+                v[2] += a.z;
+                v[3] += a.w;
+                v[4] += b.x;
+                v[5] += b.y;
+                v[6] += b.z;
+                v[7] += b.w;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, v[e], sum[e]);
         }
@@ -236,34 +363,54 @@ Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile) {
     return p;
 }
 
-cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts, int tile, const Plan &plan,
-                            const void *x, void *x16, int64_t d, int dt, bool perm, cudaStream_t s) {
+namespace {
+
+template <typename T>
+cudaError_t launch_plan(const PlanParams &p, cudaStream_t s) {
+    const int64_t vecs = static_cast<int64_t>(p.pairs) * p.nvec;
+    cudaError_t e;
+    if (p.pairs <= kSmallPairs) {
+        // four vectors a thread, at most one CTA a multiprocessor
+        const int64_t grid = std::min<int64_t>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), sm_count());
+        LaunchScope scope(K_MOE_PLAN, s);
+        e = launch_dependent(moe_plan_small_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, s, p);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    {
+        LaunchScope scope(K_MOE_PLAN, s);
+        e = launch_dependent(moe_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t grid = std::min<int64_t>((vecs + 1023) / 1024, 16 * static_cast<int64_t>(sm_count()));
+    LaunchScope scope(K_MOE_PLAN, s);
+    e = launch_dependent(moe_gather_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts, moe::Cut cut, const Plan &plan,
+                            const void *x, void *xs, int64_t d, int dt, bool to_f16, bool perm, cudaStream_t s) {
     PlanParams p{};
     p.idx = idx;
     p.pairs = static_cast<int>(rows * k);
     p.k = k;
     p.experts = experts;
-    p.tile = tile;
+    p.cut = cut;
     p.plan = plan;
     p.x = x;
-    p.x16 = x16;
-    p.nvec = rows * d / 8;
+    p.xs = xs;
+    p.nvec = static_cast<int>(d / 8);
+    p.to_f16 = to_f16;
     p.perm = perm;
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
-    // the copy's CTAs: up to four vectors a thread, at most two a multiprocessor
-    const int64_t copy = x16 ? std::min<int64_t>((p.nvec + 4 * kPlanThreads - 1) / (4 * kPlanThreads), 2 * sm_count()) : 0;
-    const dim3 grid(static_cast<unsigned>(1 + copy));
-    LaunchScope scope(K_MOE_PLAN, s);
-    const cudaError_t e = dt == DT_BF16
-                              ? launch_dependent(moe_plan_kernel<__nv_bfloat16>, grid, dim3(kPlanThreads), 0, s, p)
-                              : launch_dependent(moe_plan_kernel<__half>, grid, dim3(kPlanThreads), 0, s, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return dt == DT_BF16 ? launch_plan<__nv_bfloat16>(p, s) : launch_plan<__half>(p, s);
 }
 
-cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *part, const void *res, void *y,
-                               int64_t rows, int k, int64_t d, int dt, cudaStream_t s) {
-    CombineParams p{plan.pos, w, part, res, y, rows, d / 8, k};
+cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *part, int splits, const void *res,
+                               void *y, int64_t rows, int k, int64_t d, int dt, cudaStream_t s) {
+    CombineParams p{plan.pos, w, part, res, y, rows, d / 8, rows * k * d, k, splits};
     const int64_t blocks = std::min<int64_t>((rows * p.nvec + 255) / 256, 32 * static_cast<int64_t>(sm_count()));
     LaunchScope scope(K_MOE_COMBINE, s);
     const cudaError_t e =
@@ -272,6 +419,22 @@ cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *pa
                       : launch_dependent(moe_combine_kernel<__half>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                                          s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn) {
+    const int64_t units = std::min(pairs, experts) * ((d + 127) / 128), stages = (ffn + 127) / 128;
+    constexpr int64_t kSms = 152;   // (not the current device's: the workspace depends on it)
+    if (pairs > 1024) return 1;   // tiles enough, and each split writes a row a pair
+    int best = 1;
+    double least = 0.;
+    for (int s = 1; s <= 8 && stages / s >= 4; ++s) {
+        const double t = static_cast<double>((units * s + kSms - 1) / kSms) / s;
+        if (s == 1 || t < 0.98 * least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
 }
 
 }  // namespace ffn
