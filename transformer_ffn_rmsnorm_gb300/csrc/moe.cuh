@@ -50,7 +50,7 @@ __host__ __device__ constexpr int64_t max_tiles(int64_t pairs, int64_t experts, 
 // run through its token tiles first, so that the feature tile's weights are
 // read from HBM once and from L2 by the other token tiles.
 struct Unit {
-    int expert, f, row0, valid, n;
+    int expert, f, tt, row0, valid, n;   // tt: which token tile of the expert
 };
 template <int GRAN>
 __device__ __forceinline__ Unit unit_of(int u, int nf, const int4 &a, const int4 &b) {
@@ -58,25 +58,31 @@ __device__ __forceinline__ Unit unit_of(int u, int nf, const int4 &a, const int4
     const int local = u - a.y * nf;
     r.expert = a.x;
     r.f = local / a.z;
-    const int tt = local - r.f * a.z;
-    r.row0 = b.x + tt * a.w;
-    r.valid = min(a.w, b.y - tt * a.w);
+    r.tt = local - r.f * a.z;
+    r.row0 = b.x + r.tt * a.w;
+    r.valid = min(a.w, b.y - r.tt * a.w);
     r.n = (r.valid + GRAN - 1) & ~(GRAN - 1);
     return r;
 }
 
-// The sorted rows a tile reads, loaded in boxes of 128, 64, 32 and 16 rows
-// (a copy engine's request costs about 80 cycles whatever its size, so few
-// large ones: boxes of eight rows, or four gathered rows a request, had the
-// products wait 2400 to 2800 cycles for a stage whose MMAs take 1024).
+// The sorted rows a tile reads, loaded in boxes of 128, 64, 32 and 16 rows:
+// `rows` (a multiple of 16, at most 128) are the boxes of its set bits.
 struct RowMaps {
     CUtensorMap m[4];
 };
-// This lane's box for `rows` rows (a multiple of 16, at most 128): its first
-// row, or -1 if it has none; lanes 0 .. 3 take the boxes of 128 >> lane rows.
-__device__ __forceinline__ int row_box(int rows, int lane) {
-    const int size = 128 >> lane;
-    return lane < 4 && (rows & size) ? (rows & ~(2 * size - 1)) : -1;
+template <typename F>
+__device__ __forceinline__ void for_row_boxes(const RowMaps &maps, int rows, F load) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (rows & (128 >> i)) load(&maps.m[i], rows & ~((256 >> i) - 1));
+}
+
+// silu(gate) * up * scale in fp32.  The division is the approximate one (2 ulp,
+// and 0 for a denominator beyond 2^126, where silu is below 1e-36): next to the
+// 16-bit rounding of h nothing, and a third of the instructions of the
+// correctly rounded reciprocal, in epilogues that the MMAs wait for.
+__device__ __forceinline__ float swiglu(float gate, float up, float scale) {
+    return __fdividef(gate, 1.0f + __expf(-gate)) * (up * scale);
 }
 
 // ---- epilogues of the single-CTA products (four warps, q = warp % 4, lane:
@@ -108,7 +114,7 @@ __device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane,
         for (int i = 0; i < 8; ++i) {
             const float other = swap[pp][mat ^ 1][i][fl];
             const float mine = __uint_as_float(mat ? r[8 + i] : r[i]);
-            const float hv = silu_f32((mat ? other : mine) * acc_scale) * ((mat ? mine : other) * acc_scale) * out_scale;
+            const float hv = swiglu((mat ? other : mine) * acc_scale, mat ? mine : other, acc_scale * out_scale);
             const int col = c + 8 * mat + i;
             if (live && col < t.valid) dst[static_cast<int64_t>(col) * wrows] = from_f32<T>(hv);
         }

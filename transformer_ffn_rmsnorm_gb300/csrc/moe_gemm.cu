@@ -18,8 +18,8 @@
 // tile's MMAs.  Where every tile of the call is at most 128 wide (plan.header[1]) there are two accumulators
 // and it does; the down product always has two.
 //
-// Roles: warp 0 loads (lane 0 weights, lanes 0-3 a box of tokens each), warp 1 issues the
-// MMAs (one thread of the even CTA), warps 2-9 read the accumulators (lane =
+// Roles: warp 0 loads, warp 1 issues the
+// MMAs (one thread of the even CTA), warps 2-17 read the accumulators (lane =
 // weight row, column = token): for a fixed column a warp's 32 lanes store 32
 // neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
@@ -39,7 +39,7 @@ constexpr int kBM = 128, kBK = 64, kTile = kMoeCutPair.tile;
 constexpr uint32_t kABytes = kBM * kBK * 2;                // one CTA's weight rows of a k block
 constexpr uint32_t kBBytes = (kTile / 2) * kBK * 2;        // room for its half of the tokens
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint64_t kWaitNs = 1000000000ull;
 
@@ -143,31 +143,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
             const int half = t.n >> 1;   // this CTA's columns, a multiple of 16
             const int wrow = t.expert * p.wrows + t.f * 256 + static_cast<int>(rank) * kBM;
-            const int box = moe::row_box(half, lane);
-            const int brow = t.row0 + static_cast<int>(rank) * half + box;
+            const int brow = t.row0 + static_cast<int>(rank) * half;
             for (int ks = 0; ks < nst; ++ks) {
                 const bool got = ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (ptx::elect_one()) {
+                    const uint32_t bar = lead(full(s));
                     if (leader)
                         ptx::mbar_arrive_expect_tx(full(s), KSUB * (2 * RG::NMAT * kABytes + t.n * (kBK * 2)));
 #pragma unroll
                     for (int j = 0; j < KSUB; ++j) {
                         const int k0 = (ks * KSUB + j) * kBK;   // a block past K is zero fill
-                        ptx::tma_load_2d_pair(sA(s, j, 0), &map_w0, lead(full(s)), k0, wrow);
-                        if (MODE == GATEUP) ptx::tma_load_2d_pair(sA(s, j, 1), &map_w1, lead(full(s)), k0, wrow);
+                        ptx::tma_load_2d_pair(sA(s, j, 0), &map_w0, bar, k0, wrow);
+                        if (MODE == GATEUP) ptx::tma_load_2d_pair(sA(s, j, 1), &map_w1, bar, k0, wrow);
+                        moe::for_row_boxes(maps_b, half, [&](const CUtensorMap *m, int r) {
+                            ptx::tma_load_2d_pair(sB(s, j) + r * 128, m, bar, k0, brow + r);
+                        });
                     }
                 }
                 __syncwarp();
-                if (box >= 0) {
-#pragma unroll
-                    for (int j = 0; j < KSUB; ++j)
-                        ptx::tma_load_2d_pair(sB(s, j) + box * 128, &maps_b.m[lane], lead(full(s)),
-                                              (ks * KSUB + j) * kBK, brow);
-                }
                 ++produced;
                 if (++s == STAGES) {
                     s = 0;
@@ -179,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(p.err, DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // -------------------------------------------------------- MMA issuer
         bool ok = true;
         int s = 0, acc = 0;
@@ -196,52 +193,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nb = tile_b(u + ustep);
             }
             const uint32_t idesc = ptx::idesc_f16(256, t.n, BF16);
-            if (!ptx::mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, kWaitNs)) {
+            bool got = ptx::mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
             const uint32_t d0 = tmem + acc * 256;
             for (int ks = 0; ks < nst; ++ks) {
-                if (!ptx::mbar_wait(full(s), ph, abort_flag, kWaitNs)) {
+                got = ptx::mbar_wait(full(s), ph, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
+                if (ptx::elect_one()) {
 #pragma unroll
-                for (int j = 0; j < KSUB; ++j) {
-                    const uint64_t bd = ptx::sdesc_k_sw128(sB(s, j));
+                    for (int j = 0; j < KSUB; ++j) {
+                        const uint64_t bd = ptx::sdesc_k_sw128(sB(s, j));
 #pragma unroll
-                    for (int m = 0; m < RG::NMAT; ++m) {
-                        const uint64_t ad = ptx::sdesc_k_sw128(sA(s, j, m));
+                        for (int m = 0; m < RG::NMAT; ++m) {
+                            const uint64_t ad = ptx::sdesc_k_sw128(sA(s, j, m));
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)   // 32 bytes of k further: 2 in the address field
-                            ptx::tc_mma_f16_pair(d0 + m * up_off, ad + 2 * k, bd + 2 * k, idesc, (ks | j | k) != 0);
+                            for (int k = 0; k < kBK / 16; ++k)   // 32 bytes of k further: 2 in the address field
+                                ptx::tc_mma_f16_pair(d0 + m * up_off, ad + 2 * k, bd + 2 * k, idesc, (ks | j | k) != 0);
+                        }
                     }
+                    ptx::tc_commit_pair(empty(s), 0x3);
+                    if (ks == nst - 1) ptx::tc_commit_pair(tfull(acc), 0x3);
                 }
-                ptx::tc_commit_pair(empty(s), 0x3);
+                __syncwarp();
                 if (++s == STAGES) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) break;
-            ptx::tc_commit_pair(tfull(acc), 0x3);
             if (!two || ++acc == 2) {
                 acc = 0;
                 acc_ph ^= 1u;
             }
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
             atomicOr(p.err, DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        ptx::tc_commit_pair(ptx::smem_u32(&bar_drain), 0x1);   // every MMA ends before TMEM is freed
+        if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&bar_drain), 0x1);   // every MMA ends before TMEM is freed
         ptx::mbar_wait(ptx::smem_u32(&bar_drain), 0, never, kWaitNs);
     } else if (warp >= 2) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3;                 // this warp may read TMEM lanes 32q .. 32q+31
-        const int part = (warp - 2) >> 2;       // which 16-column chunks of every 32
+        const int part = (warp - 2) >> 2;       // which of every four 16-column chunks
         bool ok = true;
         int acc = 0;
         uint32_t acc_ph = 0;
@@ -257,19 +259,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = f < p.wrows;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
             const int64_t at = static_cast<int64_t>(t.row0) * p.wrows + f;
-            for (int c = part * 16; c < t.n; c += 32) {
+            for (int c = part * 16; c < t.n; c += 16 * (kEpiWarps / 4)) {
                 if constexpr (MODE == GATEUP) {
                     uint32_t rg[16], ru[16];
                     ptx::tmem_ld_32x32b_x16(taddr + c, rg);
                     ptx::tmem_ld_32x32b_x16(taddr + up_off + c, ru);
                     ptx::tmem_ld_wait();
                     T *dst = static_cast<T *>(p.out) + at + static_cast<int64_t>(c) * p.wrows;
+                    // h feeds the next product: one rounding to its operand type
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        // h feeds the next product: one rounding to its operand type
-                        const float hv = silu_f32(__uint_as_float(rg[i]) * p.acc_scale) *
-                                         (__uint_as_float(ru[i]) * p.acc_scale) * p.out_scale;
-                        if (live && c + i < t.valid) dst[static_cast<int64_t>(i) * p.wrows] = from_f32<T>(hv);
+                        const T hv = from_f32<T>(moe::swiglu(__uint_as_float(rg[i]) * p.acc_scale,
+                                                             __uint_as_float(ru[i]), p.acc_scale * p.out_scale));
+                        if (live && c + i < t.valid) *dst = hv;
+                        dst += p.wrows;
                     }
                 } else {
                     uint32_t r[16];

@@ -9,14 +9,16 @@
 // weights on the M side as in moe_gemm.cu.  The weights travel HBM -> shared
 // memory as 4 bits (TMA, 64 bytes of a row per 128 values; their scales, whose
 // row pitch need not be a multiple of 16 bytes, by 8-byte cp.async), from
-// there through registers, where eight warps turn them into fp16, into tensor
+// there through registers, where they become fp16, into tensor
 // memory (tcgen05.st), and tcgen05.mma takes its A operand from there.  Through
 // shared memory the fp16 form would cost 4 bytes a weight (stored and read
 // back) beside the 0.6 of the 4-bit form; so it costs none.
 //
-// What bounds it: few tokens: HBM, if the eight warps keep up -- per 128
-// values of 128 rows (9 KB, 430 cycles of this SM's share of HBM) each issues
-// about 140 instructions, two warps to a scheduler; more tokens: the
+// What bounds it: few tokens: HBM, if the dequantisation keeps up -- per 128
+// values of 128 rows (9 KB, 430 cycles of this SM's share of HBM) eight warps issue
+// about 140 instructions each, two to a scheduler, but one after the other
+// the wait, the loads, the arithmetic and the store take three times that:
+// two groups of eight warps take stages in turn; more tokens: the
 // activations from L2 (32 KB a stage at 128 columns), then the tensor pipe.
 //
 // Arithmetic: a nibble pair becomes fp16 1024 + u (or 1024 + 16 u, the high
@@ -27,8 +29,8 @@
 // the plan writes x and the gate/up epilogue writes h in that order.
 //
 // Roles: warp 0 loads nibbles, warp 3 scales, warp 2 tokens; warp 1 issues the
-// MMAs; warps 4-11 dequantise (warp w fills TMEM lanes 32 (w % 4) .. and one
-// 64-value half of the stage); warps 12-15 are the epilogue.  Every wait is
+// MMAs; warps 4-19 dequantise (warp w fills TMEM lanes 32 (w % 4) .. and one
+// 64-value half of every second stage); warps 20-23 are the epilogue.  Every wait is
 // bounded (1 s) as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
@@ -52,8 +54,9 @@ constexpr size_t kSmemBytes = kScaleOff + kRawStages * kScaleBytes + 1024;
 static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
               "one CTA per SM (each allocates all of tensor memory), beside 8 KB of static shared memory");
 constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
-constexpr int kDequantWarps = 8, kEpiWarps = 4;
-constexpr int kThreads = 32 * (4 + kDequantWarps + kEpiWarps);
+constexpr int kDequantWarps = 8, kGroups = 2, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
+constexpr int kThreads = 32 * (4 + kGroups * kDequantWarps + kEpiWarps);
+static_assert(kRawStages % kGroups == 0 && kAStages % kGroups == 0, "a group keeps its slots");
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
@@ -191,27 +194,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // -------------------------------------------------- nibbles
-            int s = 0;
-            uint32_t ph = 0;
-            for (int u = u0; u < units && ok; u += ustep) {
-                const Unit t = unit_at(u);
-                const int wrow = t.expert * p.wrows + t.f * kFRows;
-                for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
-                    if (!ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
+        // ------------------------------------------------------ nibbles
+        int s = 0;
+        uint32_t ph = 0;
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = unit_at(u);
+            const int wrow = t.expert * p.wrows + t.f * kFRows;
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+                const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                if (ptx::elect_one()) {
                     const uint32_t full = bar(&bar_rfull[s]), dst = base + kRawOff + s * kRawBytes;
                     ptx::mbar_arrive_expect_tx(full, kRawBytes);
                     ptx::tma_load_2d(dst, &map_w0, full, g * 64, wrow);
                     if (MODE == GATEUP) ptx::tma_load_2d(dst + kRawBytes / 2, &map_w1, full, g * 64, wrow);
-                    ++produced;
-                    if (++s == kRawStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                }
+                __syncwarp();
+                ++produced;
+                if (++s == kRawStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
@@ -251,22 +256,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = unit_at(u);
-            const int box = moe::row_box(t.n, lane);
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_bempty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = bar(&bar_bfull[s]);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
-                __syncwarp();
-                if (box >= 0) {
+                if (ptx::elect_one()) {
+                    const uint32_t full = bar(&bar_bfull[s]);
+                    ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)   // 64 values each; past the row's end zero fill
-                        ptx::tma_load_2d(base + s * kBBytes + j * (kBBytes / 2) + box * 128, &maps_b.m[lane], full,
-                                         g * kK + j * 64, t.row0 + box);
+                        moe::for_row_boxes(maps_b, t.n, [&](const CUtensorMap *m, int r) {
+                            ptx::tma_load_2d(base + s * kBBytes + j * (kBBytes / 2) + r * 128, m, full, g * kK + j * 64,
+                                             t.row0 + r);
+                        });
                 }
+                __syncwarp();
                 ++produced;
                 if (++s == kBStages) {
                     s = 0;
@@ -275,69 +281,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // -------------------------------------------------- MMA issuer
-            int sa = 0, sb = 0, acc = 0;
-            uint32_t pa = 0, pb = 0, pacc = 0;
-            int4 na = make_int4(0, 0, 1, 0), nb = na;
-            auto fetch = [&](int v) {
-                na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
-                nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
-            };
-            if (u0 < units) fetch(u0);
-            for (int u = u0; u < units && ok; u += ustep) {
-                const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
-                if (u + ustep < units) fetch(u + ustep);
-                const uint32_t idesc = ptx::idesc_f16(128, t.n, false);
-                if (!ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs)) {
+        // -------------------------------------------------- MMA issuer
+        int sa = 0, sb = 0, acc = 0;
+        uint32_t pa = 0, pb = 0, pacc = 0;
+        int4 na = make_int4(0, 0, 1, 0), nb = na;
+        auto fetch = [&](int v) {
+            na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
+            nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
+        };
+        if (u0 < units) fetch(u0);
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
+            if (u + ustep < units) fetch(u + ustep);
+            const uint32_t idesc = ptx::idesc_f16(128, t.n, false);
+            bool got = ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            const uint32_t d = tmem + acc * 128;
+            const int g0 = lo_of(u);
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+                got = ptx::mbar_wait(bar(&bar_bfull[sb]), pb, abort_flag, kWaitNs) &&
+                      ptx::mbar_wait(bar(&bar_afull[sa]), pa, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t d = tmem + acc * 128;
-                const int g0 = lo_of(u);
-                for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
-                    if (!ptx::mbar_wait(bar(&bar_bfull[sb]), pb, abort_flag, kWaitNs) ||
-                        !ptx::mbar_wait(bar(&bar_afull[sa]), pa, abort_flag, kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
                     const uint32_t a = tmem + kACol + sa * kAColsPerStage;
+                    const uint64_t bd = ptx::sdesc_k_sw128(base + sb * kBBytes);
 #pragma unroll
-                    for (int k = 0; k < kK / 16; ++k) {
-                        const uint64_t bd = ptx::sdesc_k_sw128(base + sb * kBBytes + (k >> 2) * (kBBytes / 2)) + 2 * (k & 3);
-                        mma_ts(d, a + 8 * k, bd, idesc, g != g0 || k != 0);
-                    }
+                    for (int k = 0; k < kK / 16; ++k)   // 32 bytes of k further: 2 in the address field
+                        mma_ts(d, a + 8 * k, bd + (k >> 2) * (kBBytes / 32) + 2 * (k & 3), idesc, g != g0 || k != 0);
                     ptx::tc_commit(bar(&bar_bempty[sb]));
                     ptx::tc_commit(bar(&bar_aempty[sa]));
-                    if (++sb == kBStages) {
-                        sb = 0;
-                        pb ^= 1u;
-                    }
-                    if (++sa == kAStages) {
-                        sa = 0;
-                        pa ^= 1u;
-                    }
+                    if (g == ge - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
                 }
-                if (!ok) break;
-                ptx::tc_commit(bar(&bar_tfull[acc]));
-                if (++acc == 2) {
-                    acc = 0;
-                    pacc ^= 1u;
+                __syncwarp();
+                if (++sb == kBStages) {
+                    sb = 0;
+                    pb ^= 1u;
+                }
+                if (++sa == kAStages) {
+                    sa = 0;
+                    pa ^= 1u;
                 }
             }
-            ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
-            ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
+            if (!ok) break;
+            if (++acc == 2) {
+                acc = 0;
+                pacc ^= 1u;
+            }
         }
-    } else if (warp < 4 + kDequantWarps) {
+        if (ptx::elect_one()) ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
+        ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
+    } else if (warp < 4 + kGroups * kDequantWarps) {
         // ------------------------------------------------------ dequantisation
-        const int q = warp & 3, hv = (warp - 4) >> 2;   // rows 32q .. 32q + 31; values 64 hv .. 64 hv + 63
+        // rows 32q .. 32q + 31; values 64 hv .. 64 hv + 63; every kGroups-th stage
+        const int q = warp & 3, hv = ((warp - 4) >> 2) & 1, group = (warp - 4) / kDequantWarps;
         const int row = 32 * q + lane;
         const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
-        int s = 0, sa = 0;
+        int s = group, sa = group, turn = 0;
         uint32_t ph = 0, pa = 0;
         for (int u = u0; u < units && ok; u += ustep) {
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+                const bool my_turn = turn == group;
+                if (++turn == kGroups) turn = 0;
+                if (!my_turn) continue;
                 bool got = ptx::mbar_wait(bar(&bar_rfull[s]), ph, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -371,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(&bar_rempty[s]));
-                if (++s == kRawStages) {
-                    s = 0;
+                if ((s += kGroups) >= kRawStages) {
+                    s = group;
                     ph ^= 1u;
                 }
                 got = ptx::mbar_wait(bar(&bar_aempty[sa]), pa ^ 1u, abort_flag, kWaitNs);
@@ -386,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(&bar_afull[sa]));
-                if (++sa == kAStages) {
-                    sa = 0;
+                if ((sa += kGroups) >= kAStages) {
+                    sa = group;
                     pa ^= 1u;
                 }
             }
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (!ok && (lane == 0 || warp >= 2)) {
+    if (!ok) {
         if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
         *abort_flag = 1;
     }

@@ -13,8 +13,7 @@
 // fills the last wave (moe_down_splits).  Four stages of 128 values keep 128
 // KB of weights in flight per SM.
 //
-// Roles: warp 0 loads (lane 0 weights, lanes 0-3 a box of tokens each), warp 1
-// issues the MMAs, warps 4-7 are the epilogue.  Every wait is bounded (1 s) as
+// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-7 are the epilogue.  Every wait is bounded (1 s) as
 // in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
@@ -119,7 +118,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = unit_at(u);
             const int wrow = t.expert * p.wrows + t.f * kFRows;
-            const int box = moe::row_box(t.n, lane);
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -127,22 +125,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t full = bar(&bar_full[s]), st = base + s * kStageBytes;
-                if (lane == 0) {
+                if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(full, 2 * (kABytes + t.n * 128));
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {   // 64 values each; past the row's end zero fill
                         const int k0 = g * kK + j * 64;
-                        ptx::tma_load_2d(st + j * kSubBytes, &map_w0, full, k0, wrow);
-                        if (MODE == GATEUP) ptx::tma_load_2d(st + j * kSubBytes + kABytes / 2, &map_w1, full, k0, wrow);
+                        const uint32_t at = st + j * kSubBytes;
+                        ptx::tma_load_2d(at, &map_w0, full, k0, wrow);
+                        if (MODE == GATEUP) ptx::tma_load_2d(at + kABytes / 2, &map_w1, full, k0, wrow);
+                        moe::for_row_boxes(maps_b, t.n, [&](const CUtensorMap *m, int r) {
+                            ptx::tma_load_2d(at + kABytes + r * 128, m, full, k0, t.row0 + r);
+                        });
                     }
                 }
                 __syncwarp();
-                if (box >= 0) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        ptx::tma_load_2d(st + j * kSubBytes + kABytes + box * 128, &maps_b.m[lane], full,
-                                         g * kK + j * 64, t.row0 + box);
-                }
                 ++produced;
                 if (++s == kStages) {
                     s = 0;
@@ -151,33 +147,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // -------------------------------------------------- MMA issuer
-            int s = 0, acc = 0;
-            uint32_t ph = 0, pacc = 0;
-            int4 na = make_int4(0, 0, 1, 0), nb = na;
-            auto fetch = [&](int v) {
-                na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
-                nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
-            };
-            if (u0 < units) fetch(u0);
-            for (int u = u0; u < units && ok; u += ustep) {
-                const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
-                if (u + ustep < units) fetch(u + ustep);
-                const uint32_t idesc = ptx::idesc_f16(128, t.n, BF16);
-                if (!ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs)) {
+        // -------------------------------------------------- MMA issuer
+        int s = 0, acc = 0;
+        uint32_t ph = 0, pacc = 0;
+        int4 na = make_int4(0, 0, 1, 0), nb = na;
+        auto fetch = [&](int v) {
+            na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
+            nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
+        };
+        if (u0 < units) fetch(u0);
+        for (int u = u0; u < units && ok; u += ustep) {
+            const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
+            if (u + ustep < units) fetch(u + ustep);
+            const uint32_t idesc = ptx::idesc_f16(128, t.n, BF16);
+            bool got = ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + acc * kTile;
+            const int g0 = lo_of(u);
+            for (int g = g0, ge = hi_of(u); g < ge; ++g) {
+                got = ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t d = tmem + acc * kTile;
-                const int g0 = lo_of(u);
-                for (int g = g0, ge = hi_of(u); g < ge; ++g) {
-                    if (!ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
+                if (ptx::elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t at = base + s * kStageBytes + j * kSubBytes;
@@ -187,21 +185,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::tc_mma_f16(d, ad + 2 * k, bd + 2 * k, idesc, (g - g0) | j | k);
                     }
                     ptx::tc_commit(bar(&bar_empty[s]));
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    if (g == ge - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
                 }
-                if (!ok) break;
-                ptx::tc_commit(bar(&bar_tfull[acc]));
-                if (++acc == 2) {
-                    acc = 0;
-                    pacc ^= 1u;
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
-            ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
+            if (!ok) break;
+            if (++acc == 2) {
+                acc = 0;
+                pacc ^= 1u;
+            }
         }
+        if (ptx::elect_one()) ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
+        ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
     } else if (warp >= 4) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3;
