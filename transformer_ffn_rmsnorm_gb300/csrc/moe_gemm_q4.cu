@@ -7,19 +7,19 @@
 // A unit of work is 128 weight rows (gate/up: 64 rows of W_gate and the same
 // 64 of W_up) of one expert against one token tile of n <= 128 columns, the
 // weights on the M side as in moe_gemm.cu.  The weights travel HBM -> shared
-// memory as 4 bits (TMA, 64 bytes of a row per 128 values; their scales, whose
-// row pitch need not be a multiple of 16 bytes, by 8-byte cp.async), from
+// memory as 4 bits (TMA, 128 bytes of a row, the values of two stages; their scales, whose
+// row pitch need not be a multiple of 16 bytes, by cp.async), from
 // there through registers, where they become fp16, into tensor
 // memory (tcgen05.st), and tcgen05.mma takes its A operand from there.  Through
 // shared memory the fp16 form would cost 4 bytes a weight (stored and read
 // back) beside the 0.6 of the 4-bit form; so it costs none.
 //
-// What bounds it: few tokens: HBM, if the dequantisation keeps up -- per 128
-// values of 128 rows (9 KB, 430 cycles of this SM's share of HBM) eight warps issue
-// about 140 instructions each, two to a scheduler, but one after the other
-// the wait, the loads, the arithmetic and the store take three times that:
-// two groups of eight warps take stages in turn; more tokens: the
-// activations from L2 (32 KB a stage at 128 columns), then the tensor pipe.
+// What bounds it: few tokens: HBM, if the dequantisation keeps up.  A stage (128 rows of 128
+// values, 9 KB) is 430 cycles of this SM's share of HBM; its dequantisation is four
+// warps of about 260 instructions, and the wait, the loads, the arithmetic and
+// the store of one warp follow one another, so three groups of four warps
+// take stages in turn, one of each group to a scheduler.  More tokens: the activations from L2 (32 KB a
+// stage at 128 columns), then the tensor pipe.
 //
 // Arithmetic: a nibble pair becomes fp16 1024 + u (or 1024 + 16 u, the high
 // nibbles where they stand), u - 8 exactly by one subtraction (one fma), and
@@ -29,8 +29,8 @@
 // the plan writes x and the gate/up epilogue writes h in that order.
 //
 // Roles: warp 0 loads nibbles, warp 3 scales, warp 2 tokens; warp 1 issues the
-// MMAs; warps 4-19 dequantise (warp w fills TMEM lanes 32 (w % 4) .. and one
-// 64-value half of every second stage); warps 20-23 are the epilogue.  Every wait is
+// MMAs; warps 4-15 dequantise (warp w fills TMEM lanes 32 (w % 4) .. of every
+// third stage); warps 16-19 are the epilogue.  Every wait is
 // bounded (1 s) as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
@@ -45,18 +45,17 @@ using moe::Plan;
 using moe::Unit;
 
 constexpr int kRows = 128, kK = 128, kTile = kMoeCutQ4.tile, kGran = kMoeCutQ4.gran;
-constexpr uint32_t kRawBytes = kRows * 64, kScaleBytes = kRows * 8;   // a stage's nibbles and scales
-constexpr uint32_t kBBytes = kTile * kK * 2;                          // room for its tokens
-constexpr int kRawStages = 12, kBStages = 3, kAStages = 4;
-constexpr uint32_t kRawOff = kBStages * kBBytes;
+constexpr uint32_t kRawBytes = kRows * 128, kScaleBytes = kRows * 16;   // nibbles and scales of two stages' values
+constexpr uint32_t kBBytes = kTile * kK * 2;                            // room for a stage's tokens
+constexpr int kRawStages = 4, kStages = 4;   // a stage: A in tensor memory, tokens in shared memory, one barrier
+constexpr uint32_t kRawOff = kStages * kBBytes;
 constexpr uint32_t kScaleOff = kRawOff + kRawStages * kRawBytes;
 constexpr size_t kSmemBytes = kScaleOff + kRawStages * kScaleBytes + 1024;
 static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
               "one CTA per SM (each allocates all of tensor memory), beside 8 KB of static shared memory");
 constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
-constexpr int kDequantWarps = 8, kGroups = 2, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
+constexpr int kDequantWarps = 4, kGroups = 3, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
 constexpr int kThreads = 32 * (4 + kGroups * kDequantWarps + kEpiWarps);
-static_assert(kRawStages % kGroups == 0 && kAStages % kGroups == 0, "a group keeps its slots");
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
@@ -75,8 +74,8 @@ struct Params {
     unsigned *err;
 };
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 // arrives on bar once this thread's cp.async so far have landed (the barrier counts the arrival)
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -132,8 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;   // features of a unit
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_rfull[kRawStages], bar_rempty[kRawStages];
-    __shared__ __align__(8) uint64_t bar_bfull[kBStages], bar_bempty[kBStages];
-    __shared__ __align__(8) uint64_t bar_afull[kAStages], bar_aempty[kAStages];
+    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
     __shared__ float s_swap[MODE == GATEUP ? 2 : 1][2][8][64];
     __shared__ uint32_t s_tmem_base;
@@ -145,15 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRawStages; ++s) {
             ptx::mbar_init(bar(&bar_rfull[s]), 1 + 32);        // the nibbles' bytes, the scale warp's lanes
-            ptx::mbar_init(bar(&bar_rempty[s]), kDequantWarps);
+            ptx::mbar_init(bar(&bar_rempty[s]), 2 * kDequantWarps);   // of both halves
         }
-        for (int s = 0; s < kBStages; ++s) {
-            ptx::mbar_init(bar(&bar_bfull[s]), 1);
-            ptx::mbar_init(bar(&bar_bempty[s]), 1);
-        }
-        for (int s = 0; s < kAStages; ++s) {
-            ptx::mbar_init(bar(&bar_afull[s]), kDequantWarps);
-            ptx::mbar_init(bar(&bar_aempty[s]), 1);
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(bar(&bar_full[s]), 1 + kDequantWarps);   // the tokens' bytes, the weights' warps
+            ptx::mbar_init(bar(&bar_empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(bar(&bar_tfull[a]), 1);
@@ -183,10 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     ptx::griddep_wait();   // the plan, x, h: written by kernels before this one
-    // unit v is split v % splits of tile unit v / splits: stages [lo, hi)
+    // unit v is split v % splits of tile unit v / splits: raw slots [lo, hi) of
+    // two stages each, but for an odd row's last
     const int units = __ldcg(p.header) * p.nf * p.splits;
-    auto lo_of = [&](int v) { return p.ngrp * (v % p.splits) / p.splits; };
-    auto hi_of = [&](int v) { return p.ngrp * (v % p.splits + 1) / p.splits; };
+    const int nraw = (p.ngrp + 1) / 2;
+    auto lo_of = [&](int v) { return nraw * (v % p.splits) / p.splits; };
+    auto hi_of = [&](int v) { return nraw * (v % p.splits + 1) / p.splits; };
+    auto stages_of = [&](int v) { return min(2 * hi_of(v), p.ngrp) - 2 * lo_of(v); };
     auto unit_at = [&](int v) {
         const int u = v / p.splits;
         const int4 *t = p.tiles + 2 * (u / p.nf);
@@ -200,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = unit_at(u);
             const int wrow = t.expert * p.wrows + t.f * kFRows;
-            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+            for (int r = lo_of(u), re = hi_of(u); r < re; ++r) {
                 const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -209,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ptx::elect_one()) {
                     const uint32_t full = bar(&bar_rfull[s]), dst = base + kRawOff + s * kRawBytes;
                     ptx::mbar_arrive_expect_tx(full, kRawBytes);
-                    ptx::tma_load_2d(dst, &map_w0, full, g * 64, wrow);
-                    if (MODE == GATEUP) ptx::tma_load_2d(dst + kRawBytes / 2, &map_w1, full, g * 64, wrow);
+                    ptx::tma_load_2d(dst, &map_w0, full, r * 128, wrow);   // past the row's end zero fill
+                    if (MODE == GATEUP) ptx::tma_load_2d(dst + kRawBytes / 2, &map_w1, full, r * 128, wrow);
                 }
                 __syncwarp();
                 ++produced;
@@ -222,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------ scales
+        const bool wide = (p.ngrp & 1) == 0;   // rows of scales start on 16 bytes
         int s = 0;
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
@@ -233,15 +231,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint16_t *m = MODE == GATEUP && i >= 2 ? p.s1 : p.s0;
                 src[i] = m + (static_cast<int64_t>(t.expert) * p.wrows + min(f, p.wrows - 1)) * (4 * p.ngrp);
             }
-            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+            for (int r = lo_of(u), re = hi_of(u); r < re; ++r) {
                 const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = base + kScaleOff + s * kScaleBytes + lane * 8;
+                const uint32_t dst = base + kScaleOff + s * kScaleBytes + lane * 16;
+                const bool last = 2 * r + 1 == p.ngrp;   // one stage, and no more scales in the row
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cp_async8(dst + i * 256, src[i] + 4 * g);
+                for (int i = 0; i < 4; ++i) {
+                    if (wide) {
+                        cp_async<16>(dst + i * 512, src[i] + 8 * r);
+                    } else {
+                        cp_async<8>(dst + i * 512, src[i] + 8 * r);
+                        if (!last) cp_async<8>(dst + i * 512 + 8, src[i] + 8 * r + 4);
+                    }
+                }
                 cp_async_arrive(bar(&bar_rfull[s]));
                 if (++s == kRawStages) {
                     s = 0;
@@ -256,14 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = unit_at(u);
-            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
-                const bool got = ptx::mbar_wait(bar(&bar_bempty[s]), ph ^ 1u, abort_flag, kWaitNs);
+            for (int g = 2 * lo_of(u), ge = g + stages_of(u); g < ge; ++g) {
+                const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 if (ptx::elect_one()) {
-                    const uint32_t full = bar(&bar_bfull[s]);
+                    const uint32_t full = bar(&bar_full[s]);
                     ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)   // 64 values each; past the row's end zero fill
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++produced;
-                if (++s == kBStages) {
+                if (++s == kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -282,8 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // -------------------------------------------------- MMA issuer
-        int sa = 0, sb = 0, acc = 0;
-        uint32_t pa = 0, pb = 0, pacc = 0;
+        // (the next stage's barrier is looked at before this stage's MMAs are
+        // issued: a wait that has nothing to wait for costs 100 cycles, as
+        // much as four of them)
+        int s = 0, acc = 0;
+        uint32_t ph = 0, pacc = 0;
+        bool ready = false;
         int4 na = make_int4(0, 0, 1, 0), nb = na;
         auto fetch = [&](int v) {
             na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
@@ -300,34 +310,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             const uint32_t d = tmem + acc * 128;
-            const int g0 = lo_of(u);
-            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
-                got = ptx::mbar_wait(bar(&bar_bfull[sb]), pb, abort_flag, kWaitNs) &&
-                      ptx::mbar_wait(bar(&bar_afull[sa]), pa, abort_flag, kWaitNs);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
+            const int n = stages_of(u);
+            for (int g = 0; g < n; ++g) {
+                if (!__all_sync(0xffffffffu, ready)) {
+                    got = ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, kWaitNs);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 ptx::tc_fence_after();
+                const int at = s;
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                ready = ptx::mbar_test(bar(&bar_full[s]), ph);
                 if (ptx::elect_one()) {
-                    const uint32_t a = tmem + kACol + sa * kAColsPerStage;
-                    const uint64_t bd = ptx::sdesc_k_sw128(base + sb * kBBytes);
+                    const uint32_t a = tmem + kACol + at * kAColsPerStage;
+                    const uint64_t bd = ptx::sdesc_k_sw128(base + at * kBBytes);
 #pragma unroll
                     for (int k = 0; k < kK / 16; ++k)   // 32 bytes of k further: 2 in the address field
-                        mma_ts(d, a + 8 * k, bd + (k >> 2) * (kBBytes / 32) + 2 * (k & 3), idesc, g != g0 || k != 0);
-                    ptx::tc_commit(bar(&bar_bempty[sb]));
-                    ptx::tc_commit(bar(&bar_aempty[sa]));
-                    if (g == ge - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
+                        mma_ts(d, a + 8 * k, bd + (k >> 2) * (kBBytes / 32) + 2 * (k & 3), idesc, (g | k) != 0);
+                    ptx::tc_commit(bar(&bar_empty[at]));
+                    if (g == n - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
                 }
                 __syncwarp();
-                if (++sb == kBStages) {
-                    sb = 0;
-                    pb ^= 1u;
-                }
-                if (++sa == kAStages) {
-                    sa = 0;
-                    pa ^= 1u;
-                }
             }
             if (!ok) break;
             if (++acc == 2) {
@@ -339,70 +347,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_wait(bar(&bar_drain), 0, never, kWaitNs);
     } else if (warp < 4 + kGroups * kDequantWarps) {
         // ------------------------------------------------------ dequantisation
-        // rows 32q .. 32q + 31; values 64 hv .. 64 hv + 63; every kGroups-th stage
-        const int q = warp & 3, hv = ((warp - 4) >> 2) & 1, group = (warp - 4) / kDequantWarps;
+        // this warp's rows are 32q .. 32q + 31; its group takes every kGroups-th stage
+        const int q = warp & 3, group = (warp - 4) / kDequantWarps;
         const int row = 32 * q + lane;
-        const uint32_t swz = static_cast<uint32_t>((row >> 1) & 3);
-        int s = group, sa = group, turn = 0;
-        uint32_t ph = 0, pa = 0;
+        const uint32_t a0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + kACol;
+        uint32_t raw0 = 0, stage0 = 0;   // raw slots and stages of the units before
+        uint32_t mine = group;           // this group's next stage
         for (int u = u0; u < units && ok; u += ustep) {
-            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
-                const bool my_turn = turn == group;
-                if (++turn == kGroups) turn = 0;
-                if (!my_turn) continue;
-                bool got = ptx::mbar_wait(bar(&bar_rfull[s]), ph, abort_flag, kWaitNs);
+            const int n = stages_of(u);
+            for (; mine < stage0 + n; mine += kGroups) {
+                const int i = static_cast<int>(mine - stage0);
+                const uint32_t raw = raw0 + (i >> 1), s = raw % kRawStages, slot = mine % kStages;
+                bool got = ptx::mbar_wait(bar(&bar_rfull[s]), (raw / kRawStages) & 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t src = base + kRawOff + s * kRawBytes + row * 64 + hv * 8;
-                uint2 w[4];   // this half's two blocks: words of canonical bytes 4t .. 4t + 3
+                const uint32_t src = base + kRawOff + s * kRawBytes + row * 128;
+                uint4 w[4];   // words of canonical bytes 4t .. 4t + 3 of the four blocks
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(w[t].x), "=r"(w[t].y)
-                                 : "r"(src + ((t ^ swz) << 4)));
-                uint32_t sc;
-                asm volatile("ld.shared.u32 %0, [%1];"
-                             : "=r"(sc)
-                             : "r"(base + kScaleOff + s * kScaleBytes + row * 8 + hv * 4));
-                uint32_t o[32];
-                const __half2 sp = *reinterpret_cast<const __half2 *>(&sc);
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[t].x), "=r"(w[t].y), "=r"(w[t].z), "=r"(w[t].w)
+                                 : "r"(src + (((4 * (i & 1) + t) ^ (row & 7)) << 4)));
+                uint32_t sc[2];
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(sc[0]), "=r"(sc[1])
+                             : "r"(base + kScaleOff + s * kScaleBytes + row * 16 + 8 * (i & 1)));
+                __syncwarp();
+                if (lane == 0) {   // everything is in registers; a slot with one stage is released for both
+                    ptx::mbar_arrive(bar(&bar_rempty[s]));
+                    if (i == n - 1 && (n & 1)) ptx::mbar_arrive(bar(&bar_rempty[s]));
+                }
+                // all of the arithmetic before the wait: a slot's way round (MMAs,
+                // release, store, MMAs) is what the products wait for otherwise
+                uint32_t o[2][32];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const __half2 s2 = b ? __high2half2(sp) : __low2half2(sp);
+                for (int blk = 0; blk < 4; ++blk) {
+                    const __half2 sp = *reinterpret_cast<const __half2 *>(&sc[blk >> 1]);
+                    const __half2 s2 = blk & 1 ? __high2half2(sp) : __low2half2(sp);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         uint32_t v[4];
-                        dequant_word(b ? w[t].y : w[t].x, s2, v);
-                        o[16 * b + 2 * t] = v[0];
-                        o[16 * b + 2 * t + 1] = v[1];
-                        o[16 * b + 8 + 2 * t] = v[2];
-                        o[16 * b + 8 + 2 * t + 1] = v[3];
+                        dequant_word(blk == 0 ? w[t].x : blk == 1 ? w[t].y : blk == 2 ? w[t].z : w[t].w, s2, v);
+                        uint32_t *to = &o[blk >> 1][16 * (blk & 1) + 2 * t];
+                        to[0] = v[0];
+                        to[1] = v[1];
+                        to[8] = v[2];
+                        to[9] = v[3];
                     }
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(&bar_rempty[s]));
-                if ((s += kGroups) >= kRawStages) {
-                    s = group;
-                    ph ^= 1u;
-                }
-                got = ptx::mbar_wait(bar(&bar_aempty[sa]), pa ^ 1u, abort_flag, kWaitNs);
+                got = ptx::mbar_wait(bar(&bar_empty[slot]), ((mine / kStages) & 1u) ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                tmem_st_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + kACol + sa * kAColsPerStage + 32 * hv, o);
+                tmem_st_x32(a0 + slot * kAColsPerStage, o[0]);
+                tmem_st_x32(a0 + slot * kAColsPerStage + 32, o[1]);
                 tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(&bar_afull[sa]));
-                if ((sa += kGroups) >= kAStages) {
-                    sa = group;
-                    pa ^= 1u;
-                }
+                if (lane == 0) ptx::mbar_arrive(bar(&bar_full[slot]));
             }
+            stage0 += n;
+            raw0 += hi_of(u) - lo_of(u);
         }
     } else {
         // ---------------------------------------------------------- epilogue
@@ -447,9 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_wait(bar(&bar_rfull[s]), ((produced - s + kRawStages - 1) / kRawStages - 1) & 1u, never,
                                kWaitNs);
     if (warp == 2 && lane == 0)
-        for (uint32_t s = 0; s < kBStages; ++s)
+        for (uint32_t s = 0; s < kStages; ++s)
             if (produced > s)
-                ptx::mbar_wait(bar(&bar_bfull[s]), ((produced - s + kBStages - 1) / kBStages - 1) & 1u, never, kWaitNs);
+                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + kStages - 1) / kStages - 1) & 1u, never, kWaitNs);
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
@@ -494,11 +503,11 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// nibbles: 64 bytes of box_rows rows, rows of whole 128-value groups
+// nibbles: 128 bytes of box_rows rows, rows of whole 128-value groups
 bool map_q4(CUtensorMap *m, const uint8_t *qs, int64_t K, int64_t rows, uint32_t box_rows) {
     const int64_t pitch = 64 * ((K + kK - 1) / kK);
-    return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 64, box_rows,
-                         CU_TENSOR_MAP_SWIZZLE_64B);
+    return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 128, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 bool map_rows(moe::RowMaps *m, const void *ptr, int64_t inner, int64_t rows) {
     for (int i = 0; i < 4; ++i)
