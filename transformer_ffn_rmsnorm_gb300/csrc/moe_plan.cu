@@ -105,9 +105,8 @@ struct PlanShared {
     int widest;
 };
 
-// From the experts' counts in sh.count: first tiles and first rows; with
-// `write` also the tables.  Returns the number of sorted rows.
-__device__ __forceinline__ int plan_tables(const PlanParams &p, PlanShared &sh, bool write) {
+// From the experts' counts in sh.count: first tiles, first rows, the tables.
+__device__ __forceinline__ void plan_tables(const PlanParams &p, PlanShared &sh) {
     const int c = sh.count[threadIdx.x];
     const int nt = (c + p.cut.tile - 1) / p.cut.tile;
     int row0 = c, first = nt, total, ntiles;
@@ -117,82 +116,104 @@ __device__ __forceinline__ int plan_tables(const PlanParams &p, PlanShared &sh, 
     auto width = [&](int rows, int tiles) {
         return ((rows + tiles - 1) / tiles + p.cut.gran - 1) / p.cut.gran * p.cut.gran;
     };
-    if (write && nt) atomicMax(&sh.widest, width(c, nt));
+    if (nt) atomicMax(&sh.widest, width(c, nt));
     __syncthreads();
-    if (write) {
-        if (threadIdx.x == 0) {
-            p.plan.header[0] = ntiles;
-            p.plan.header[1] = sh.widest;
-            p.plan.header[2] = total;
-        }
-        for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
-            // the last expert whose first tile is at or before q (one without
-            // tiles shares its first with the next one)
-            int lo = 0, hi = p.experts - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (sh.first[mid] <= q) lo = mid;
-                else hi = mid - 1;
-            }
-            Tile t;
-            t.expert = lo;
-            t.first = sh.first[lo];
-            t.rows = sh.count[lo];
-            t.count = (t.rows + p.cut.tile - 1) / p.cut.tile;
-            t.cols = width(t.rows, t.count);
-            t.row0 = sh.row0[lo];
-            t.pad0 = t.pad1 = 0;
-            p.plan.tiles[q] = t;
-        }
+    if (threadIdx.x == 0) {
+        p.plan.header[0] = ntiles;
+        p.plan.header[1] = sh.widest;
+        p.plan.header[2] = total;
     }
-    return total;
+    for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
+        // the last expert whose first tile is at or before q (one without
+        // tiles shares its first with the next one)
+        int lo = 0, hi = p.experts - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sh.first[mid] <= q) lo = mid;
+            else hi = mid - 1;
+        }
+        Tile t;
+        t.expert = lo;
+        t.first = sh.first[lo];
+        t.rows = sh.count[lo];
+        t.count = (t.rows + p.cut.tile - 1) / p.cut.tile;
+        t.cols = width(t.rows, t.count);
+        t.row0 = sh.row0[lo];
+        t.pad0 = t.pad1 = 0;
+        p.plan.tiles[q] = t;
+    }
 }
 
-// Few pairs: every CTA sorts them for itself (a row's place is the number of
-// equal experts before it, so all CTAs agree) and copies its share of the
-// rows; the first one writes the tables.
+// Few pairs: every CTA sorts them for itself, by counting for each pair the
+// pairs before it in sorted order (no scan: two barriers in all), and copies
+// its piece of one sorted row; the first CTA writes the tables.
 template <typename T>
-__global__ void __launch_bounds__(kPlanThreads) moe_plan_small_kernel(const PlanParams p) {
-    __shared__ PlanShared sh;
-    __shared__ __align__(16) int s_e[kSmallPairs];
-    __shared__ int s_token[kSmallPairs];
+__global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanParams p) {
+    __shared__ __align__(16) int s_e[kSmallPairs], s_lead[kSmallPairs], s_tiles[kSmallPairs];
+    __shared__ int s_token, s_ntiles, s_widest;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int i = threadIdx.x;
+    const int i = threadIdx.x, r = blockIdx.y;
     int e = i < p.pairs ? p.idx[i] : -1;
-    if (e >= p.experts) e = -1;
-    sh.count[i] = 0;
-    if (i < kSmallPairs) s_e[i] = e;
-    if (i == 0) sh.widest = 0;
+    if (e < 0 || e >= p.experts) e = -1;
+    s_e[i] = e;
+    if (i == 0) s_token = -1;
+    if (i == 0) s_ntiles = s_widest = 0;
     __syncthreads();
-    int rank = 0;
+    int at = -1, rank = 0, count = 0;
     if (e >= 0) {
-        atomicAdd(&sh.count[e], 1);
         const int4 *v = reinterpret_cast<const int4 *>(s_e);
-        for (int j = 0; 4 * j < i; ++j) {
+        int less = 0;
+        for (int j = 0; 4 * j < p.pairs; ++j) {
             const int4 o = v[j];
-            rank += (o.x == e) + (o.y == e && 4 * j + 1 < i) + (o.z == e && 4 * j + 2 < i) + (o.w == e && 4 * j + 3 < i);
+            const int all[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                less += all[q] >= 0 && all[q] < e;
+                count += all[q] == e;
+                rank += all[q] == e && 4 * j + q < i;
+            }
         }
+        at = less + rank;
+        if (at == r) s_token = i / p.k;
     }
-    __syncthreads();
-    const int total = plan_tables(p, sh, blockIdx.x == 0);
-    if (i < p.pairs) {
-        const int at = e >= 0 ? sh.row0[e] + rank : -1;
-        if (e >= 0) s_token[at] = i / p.k;
-        if (blockIdx.x == 0) {
-            p.plan.pos[i] = at;
-            if (e >= 0) p.plan.row_token[at] = i / p.k;
+    if (blockIdx.x == 0 && r == 0) {
+        const bool lead = e >= 0 && rank == 0;   // the expert's first pair
+        const int nt = lead ? (count + p.cut.tile - 1) / p.cut.tile : 0;
+        s_lead[i] = lead ? e : 0x7fffffff;
+        s_tiles[i] = nt;
+        const int total = __syncthreads_count(e >= 0);
+        if (lead) {
+            int first = 0;
+            for (int j = 0; j < p.pairs; ++j) first += s_lead[j] < e ? s_tiles[j] : 0;
+            Tile t;
+            t.expert = e;
+            t.first = first;
+            t.rows = count;
+            t.count = nt;
+            t.cols = ((count + nt - 1) / nt + p.cut.gran - 1) / p.cut.gran * p.cut.gran;
+            t.row0 = at;
+            t.pad0 = t.pad1 = 0;
+            for (int q = 0; q < nt; ++q) p.plan.tiles[first + q] = t;
+            atomicMax(&s_ntiles, first + nt);
+            atomicMax(&s_widest, t.cols);
         }
+        if (i < p.pairs) p.plan.pos[i] = at;
+        __syncthreads();
+        if (i == 0) {
+            p.plan.header[0] = s_ntiles;
+            p.plan.header[1] = s_widest;
+            p.plan.header[2] = total;
+        }
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
-    const uint4 *src = static_cast<const uint4 *>(p.x);
-    uint4 *dst = static_cast<uint4 *>(p.xs);
+    if (s_token < 0) return;
+    const uint4 *src = static_cast<const uint4 *>(p.x) + static_cast<int64_t>(s_token) * p.nvec;
+    uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(r) * p.nvec;
     bool bad = false;
-    const int64_t n = static_cast<int64_t>(total) * p.nvec;
-    for (int64_t v = blockIdx.x * kPlanThreads + threadIdx.x; v < n; v += gridDim.x * kPlanThreads) {
-        const int r = static_cast<int>(v / p.nvec), c = static_cast<int>(v - static_cast<int64_t>(r) * p.nvec);
-        dst[v] = convert_vec<T>(p, src[static_cast<int64_t>(s_token[r]) * p.nvec + c], bad);
-    }
+    for (int c = blockIdx.x * kSmallPairs + i; c < p.nvec; c += gridDim.x * kSmallPairs)
+        dst[c] = convert_vec<T>(p, src[c], bad);
     if (bad) atomicOr(p.err, DEVERR_RANGE);
 }
 
@@ -235,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const PlanParams
         }
     }
     __syncthreads();
-    plan_tables(p, sh, true);
+    plan_tables(p, sh);
     for (int i0 = threadIdx.x; i0 < p.pairs; i0 += kBatch * kPlanThreads) {
         int e[kBatch], rank[kBatch];
 #pragma unroll
@@ -255,30 +276,21 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const PlanParams
     }
 }
 
-// The sorted copy of x's rows, after moe_plan_kernel.
+// The sorted copy of x's rows, after moe_plan_kernel: a row per CTA.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const PlanParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const uint4 *src = static_cast<const uint4 *>(p.x);
-    uint4 *dst = static_cast<uint4 *>(p.xs);
+    const int r = blockIdx.x;
+    if (r >= p.plan.header[2]) return;
+    const uint4 *src = static_cast<const uint4 *>(p.x) + static_cast<int64_t>(p.plan.row_token[r]) * p.nvec;
+    uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(r) * p.nvec;
     bool bad = false;
-    const int64_t n = static_cast<int64_t>(p.plan.header[2]) * p.nvec, step = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v0 < n; v0 += 4 * step) {
-        uint4 a[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = v0 + b * step;
-            if (v < n) {
-                const int64_t r = v / p.nvec, c = v - r * p.nvec;
-                a[b] = src[static_cast<int64_t>(p.plan.row_token[r]) * p.nvec + c];
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = v0 + b * step;
-            if (v < n) dst[v] = convert_vec<T>(p, a[b], bad);
-        }
+    for (int c0 = threadIdx.x; c0 < p.nvec; c0 += 2 * blockDim.x) {
+        const int c1 = c0 + blockDim.x;
+        const uint4 a = src[c0], b = c1 < p.nvec ? src[c1] : make_uint4(0, 0, 0, 0);
+        dst[c0] = convert_vec<T>(p, a, bad);
+        if (c1 < p.nvec) dst[c1] = convert_vec<T>(p, b, bad);
     }
     if (bad) atomicOr(p.err, DEVERR_RANGE);
 }
@@ -288,7 +300,7 @@ struct CombineParams {
     const float *w, *part;
     const void *res;
     void *y;
-    int64_t rows, nvec;   // nvec: 8-element vectors of a row
+    int64_t nvec;         // 8-element vectors of a row
     int64_t split_stride; // floats from one split of part to the next
     int k, splits;
 };
@@ -297,10 +309,9 @@ template <typename T>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t n = p.rows * p.nvec;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = i / p.nvec, c = i - t * p.nvec;
+    const int64_t t = blockIdx.x;
+    for (int64_t c = blockIdx.y * blockDim.x + threadIdx.x; c < p.nvec; c += gridDim.y * blockDim.x) {
+        const int64_t i = t * p.nvec + c;
         float f[8];
         if (p.res) {
             Vec16<T>::unpack(__ldcs(static_cast<const uint4 *>(p.res) + i), f);
@@ -367,13 +378,13 @@ namespace {
 
 template <typename T>
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s) {
-    const int64_t vecs = static_cast<int64_t>(p.pairs) * p.nvec;
     cudaError_t e;
     if (p.pairs <= kSmallPairs) {
-        // four vectors a thread, at most one CTA a multiprocessor
-        const int64_t grid = std::min<int64_t>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), sm_count());
+        // two vectors a thread
+        const dim3 grid(static_cast<unsigned>((p.nvec + 2 * kSmallPairs - 1) / (2 * kSmallPairs)),
+                        static_cast<unsigned>(p.pairs));
         LaunchScope scope(K_MOE_PLAN, s);
-        e = launch_dependent(moe_plan_small_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, s, p);
+        e = launch_dependent(moe_plan_small_kernel<T>, grid, dim3(kSmallPairs), 0, s, p);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     {
@@ -381,9 +392,9 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t s) {
         e = launch_dependent(moe_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
     }
     if (e != cudaSuccess) return e;
-    const int64_t grid = std::min<int64_t>((vecs + 1023) / 1024, 16 * static_cast<int64_t>(sm_count()));
+    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(256, (p.nvec + 31) / 32 * 32));
     LaunchScope scope(K_MOE_PLAN, s);
-    e = launch_dependent(moe_gather_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    e = launch_dependent(moe_gather_kernel<T>, dim3(static_cast<unsigned>(p.pairs)), dim3(threads), 0, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -410,14 +421,14 @@ cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts
 
 cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *part, int splits, const void *res,
                                void *y, int64_t rows, int k, int64_t d, int dt, cudaStream_t s) {
-    CombineParams p{plan.pos, w, part, res, y, rows, d / 8, rows * k * d, k, splits};
-    const int64_t blocks = std::min<int64_t>((rows * p.nvec + 255) / 256, 32 * static_cast<int64_t>(sm_count()));
+    CombineParams p{plan.pos, w, part, res, y, d / 8, rows * k * d, k, splits};
+    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(256, (p.nvec + 31) / 32 * 32));
+    const dim3 grid(static_cast<unsigned>(rows),
+                    static_cast<unsigned>(std::min<int64_t>((p.nvec + threads - 1) / threads, 65535)));
     LaunchScope scope(K_MOE_COMBINE, s);
     const cudaError_t e =
-        dt == DT_BF16 ? launch_dependent(moe_combine_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(blocks)),
-                                         dim3(256), 0, s, p)
-                      : launch_dependent(moe_combine_kernel<__half>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                                         s, p);
+        dt == DT_BF16 ? launch_dependent(moe_combine_kernel<__nv_bfloat16>, grid, dim3(threads), 0, s, p)
+                      : launch_dependent(moe_combine_kernel<__half>, grid, dim3(threads), 0, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

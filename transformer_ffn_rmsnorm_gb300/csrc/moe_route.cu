@@ -6,9 +6,10 @@
 //   idx = the k largest order_e, descending;  w_j = s_(idx_j) [/ sum_j] * scale
 // Ties go to the lower index.  A logit of -inf or NaN is never chosen.
 //
-// One warp per token: lane l holds experts l, l + 32, ... in registers and
-// the k largest come out one by one (a scan of the lane's registers, a warp
-// maximum, a warp minimum over the indices that have it).
+// One warp per token: lane l holds experts l, l + 32, ... in registers,
+// sorted (up to 8 of them; more are scanned each time), and the k largest
+// come out one by one: a warp maximum over the lanes' largest, a warp minimum
+// over the indices that have it.  Bound by the instructions a token takes.
 //
 // The chosen set is that of the formula in 64 bits although the scores are
 // computed in 32.  Without a bias nothing has to be computed: the order is
@@ -18,11 +19,11 @@
 // candidates computed in 64 bits and compared again.  (FP64 runs at a small
 // fraction of the FP32 rate on this GPU: a 64-bit exponential for every
 // score would be most of the kernel.)  Groups are decided the same way.
-//   DELTA, in units of 2^-24 of s <= 1: sigmoid: expf 2, its sum with 1 and
-//   the division 1 each: 4, taken as 8.  softmax: l - max rounds by |l - max|
+//   DELTA, in units of 2^-24 of s <= 1 (the approximate division is within 2 ulp, 4 units): sigmoid: expf 2, its sum with 1 one, the
+//   division 4: 7, taken as 8.  softmax: l - max rounds by |l - max|
 //   2^-24, which moves exp(l - max) by at most 1 (x e^-x < 1), expf 2; the
 //   denominator adds terms with those errors over at most 10 levels (a
-//   lane's 32 in pairs, then 32 lanes): 13; the division 1: 17, taken as 32.
+//   lane's 32 in pairs, then 32 lanes): 13; the division 4: 20, taken as 32.
 #include "ffn_internal.cuh"
 
 namespace ffn {
@@ -56,9 +57,9 @@ __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_m
 
 // NaN counts as -inf (never chosen), +inf as the largest finite value
 __device__ __forceinline__ float clean_logit(float l) {
-    return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+    return fminf(fmaxf(l, -INFINITY), 3.402823466e38f);   // (fmaxf gives the other operand for NaN)
 }
-__device__ __forceinline__ float clean_bias(float b) { return b != b ? -1e30f : fminf(fmaxf(b, -1e30f), 1e30f); }
+__device__ __forceinline__ float clean_bias(float b) { return fminf(fmaxf(b, -1e30f), 1e30f); }
 
 // a token's scores in 64 bits
 struct Exact {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, o);
     }
-    auto score32 = [&](float z) { return p.sigmoid ? 1.f / (1.f + expf(-z)) : expf(z - top) / denom; };
+    auto score32 = [&](float z) { return p.sigmoid ? __fdividef(1.f, 1.f + expf(-z)) : __fdividef(expf(z - top), denom); };
     auto bias_of = [&](int e) { return p.bias ? clean_bias(__ldg(p.bias + e)) : 0.f; };
 
     Exact ex;
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
         if (grouped) {
             __syncwarp();
             const int per = E / p.groups;
+            const float inv_per = 1.f / static_cast<float>(per);
             auto approx = [&](int e) -> float { return sc[e]; };
             auto exact = [&](int e) -> double {
                 if (!(sc[e] > -INFINITY)) return -INFINITY;
@@ -227,43 +229,94 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const int e = i * 32 + lane;
-                if (e < E && !((kept >> (e / per)) & 1u)) l[i] = -INFINITY;
+                // e / per: e + 1/2 is at least 1 / (2 per) from a multiple, far more than the product's rounding
+                const int g = static_cast<int>((static_cast<float>(e) + 0.5f) * inv_per);
+                if (e < E && !((kept >> g) & 1u)) l[i] = -INFINITY;
             }
         }
     }
 
+    constexpr bool SORTED = EPL <= 8;
+    int id[EPL];   // register i holds expert id[i] * 32 + lane
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) id[i] = i;
+    if constexpr (SORTED) {
+        // largest first, the lower index first among equals (odd-even merge network)
+        auto order_pair = [&](int x, int y) {
+            const bool swap = l[y] > l[x] || (l[y] == l[x] && id[y] < id[x]);
+            const float lx = l[x], ly = l[y];
+            const int ix = id[x], iy = id[y];
+            l[x] = swap ? ly : lx;
+            l[y] = swap ? lx : ly;
+            id[x] = swap ? iy : ix;
+            id[y] = swap ? ix : iy;
+        };
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; i += 2) order_pair(i, i + 1);
+        if constexpr (EPL >= 4) {
+#pragma unroll
+            for (int i = 0; i + 3 < EPL; i += 4) {
+                order_pair(i, i + 2);
+                order_pair(i + 1, i + 3);
+                order_pair(i + 1, i + 2);
+            }
+        }
+        if constexpr (EPL == 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) order_pair(i, i + 4);
+            order_pair(2, 4);
+            order_pair(3, 5);
+            order_pair(1, 2);
+            order_pair(3, 4);
+            order_pair(5, 6);
+        }
+    }
     int my_idx = -1;   // lane j keeps the j-th choice
     for (int j = 0; j < p.k; ++j) {
         float best = l[0];
-        int at = 0;
+        int at = id[0];
+        if constexpr (!SORTED) {
 #pragma unroll
-        for (int i = 1; i < EPL; ++i)
-            if (l[i] > best) {
-                best = l[i];
-                at = i;
-            }
+            for (int i = 1; i < EPL; ++i)
+                if (l[i] > best) {
+                    best = l[i];
+                    at = i;
+                }
+        }
         const float m = warp_max(best);
         if (!(m > -INFINITY)) break;   // nothing eligible is left
         unsigned pick = __reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(at * 32 + lane) : 0xffffffffu);
         if (p.bias) {
             const float near = m - 2.f * (delta + kDeltaRel * fabsf(m));
-            int close = 0;
+            bool close;   // whether a second candidate is near the maximum
+            if constexpr (SORTED) {
+                const unsigned heads = __ballot_sync(0xffffffffu, l[0] >= near);
+                close = (heads & (heads - 1u)) != 0u || __any_sync(0xffffffffu, l[1] >= near);
+            } else {
+                unsigned n = 0;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) close += l[i] >= near;
-            if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(close)) > 1u) {
+                for (int i = 0; i < EPL; ++i) n += l[i] >= near;
+                close = __reduce_add_sync(0xffffffffu, n) > 1u;
+            }
+            if (close) {
                 prepare_exact();
                 double bd = -INFINITY;
                 unsigned be = 0xffffffffu;
                 for (int i = 0; i < EPL; ++i) {
                     float v = -INFINITY;
+                    int vi = 0;
 #pragma unroll
                     for (int q = 0; q < EPL; ++q)
-                        if (q == i) v = l[q];
+                        if (q == i) {
+                            v = l[q];
+                            vi = id[q];
+                        }
                     if (v >= near) {
-                        const double o = exact_order(i * 32 + lane);
-                        if (o > bd) {
+                        const unsigned e = static_cast<unsigned>(vi * 32 + lane);
+                        const double o = exact_order(static_cast<int>(e));
+                        if (o > bd || (o == bd && e < be)) {
                             bd = o;
-                            be = static_cast<unsigned>(i * 32 + lane);
+                            be = e;
                         }
                     }
                 }
@@ -279,10 +332,27 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
             }
         }
         if (lane == j) my_idx = static_cast<int>(pick);
-        const bool owner = (pick & 31u) == static_cast<unsigned>(lane);
+        if ((pick & 31u) == static_cast<unsigned>(lane)) {   // taken out of its lane
+            const int gone = static_cast<int>(pick >> 5);
+            if constexpr (SORTED) {
+                bool after = false;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (owner && (pick >> 5) == static_cast<unsigned>(i)) l[i] = -INFINITY;
+                for (int i = 0; i + 1 < EPL; ++i) {
+                    after = after || id[i] == gone;
+                    if (after) {
+                        l[i] = l[i + 1];
+                        id[i] = id[i + 1];
+                    }
+                }
+                l[EPL - 1] = -INFINITY;
+                id[EPL - 1] = -1;
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (i == gone) l[i] = -INFINITY;
+            }
+        }
+        __syncwarp();
     }
 
     float s = 0.f;

@@ -10,7 +10,6 @@ every step of the computation runs in the library's own kernels.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import numpy as np
 import torch
@@ -64,35 +63,28 @@ def _need_cuda(*ts):
 
 def _expect(name: str, t, shape, dtype, device):
     """A tensor the C side cannot look into: its sizes, type and place."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
-    if t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of the input")
+    raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of the input")
 
 
 def _launch(fn, where: str, device: int, *args):
     """fn(*args, stream) on the current stream of `device`, with it current."""
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         with torch.cuda.device(device):
             return _launch(fn, where, device, *args)
-    status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    status = fn(*args, _raw_stream(device))
     if status != 0:
         raise FFNError(status, where)
 
 
-def _on_stream(f):
-    """Runs f under its `stream` argument, so that outputs and workspaces made
-    in the call come from that stream's memory (memory of another stream may
-    still be in use there)."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+# what torch.cuda.current_device() and current_stream() come down to once a
+# CUDA tensor exists (these calls are a third of a small operator's time)
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _rows_of(x: torch.Tensor):
@@ -104,12 +96,14 @@ def _rows_of(x: torch.Tensor):
     return (x.numel() // d if d else 0), d, dev
 
 
-@_on_stream
 def ffn_add_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
-                    r_out: torch.Tensor | None = None, out: torch.Tensor | None = None):
+                    r_out: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
     """(r, n): r = x + res (x itself without `res`) and n = RMSNorm(r) * g.
 
     `r_out` may be x or res (in place); without it a new tensor takes r."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_add_rmsnorm(x, g, eps, res, r_out, out)
     rows, d, dev = _rows_of(x)
     dt, shape = x.dtype, x.shape
     code = _dtype(x)
@@ -130,14 +124,16 @@ def ffn_add_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Ten
     return (x if r_out is None else r_out), out
 
 
-@_on_stream
 def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torch.Tensor | None = None,
                          group: int = 0, r_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                         scales: torch.Tensor | None = None):
+                         scales: torch.Tensor | None = None, stream=None):
     """(r, q, scales): as ffn_add_rmsnorm with the norm's output as
     torch.float8_e4m3fn codes and fp32 scales, one per row (group 0, shape
     [rows, 1]) or per `group` columns (32, 64 or 128; [rows, ceil(d / group)]):
     RMSNorm(r) * g is about q * scale."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_add_rmsnorm_e4m3(x, g, eps, res, group, r_out, out, scales)
     rows, d, dev = _rows_of(x)
     dt, shape = x.dtype, x.shape
     code = _dtype(x)
@@ -148,7 +144,7 @@ def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torc
             r_out = torch.empty_like(x)
     if r_out is not None:
         _expect("r_out", r_out, shape, dt, dev)
-    sshape = (*shape[:-1], -(-d // group) if group > 0 else 1)
+    sshape = shape[:-1] + (-(-d // group) if group > 0 else 1,)
     if out is None:
         out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
     else:
@@ -163,18 +159,20 @@ def ffn_add_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, res: torc
     return (x if r_out is None else r_out), out, scales
 
 
-@_on_stream
 def ffn_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, groups: int = 1,
                   topk_groups: int = 1, scale: float = 1.0, flags: int = 0, idx: torch.Tensor | None = None,
-                  weights: torch.Tensor | None = None):
+                  weights: torch.Tensor | None = None, stream=None):
     """(idx int32 [rows, k], weights fp32 [rows, k]) of a [rows, experts] tensor
     of router logits; flags: FFN_ROUTE_SIGMOID, FFN_ROUTE_RENORM.  A slot
     that no eligible expert is left for has index -1 and weight 0."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_route(logits, k, bias, groups, topk_groups, scale, flags, idx, weights)
     rows, experts, dev = _rows_of(logits)
     code = _dtype(logits)
     if bias is not None:
         _expect("bias", bias, (experts,), torch.float32, dev)
-    shape = (*logits.shape[:-1], k)
+    shape = logits.shape[:-1] + (k,)
     if idx is None:
         idx = torch.empty(shape, dtype=torch.int32, device=logits.device)
     else:
@@ -201,7 +199,7 @@ def _moe_inputs(x, idx, weights, res, out):
     """Checks what both routed blocks take; (rows, d, k, device index)."""
     rows, d, dev = _rows_of(x)
     k = idx.shape[-1]
-    shape = (*x.shape[:-1], k)
+    shape = x.shape[:-1] + (k,)
     _expect("idx", idx, shape, torch.int32, dev)
     _expect("weights", weights, shape, torch.float32, dev)
     if res is not None:
@@ -211,14 +209,16 @@ def _moe_inputs(x, idx, weights, res, out):
     return rows, d, k, dev
 
 
-@_on_stream
 def ffn_moe_forward(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor,
                     w_up: torch.Tensor, w_down: torch.Tensor, res: torch.Tensor | None = None, flags: int = 0,
-                    out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+                    out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The routed block: y = [res +] sum over a token's slots of weight * the
     chosen expert's SwiGLU block of x.  idx, weights: ffn_moe_route's [rows, k];
     w_gate, w_up [experts, ffn, d], w_down [experts, d, ffn] of x's type, or
     ffn_prepare_weights output with FFN_PREPARED_WEIGHTS."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_forward(x, idx, weights, w_gate, w_up, w_down, res, flags, out, ws)
     rows, d, k, dev = _moe_inputs(x, idx, weights, res, out)
     code = _dtype(x)
     experts, ffn = w_gate.shape[0], w_gate.shape[1]
@@ -253,13 +253,15 @@ def _moe_q4_weight(name, w, experts, out, inn, dev):
     return Q4Weight(qs.data_ptr(), sc.data_ptr())
 
 
-@_on_stream
 def ffn_moe_forward_q4(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_gate, w_up, w_down, ffn: int,
                        res: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                       ws: torch.Tensor | None = None) -> torch.Tensor:
+                       ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """ffn_moe_forward (bf16) with Q4 weights: ``w_*`` are (qs uint8 [experts,
     rows, 64 ceil(in/128)], scales [experts, rows, 4 ceil(in/128)] fp16 or
     their bits) pairs in the device layout of include/ffn.h."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_forward_q4(x, idx, weights, w_gate, w_up, w_down, ffn, res, out, ws)
     rows, d, k, dev = _moe_inputs(x, idx, weights, res, out)
     if x.dtype is not torch.bfloat16:
         raise TypeError("x must be torch.bfloat16")
