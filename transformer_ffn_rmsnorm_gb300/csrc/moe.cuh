@@ -85,38 +85,39 @@ __device__ __forceinline__ float swiglu(float gate, float up, float scale) {
     return __fdividef(gate, 1.0f + __expf(-gate)) * (up * scale);
 }
 
-// ---- epilogues of the single-CTA products (four warps, q = warp % 4, lane:
-// weight row 32 q + lane of the unit; columns are the tile's rows)
+// ---- epilogues (four warps, q = warp % 4, lane: weight row 32 q + lane of the
+// accumulator; columns are the tile's rows)
 
-constexpr int kSwapFloats = 2 * 2 * 8 * 64;   // shared memory of swiglu_epilogue
-
-// Lanes 0-63 of the accumulator hold gate, 64-127 up of the same 64 features.
-// Of every 16 columns the gate warps finish the first eight and the up warps
-// the others; each side hands over what the other needs.  PERM: h's columns 1
+// Lanes 0-63 of the accumulator hold gate, 64-127 up of the 64 features from
+// f0.  Of every 16 columns (from c0, `step` on) the gate warps finish the
+// first eight and the up warps the others; each side hands over what the
+// other needs, through `swap` and named barrier `id`.  PERM: h's columns 1
 // and 2 of every four exchanged.  h feeds the next product: one rounding to
 // its operand type.
 template <typename T, bool PERM>
-__device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane, const Unit &t, int wrows, T *h,
-                                                float (*swap)[2][8][64], float acc_scale, float out_scale) {
+__device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane, const Unit &t, int f0, int wrows, T *h,
+                                                float (*swap)[2][8][64], int c0, int step, int id, float acc_scale,
+                                                float out_scale) {
     const int fl = 32 * (q & 1) + lane, mat = q >> 1;
-    const int f = t.f * 64 + fl;
+    const int f = f0 + fl;
     const int at = PERM ? (f & ~3) | ((f & 1) << 1) | ((f >> 1) & 1) : f;
     const bool live = f < wrows;
     T *dst = h + static_cast<int64_t>(t.row0) * wrows + at;
-    for (int c = 0, pp = 0; c < t.n; c += 16, pp ^= 1) {
+    for (int c = c0, pp = 0; c < t.n; c += step, pp ^= 1) {
         uint32_t r[16];
         ptx::tmem_ld_32x32b_x16(taddr + c, r);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) swap[pp][mat][i][fl] = __uint_as_float(mat ? r[i] : r[8 + i]);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+        T *to = dst + static_cast<int64_t>(c + 8 * mat) * wrows;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float other = swap[pp][mat ^ 1][i][fl];
             const float mine = __uint_as_float(mat ? r[8 + i] : r[i]);
             const float hv = swiglu((mat ? other : mine) * acc_scale, mat ? mine : other, acc_scale * out_scale);
-            const int col = c + 8 * mat + i;
-            if (live && col < t.valid) dst[static_cast<int64_t>(col) * wrows] = from_f32<T>(hv);
+            if (live && c + 8 * mat + i < t.valid) *to = from_f32<T>(hv);
+            to += wrows;
         }
     }
 }
@@ -135,15 +136,16 @@ __device__ __forceinline__ void store_epilogue(uint32_t taddr, int q, int lane, 
     }
 }
 
-// Whether all four epilogue warps passed their wait (they leave together).
-__device__ __forceinline__ bool epilogue_vote(bool got) {
+// Whether all four warps of named barrier `id` passed their wait (they stay
+// or leave together).
+__device__ __forceinline__ bool epilogue_vote(bool got, int id) {
     int all;
     __syncwarp();
     asm volatile(
-        "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, 1, 128, a;\n\t"
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, %2, 128, a;\n\t"
         "selp.b32 %0, 1, 0, b;\n\t}"
         : "=r"(all)
-        : "r"(got ? 1 : 0)
+        : "r"(got ? 1 : 0), "r"(id)
         : "memory");
     return all != 0;
 }

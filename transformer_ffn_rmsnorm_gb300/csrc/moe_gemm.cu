@@ -5,23 +5,21 @@
 //   down:     part[r, o] = (W_down[e] h_r)_o                         (fp32)
 //
 // CTA pairs (tcgen05 .cta_group::2): a unit of work is 256 weight rows (128
-// in each CTA) against one token tile of n <= 256 columns of one expert.  The
-// weights are the M operand, loaded by TMA as 128 x 64 boxes; the tokens'
-// sorted rows (of x or of h) are the N operand, each CTA holding half of the
-// columns in boxes of 128, 64, 32 and 16 rows.
+// in each CTA; gate/up: 64 rows of W_gate stacked on the same 64 of W_up)
+// against one token tile of n <= 256 columns of one expert.  The
+// weights are the M operand; the tokens' sorted rows (of x or of h) are the N
+// operand, each CTA holding half of the columns in boxes of 128, 64, 32 and 16 rows.
 //
-// What bounds it: the tensor pipe.  Why the
-// tile is 256 x 256: per 64 k values a CTA takes 32 KB of gate and up rows and 16 KB of
-// tokens for 1024 cycles of MMAs, 48 bytes a cycle from L2; with 128 columns
-// it would be 80.  The price is tensor memory: gate and up together fill its
-// 512 columns, so a wide gate/up tile's epilogue does not overlap the next
-// tile's MMAs.  Where every tile of the call is at most 128 wide (plan.header[1]) there are two accumulators
-// and it does; the down product always has two.
+// What bounds it: the tensor pipe.  The 256 x 256 tile takes 64 bytes a cycle and
+// SM from L2, and its accumulator half of tensor memory, so that a unit's
+// epilogue runs under the next unit's MMAs.  (Gate and up in two accumulators
+// of 256 columns would take 48 bytes a cycle, but fill tensor memory: the
+// epilogue then stood between the units, 7000 cycles after 30000 at d = 2048.
+// Tiles of 128 tokens instead, which leave room, were slower still: 80 bytes.)
 //
-// Roles: warp 0 loads, warp 1 issues the
-// MMAs (one thread of the even CTA), warps 2-17 read the accumulators (lane =
-// weight row, column = token): for a fixed column a warp's 32 lanes store 32
-// neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
+// Roles: warp 0 loads, warp 1 issues the MMAs (the even CTA's), warps 2-9 read
+// the accumulators (lane = weight row, column = token): for a fixed column a
+// warp's 32 lanes store 32 neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -39,28 +37,24 @@ constexpr int kBM = 128, kBK = 64, kTile = kMoeCutPair.tile;
 constexpr uint32_t kABytes = kBM * kBK * 2;                // one CTA's weight rows of a k block
 constexpr uint32_t kBBytes = (kTile / 2) * kBK * 2;        // room for its half of the tokens
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
 
-// A stage holds KSUB blocks of 64 k values: gate rows, up rows, tokens, or
-// (two such blocks) down rows, tokens.
-template <int MODE> struct Ring {
-    static constexpr int NMAT = MODE == GATEUP ? 2 : 1;
-    static constexpr int KSUB = MODE == GATEUP ? 1 : 2;
-    static constexpr uint32_t SUB_BYTES = NMAT * kABytes + kBBytes;
-    static constexpr uint32_t STAGE_BYTES = KSUB * SUB_BYTES;
-    static constexpr int STAGES = static_cast<int>((225u * 1024u) / STAGE_BYTES);
-    static constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
-    static_assert(STAGES >= 3 && SMEM_BYTES > 114 * 1024, "one CTA per SM: each allocates all of tensor memory");
-};
+// A stage holds two blocks of 64 k values: weight rows, tokens.
+constexpr int kSub = 2;
+constexpr uint32_t kSubBytes = kABytes + kBBytes, kStageBytes = kSub * kSubBytes;
+constexpr int kStages = 3;
+constexpr size_t kSmemBytes = kStages * kStageBytes + 1024;
+static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 210 * 1024,
+              "one CTA per SM (each allocates all of tensor memory), beside 16 KB of static shared memory");
 
 struct Params {
     const int *header;
     const int4 *tiles;
-    int nf;            // feature tiles of 256 rows
+    int nf;            // feature tiles of 128 (gate/up) or 256 rows
     int wrows;         // weight rows of an expert (ffn or d)
     int nkb;           // 64-wide k blocks
     void *out;         // h (operand type) or part (fp32), [pairs x wrows]
@@ -73,25 +67,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                     const __grid_constant__ moe::RowMaps maps_b, const Params p) {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    using RG = Ring<MODE>;
-    constexpr int STAGES = RG::STAGES, KSUB = RG::KSUB;
+    constexpr int kFRows = MODE == GATEUP ? 128 : 256;   // features of a unit
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
+    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
+    __shared__ float s_swap[MODE == GATEUP ? kEpiWarps / 4 : 1][MODE == GATEUP ? 2 : 1][2][8][64];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort, s_never;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-    auto sA = [&](int s, int j, int m) { return base + s * RG::STAGE_BYTES + j * RG::SUB_BYTES + m * kABytes; };
-    auto sB = [&](int s, int j) { return base + s * RG::STAGE_BYTES + j * RG::SUB_BYTES + RG::NMAT * kABytes; };
+    auto sA = [&](int s, int j) { return base + s * kStageBytes + j * kSubBytes; };
+    auto sB = [&](int s, int j) { return sA(s, j) + kABytes; };
     auto full = [&](int s) { return ptx::smem_u32(&bar_full[s]); };
     auto empty = [&](int s) { return ptx::smem_u32(&bar_empty[s]); };
     auto tfull = [&](int a) { return ptx::smem_u32(&bar_tfull[a]); };
     auto tempty = [&](int a) { return ptx::smem_u32(&bar_tempty[a]); };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(full(s), 1);
             ptx::mbar_init(empty(s), 1);
         }
@@ -122,15 +116,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto lead = [&](uint32_t bar) { return ptx::mapa_shared(bar, 0); };   // the pair's barriers live in the even CTA
     volatile int *abort_flag = &s_abort;
     volatile int *never = &s_never;
-    const int nst = (p.nkb + KSUB - 1) / KSUB;
+    const int nst = (p.nkb + kSub - 1) / kSub;
     const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
     uint32_t produced = 0;
 
     ptx::griddep_wait();   // the plan, x, h: all written by kernels before this one
     const int units = __ldcg(p.header) * p.nf;
-    // two accumulators where gate and up of the widest tile fit in half of tensor memory
-    const bool two = MODE == DOWN || __ldcg(p.header + 1) <= 128;
-    const uint32_t up_off = two ? 128u : 256u;
     auto tile_a = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf)); };
     auto tile_b = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf) + 1); };
 
@@ -142,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
             const int half = t.n >> 1;   // this CTA's columns, a multiple of 16
-            const int wrow = t.expert * p.wrows + t.f * 256 + static_cast<int>(rank) * kBM;
+            const int wrow = t.expert * p.wrows + t.f * kFRows + static_cast<int>(rank) * (kFRows / 2);
             const int brow = t.row0 + static_cast<int>(rank) * half;
             for (int ks = 0; ks < nst; ++ks) {
                 const bool got = ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, kWaitNs);
@@ -153,12 +144,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ptx::elect_one()) {
                     const uint32_t bar = lead(full(s));
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(full(s), KSUB * (2 * RG::NMAT * kABytes + t.n * (kBK * 2)));
+                        ptx::mbar_arrive_expect_tx(full(s), kSub * (2 * kABytes + t.n * (kBK * 2)));
 #pragma unroll
-                    for (int j = 0; j < KSUB; ++j) {
-                        const int k0 = (ks * KSUB + j) * kBK;   // a block past K is zero fill
-                        ptx::tma_load_2d_pair(sA(s, j, 0), &map_w0, bar, k0, wrow);
-                        if (MODE == GATEUP) ptx::tma_load_2d_pair(sA(s, j, 1), &map_w1, bar, k0, wrow);
+                    for (int j = 0; j < kSub; ++j) {
+                        const int k0 = (ks * kSub + j) * kBK;   // a block past K is zero fill
+                        ptx::tma_load_2d_pair(sA(s, j), &map_w0, bar, k0, wrow);
+                        if (MODE == GATEUP) ptx::tma_load_2d_pair(sA(s, j) + kABytes / 2, &map_w1, bar, k0, wrow);
                         moe::for_row_boxes(maps_b, half, [&](const CUtensorMap *m, int r) {
                             ptx::tma_load_2d_pair(sB(s, j) + r * 128, m, bar, k0, brow + r);
                         });
@@ -166,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++produced;
-                if (++s == STAGES) {
+                if (++s == kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -209,27 +200,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < KSUB; ++j) {
-                        const uint64_t bd = ptx::sdesc_k_sw128(sB(s, j));
+                    for (int j = 0; j < kSub; ++j) {
+                        const uint64_t ad = ptx::sdesc_k_sw128(sA(s, j)), bd = ptx::sdesc_k_sw128(sB(s, j));
 #pragma unroll
-                        for (int m = 0; m < RG::NMAT; ++m) {
-                            const uint64_t ad = ptx::sdesc_k_sw128(sA(s, j, m));
-#pragma unroll
-                            for (int k = 0; k < kBK / 16; ++k)   // 32 bytes of k further: 2 in the address field
-                                ptx::tc_mma_f16_pair(d0 + m * up_off, ad + 2 * k, bd + 2 * k, idesc, (ks | j | k) != 0);
-                        }
+                        for (int k = 0; k < kBK / 16; ++k)   // 32 bytes of k further: 2 in the address field
+                            ptx::tc_mma_f16_pair(d0, ad + 2 * k, bd + 2 * k, idesc, (ks | j | k) != 0);
                     }
                     ptx::tc_commit_pair(empty(s), 0x3);
                     if (ks == nst - 1) ptx::tc_commit_pair(tfull(acc), 0x3);
                 }
                 __syncwarp();
-                if (++s == STAGES) {
+                if (++s == kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) break;
-            if (!two || ++acc == 2) {
+            if (++acc == 2) {
                 acc = 0;
                 acc_ph ^= 1u;
             }
@@ -243,46 +230,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 2) {
         // ---------------------------------------------------------- epilogue
         const int q = warp & 3;                 // this warp may read TMEM lanes 32q .. 32q+31
-        const int part = (warp - 2) >> 2;       // which of every four 16-column chunks
+        const int part = (warp - 2) >> 2;       // which of every two 16-column chunks
         bool ok = true;
         int acc = 0;
         uint32_t acc_ph = 0;
         for (int u = u0; u < units; u += ustep) {
             const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
             const bool got = ptx::mbar_wait(tfull(acc), acc_ph, abort_flag, kWaitNs);
-            if (!__all_sync(0xffffffffu, got)) {
+            if (!moe::epilogue_vote(got, 1 + part)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const int f = t.f * 256 + static_cast<int>(rank) * kBM + q * 32 + lane;
-            const bool live = f < p.wrows;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            const int64_t at = static_cast<int64_t>(t.row0) * p.wrows + f;
-            for (int c = part * 16; c < t.n; c += 16 * (kEpiWarps / 4)) {
-                if constexpr (MODE == GATEUP) {
-                    uint32_t rg[16], ru[16];
-                    ptx::tmem_ld_32x32b_x16(taddr + c, rg);
-                    ptx::tmem_ld_32x32b_x16(taddr + up_off + c, ru);
-                    ptx::tmem_ld_wait();
-                    T *dst = static_cast<T *>(p.out) + at + static_cast<int64_t>(c) * p.wrows;
-                    // h feeds the next product: one rounding to its operand type
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const T hv = from_f32<T>(moe::swiglu(__uint_as_float(rg[i]) * p.acc_scale,
-                                                             __uint_as_float(ru[i]), p.acc_scale * p.out_scale));
-                        if (live && c + i < t.valid) *dst = hv;
-                        dst += p.wrows;
-                    }
-                } else {
+            const int f0 = t.f * kFRows + static_cast<int>(rank) * (kFRows / 2);
+            if constexpr (MODE == GATEUP) {
+                moe::swiglu_epilogue<T, false>(taddr, q, lane, t, f0, p.wrows, static_cast<T *>(p.out), s_swap[part],
+                                               16 * part, 16 * (kEpiWarps / 4), 1 + part, p.acc_scale, p.out_scale);
+            } else {
+                const int f = f0 + q * 32 + lane;
+                float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + f;
+                for (int c = 16 * part; c < t.n; c += 16 * (kEpiWarps / 4)) {
                     uint32_t r[16];
                     ptx::tmem_ld_32x32b_x16(taddr + c, r);
                     ptx::tmem_ld_wait();
-                    float *dst = static_cast<float *>(p.out) + at + static_cast<int64_t>(c) * p.wrows;
+                    float *to = dst + static_cast<int64_t>(c) * p.wrows;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (live && c + i < t.valid)
-                            dst[static_cast<int64_t>(i) * p.wrows] = __uint_as_float(r[i]) * p.acc_scale;
+                    for (int i = 0; i < 16; ++i) {
+                        if (f < p.wrows && c + i < t.valid) *to = __uint_as_float(r[i]) * p.acc_scale;
+                        to += p.wrows;
+                    }
                 }
             }
             ptx::tc_fence_before();
@@ -291,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) ptx::mbar_arrive(tempty(acc));
                 else ptx::mbar_arrive_cluster(lead(tempty(acc)));
             }
-            if (!two || ++acc == 2) {
+            if (++acc == 2) {
                 acc = 0;
                 acc_ph ^= 1u;
             }
@@ -305,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 0 && lane == 0 && leader) {
         // loads still in flight (only after an abandoned wait) land before shared memory is released
-        for (uint32_t s = 0; s < STAGES; ++s)
+        for (uint32_t s = 0; s < kStages; ++s)
             if (produced > s)
-                ptx::mbar_wait(full(s), ((produced - s + STAGES - 1) / STAGES - 1) & 1u, never, kWaitNs);
+                ptx::mbar_wait(full(s), ((produced - s + kStages - 1) / kStages - 1) & 1u, never, kWaitNs);
     }
     __syncthreads();
     ptx::cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
@@ -327,7 +304,7 @@ template <int MODE, bool BF16>
 cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const moe::RowMaps &b, int64_t pairs,
                    int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, float out_scale,
                    cudaStream_t s) {
-    using RG = Ring<MODE>;
+    constexpr int kFRows = MODE == GATEUP ? 128 : 256;
     const auto kern = &moe_gemm_kernel<MODE, BF16>;
     static int configured_device = -1, slots = 0;   // co-resident CTA pairs
     int dev = 0;
@@ -342,10 +319,10 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = RG::SMEM_BYTES;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = attr;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(RG::SMEM_BYTES));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
         cfg.numAttrs = 1;
@@ -357,7 +334,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     Params p{};
     p.header = plan.header;
     p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
-    p.nf = static_cast<int>((wrows + 255) / 256);
+    p.nf = static_cast<int>((wrows + kFRows - 1) / kFRows);
     p.wrows = static_cast<int>(wrows);
     p.nkb = static_cast<int>((K + kBK - 1) / kBK);
     p.out = out;
@@ -388,7 +365,7 @@ cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *xs, const vo
     const bool bf = op == DT_BF16;
     CUtensorMap w0, w1;
     moe::RowMaps b;
-    if (!map_16(&w0, wg, bf, d, experts * ffn, kBM) || !map_16(&w1, wu, bf, d, experts * ffn, kBM) ||
+    if (!map_16(&w0, wg, bf, d, experts * ffn, kBM / 2) || !map_16(&w1, wu, bf, d, experts * ffn, kBM / 2) ||
         !map_rows(&b, xs, bf, d, pairs))
         return cudaErrorInvalidValue;
     return bf ? launch<GATEUP, true>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s)

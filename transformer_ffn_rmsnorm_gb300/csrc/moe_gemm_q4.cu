@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units; u += ustep) {
             const Unit t = unit_at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
-            const bool stay = moe::epilogue_vote(got);
+            const bool stay = moe::epilogue_vote(got, 1);
             if (!stay) {
                 ok = false;
                 break;
@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 128;
             if constexpr (MODE == GATEUP)
-                moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, p.wrows, static_cast<__half *>(p.out), s_swap,
-                                                   p.acc_scale, p.out_scale);
+                moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<__half *>(p.out), s_swap,
+                                                   0, 16, 1, p.acc_scale, p.out_scale);
             else
                 moe::store_epilogue(taddr, q, lane, t, p.wrows,
                                     static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);

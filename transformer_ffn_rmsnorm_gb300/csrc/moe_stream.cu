@@ -209,15 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = u0; u < units; u += ustep) {
             const Unit t = unit_at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
-            if (!moe::epilogue_vote(got)) {
+            if (!moe::epilogue_vote(got, 1)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
             if constexpr (MODE == GATEUP)
-                moe::swiglu_epilogue<T, false>(taddr, q, lane, t, p.wrows, static_cast<T *>(p.out), s_swap, p.acc_scale,
-                                               p.out_scale);
+                moe::swiglu_epilogue<T, false>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<T *>(p.out), s_swap, 0, 16,
+                                               1, p.acc_scale, p.out_scale);
             else
                 moe::store_epilogue(taddr, q, lane, t, p.wrows,
                                     static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
