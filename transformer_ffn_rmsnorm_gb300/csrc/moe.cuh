@@ -65,6 +65,30 @@ __device__ __forceinline__ Unit unit_of(int u, int nf, const int4 &a, const int4
     return r;
 }
 
+// A role's walk over its units: the next unit's table entry is requested when
+// the current one is handed out, so that its latency (an L2 access) passes
+// under the current unit's stages.
+template <int GRAN> struct Walk {
+    const int4 *tiles;
+    int nf, splits, units, step;
+    int4 a, b;
+    __device__ __forceinline__ void fetch(int v) {
+        if (v >= units) return;
+        const int4 *t = tiles + 2 * (v / splits / nf);
+        a = __ldcg(t);
+        b = __ldcg(t + 1);
+    }
+    __device__ __forceinline__ Walk(const int4 *t, int n, int s, int total, int first, int by)
+        : tiles(t), nf(n), splits(s), units(total), step(by), a(make_int4(0, 0, 1, 0)), b(a) {
+        fetch(first);
+    }
+    __device__ __forceinline__ Unit at(int v) {
+        const Unit u = unit_of<GRAN>(v / splits, nf, a, b);
+        fetch(v + step);
+        return u;
+    }
+};
+
 // The sorted rows a tile reads, loaded in boxes of 128, 64, 32 and 16 rows:
 // `rows` (a multiple of 16, at most 128) are the boxes of its set bits.
 struct RowMaps {

@@ -122,16 +122,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     ptx::griddep_wait();   // the plan, x, h: all written by kernels before this one
     const int units = __ldcg(p.header) * p.nf;
-    auto tile_a = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf)); };
-    auto tile_b = [&](int u) { return __ldcg(p.tiles + 2 * (u / p.nf) + 1); };
+    auto walk_units = [&]() { return moe::Walk<kMoeCutPair.gran>(p.tiles, p.nf, 1, units, u0, ustep); };
 
     if (warp == 0) {
         // ------------------------------------------------------ producer
         bool ok = true;
+        auto walk = walk_units();
         int s = 0;
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
+            const Unit t = walk.at(u);
             const int half = t.n >> 1;   // this CTA's columns, a multiple of 16
             const int wrow = t.expert * p.wrows + t.f * kFRows + static_cast<int>(rank) * (kFRows / 2);
             const int brow = t.row0 + static_cast<int>(rank) * half;
@@ -170,19 +170,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && leader) {
         // -------------------------------------------------------- MMA issuer
         bool ok = true;
+        auto walk = walk_units();
         int s = 0, acc = 0;
         uint32_t ph = 0, acc_ph = 0;
-        int4 na = make_int4(0, 0, 1, 0), nb = na;
-        if (u0 < units) {
-            na = tile_a(u0);
-            nb = tile_b(u0);
-        }
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, na, nb);
-            if (u + ustep < units) {   // the next unit's tile, under this one's MMAs
-                na = tile_a(u + ustep);
-                nb = tile_b(u + ustep);
-            }
+            const Unit t = walk.at(u);
             const uint32_t idesc = ptx::idesc_f16(256, t.n, BF16);
             bool got = ptx::mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -232,10 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;                 // this warp may read TMEM lanes 32q .. 32q+31
         const int part = (warp - 2) >> 2;       // which of every two 16-column chunks
         bool ok = true;
+        auto walk = walk_units();
         int acc = 0;
         uint32_t acc_ph = 0;
         for (int u = u0; u < units; u += ustep) {
-            const Unit t = moe::unit_of<kMoeCutPair.gran>(u, p.nf, tile_a(u), tile_b(u));
+            const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(tfull(acc), acc_ph, abort_flag, kWaitNs);
             if (!moe::epilogue_vote(got, 1 + part)) {
                 ok = false;

@@ -184,18 +184,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto lo_of = [&](int v) { return nraw * (v % p.splits) / p.splits; };
     auto hi_of = [&](int v) { return nraw * (v % p.splits + 1) / p.splits; };
     auto stages_of = [&](int v) { return min(2 * hi_of(v), p.ngrp) - 2 * lo_of(v); };
-    auto unit_at = [&](int v) {
-        const int u = v / p.splits;
-        const int4 *t = p.tiles + 2 * (u / p.nf);
-        return moe::unit_of<kGran>(u, p.nf, __ldcg(t), __ldcg(t + 1));
-    };
+    auto walk_units = [&]() { return moe::Walk<kGran>(p.tiles, p.nf, p.splits, units, u0, ustep); };
 
     if (warp == 0) {
         // ------------------------------------------------------ nibbles
         int s = 0;
         uint32_t ph = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             const int wrow = t.expert * p.wrows + t.f * kFRows;
             for (int r = lo_of(u), re = hi_of(u); r < re; ++r) {
                 const bool got = ptx::mbar_wait(bar(&bar_rempty[s]), ph ^ 1u, abort_flag, kWaitNs);
@@ -222,8 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = (p.ngrp & 1) == 0;   // rows of scales start on 16 bytes
         int s = 0;
         uint32_t ph = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             const uint16_t *src[4];   // of this lane's rows lane, lane + 32, ...
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -260,8 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ tokens
         int s = 0;
         uint32_t ph = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             for (int g = 2 * lo_of(u), ge = g + stages_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -294,15 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, acc = 0;
         uint32_t ph = 0, pacc = 0;
         bool ready = false;
-        int4 na = make_int4(0, 0, 1, 0), nb = na;
-        auto fetch = [&](int v) {
-            na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
-            nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
-        };
-        if (u0 < units) fetch(u0);
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
-            if (u + ustep < units) fetch(u + ustep);
+            const Unit t = walk.at(u);
             const uint32_t idesc = ptx::idesc_f16(128, t.n, false);
             bool got = ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -418,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;
         int acc = 0;
         uint32_t pacc = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
             const bool stay = moe::epilogue_vote(got, 1);
             if (!stay) {

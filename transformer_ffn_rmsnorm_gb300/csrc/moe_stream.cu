@@ -105,18 +105,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int units = __ldcg(p.header) * p.nf * p.splits;
     auto lo_of = [&](int v) { return p.nst * (v % p.splits) / p.splits; };
     auto hi_of = [&](int v) { return p.nst * (v % p.splits + 1) / p.splits; };
-    auto unit_at = [&](int v) {
-        const int u = v / p.splits;
-        const int4 *t = p.tiles + 2 * (u / p.nf);
-        return moe::unit_of<kGran>(u, p.nf, __ldcg(t), __ldcg(t + 1));
-    };
+    auto walk_units = [&]() { return moe::Walk<kGran>(p.tiles, p.nf, p.splits, units, u0, ustep); };
 
     if (warp == 0) {
         // ------------------------------------------------------ producer
         int s = 0;
         uint32_t ph = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             const int wrow = t.expert * p.wrows + t.f * kFRows;
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
@@ -150,15 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------- MMA issuer
         int s = 0, acc = 0;
         uint32_t ph = 0, pacc = 0;
-        int4 na = make_int4(0, 0, 1, 0), nb = na;
-        auto fetch = [&](int v) {
-            na = __ldcg(p.tiles + 2 * (v / p.splits / p.nf));
-            nb = __ldcg(p.tiles + 2 * (v / p.splits / p.nf) + 1);
-        };
-        if (u0 < units) fetch(u0);
+        auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
-            const Unit t = moe::unit_of<kGran>(u / p.splits, p.nf, na, nb);
-            if (u + ustep < units) fetch(u + ustep);
+            const Unit t = walk.at(u);
             const uint32_t idesc = ptx::idesc_f16(128, t.n, BF16);
             bool got = ptx::mbar_wait(bar(&bar_tempty[acc]), pacc ^ 1u, abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -206,8 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;
         int acc = 0;
         uint32_t pacc = 0;
+        auto walk = walk_units();
         for (int u = u0; u < units; u += ustep) {
-            const Unit t = unit_at(u);
+            const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
             if (!moe::epilogue_vote(got, 1)) {
                 ok = false;
