@@ -56,6 +56,12 @@ static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
 constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
 constexpr int kDequantWarps = 4, kGroups = 3, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
 constexpr int kThreads = 32 * (4 + kGroups * kDequantWarps + kEpiWarps);
+// A wait tells phases apart by parity alone, so no group may come to a barrier
+// two phases early.  A group that comes for stage m has stored stage m -
+// kGroups, for which the MMAs had consumed all stages up to m - kGroups -
+// kStages: the slot's use m - 2 kStages, and the raw slot's last use, must be
+// among those.
+static_assert(kGroups <= kStages && kGroups + kStages <= 2 * kRawStages, "waits by parity");
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
