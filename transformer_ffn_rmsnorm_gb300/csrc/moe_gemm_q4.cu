@@ -17,8 +17,8 @@
 // What bounds it: few tokens: HBM, if the dequantisation keeps up.  A stage (128 rows of 128
 // values, 9 KB) is 430 cycles of this SM's share of HBM; its dequantisation is four
 // warps of about 260 instructions, and the wait, the loads, the arithmetic and
-// the store of one warp follow one another, so three groups of four warps
-// take stages in turn, one of each group to a scheduler.  More tokens: the activations from L2 (32 KB a
+// the store of one warp follow one another, so two groups of four warps
+// take stages in turn, one of each group to a scheduler (a third changed nothing).  More tokens: the activations from L2 (32 KB a
 // stage at 128 columns), then the tensor pipe.
 //
 // Arithmetic: a nibble pair becomes fp16 1024 + u (or 1024 + 16 u, the high
@@ -29,8 +29,8 @@
 // the plan writes x and the gate/up epilogue writes h in that order.
 //
 // Roles: warp 0 loads nibbles, warp 3 scales, warp 2 tokens; warp 1 issues the
-// MMAs; warps 4-15 dequantise (warp w fills TMEM lanes 32 (w % 4) .. of every
-// third stage); warps 16-19 are the epilogue.  Every wait is
+// MMAs; warps 4-11 dequantise (warp w fills TMEM lanes 32 (w % 4) .. of every
+// second stage); warps 12-15 are the epilogue.  Every wait is
 // bounded (1 s) as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
@@ -47,21 +47,22 @@ using moe::Unit;
 constexpr int kRows = 128, kK = 128, kTile = kMoeCutQ4.tile, kGran = kMoeCutQ4.gran;
 constexpr uint32_t kRawBytes = kRows * 128, kScaleBytes = kRows * 16;   // nibbles and scales of two stages' values
 constexpr uint32_t kBBytes = kTile * kK * 2;                            // room for a stage's tokens
-constexpr int kRawStages = 4, kStages = 4;   // a stage: A in tensor memory, tokens in shared memory, one barrier
+constexpr int kRawStages = 6, kStages = 3;   // a stage: A in tensor memory, tokens in shared memory, one barrier
 constexpr uint32_t kRawOff = kStages * kBBytes;
 constexpr uint32_t kScaleOff = kRawOff + kRawStages * kRawBytes;
 constexpr size_t kSmemBytes = kScaleOff + kRawStages * kScaleBytes + 1024;
 static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
               "one CTA per SM (each allocates all of tensor memory), beside 8 KB of static shared memory");
 constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
-constexpr int kDequantWarps = 4, kGroups = 3, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
+constexpr int kDequantWarps = 4, kGroups = 2, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
 constexpr int kThreads = 32 * (4 + kGroups * kDequantWarps + kEpiWarps);
 // A wait tells phases apart by parity alone, so no group may come to a barrier
-// two phases early.  A group that comes for stage m has stored stage m -
-// kGroups, for which the MMAs had consumed all stages up to m - kGroups -
-// kStages: the slot's use m - 2 kStages, and the raw slot's last use, must be
-// among those.
-static_assert(kGroups <= kStages && kGroups + kStages <= 2 * kRawStages, "waits by parity");
+// a phase too early.  A group that comes for stage m has stored stage m -
+// kGroups, for which the MMAs had consumed every stage up to m - kGroups -
+// kStages: the slot's use before the last (m - 2 kStages) and the raw slot's
+// last use (m - kRawStages where raw slots hold a single stage, as in rows of
+// one group) must be among those.
+static_assert(kGroups <= kStages && kGroups + kStages <= kRawStages, "waits by parity");
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
