@@ -228,6 +228,23 @@ def test_captured_with_other_experts_at_replay(env):
         assert torch.equal(y1, ffn.ffn_moe_forward(x2[:1], idx2[:1], w2[:1], wg, wu, wd))
 
 
+@pytest.mark.parametrize("rows,experts", [(96, 2), (128, 3), (40, 1), (20, 8), (300, 4)])
+def test_many_calls_in_a_row(env, rows, experts):
+    """Calls queued back to back: each one's kernels start while the ones
+    before still hold some multiprocessors (small plans, CTA pairs and single
+    CTAs), where a pair's allocation of tensor memory has to wait for both."""
+    torch, ffn = env
+    x, idx, w, wg, wu, wd, res = make(torch, rows, 512, 1024, experts, min(2, experts), torch.bfloat16)
+    want = ffn.ffn_moe_forward(x, idx, w, wg, wu, wd, res=res)
+    ws = ffn.workspace(ffn.ffn_moe_workspace_bytes(rows, 512, 1024, experts, min(2, experts), x.dtype), "cuda")
+    y = torch.empty_like(x)
+    for _ in range(600):
+        ffn.ffn_moe_forward(x, idx, w, wg, wu, wd, res=res, out=y, ws=ws)
+    torch.cuda.synchronize()
+    ffn.ffn_device_status()
+    assert torch.equal(y, want)
+
+
 def test_streams_with_their_own_workspaces(env):
     torch, ffn = env
     sets = [make(torch, 150 + 30 * i, 256, 512, 8, 2, torch.bfloat16, seed=i) for i in range(3)]

@@ -332,8 +332,12 @@ struct MoePlan {
 };
 
 // Rows an expert has on average (of those in use, at most) up to which 16-bit
-// weights stream through single CTAs.
-constexpr int64_t kMoeStreamRows = 32;
+// weights stream through single CTAs.  Whole calls, us, single CTAs / pairs:
+// 8 experts of 4096 x 4096, 2 a token: 1 row 48.0 / 51.2; 16 rows an expert
+// 145 / 147, 24 151.6 / 150.3, 48 169 / 157, 96 210 / 165.  64 experts of 2048
+// x 1408, 6 a token: 1 row 26 / 30; 6 rows an expert 184 / 191, 24 192 / 199,
+// 48 203 / 209, 96 257 / 230.
+constexpr int64_t kMoeStreamRows = 24;
 
 ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, bool q4, MoePlan *m) {
     if (rows < 0 || d < 1 || ffn < 1 || experts < 1 || experts > moe::kMaxExperts || k < 1 || k > 32)

@@ -101,6 +101,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MODE == GATEUP) ptx::tma_prefetch_map(&map_w1);
         for (int i = 0; i < 4; ++i) ptx::tma_prefetch_map(&maps_b.m[i]);
     }
+    // Both CTAs run before either allocates: the allocation is the pair's, and
+    // one that the even CTA began before the odd one had started (a CTA of the
+    // kernel before still on its SM) left the odd one waiting in it for good.
+    __syncwarp();
+    ptx::cluster_sync();
     if (warp == 1) {
         ptx::tmem_alloc_pair(ptx::smem_u32(&s_tmem_base), kTmemCols);
         ptx::tmem_relinquish_pair();
