@@ -256,6 +256,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::tma_prefetch_map(&map_b0);
         if (MODE != MODE_PLAIN) ptx::tma_prefetch_map(&map_b1);
     }
+    if constexpr (PAIR) {
+        // both CTAs run before either allocates: the allocation is the pair's,
+        // and one begun while the other CTA had not started yet (a CTA of the
+        // kernel before still on its SM) can leave that one waiting for good
+        __syncwarp();
+        ptx::cluster_sync();
+    }
     if (warp == 1) {
         if constexpr (PAIR) {
             ptx::tmem_alloc_pair(ptx::smem_u32(&s_tmem_base), TMEM_COLS);
