@@ -28,9 +28,9 @@ struct Tile {
 };
 
 struct Plan {
-    int *header;       // [0] token tiles, [1] columns of the widest tile, [2] sorted rows
+    int *header;       // [0] token tiles, [1] columns of the widest tile
     Tile *tiles;
-    int *row_token;    // token of each sorted row
+    int *hist;         // [chunks][experts] pairs of each expert (more than 256 pairs)
     int *pos;          // sorted row of pair (token, slot), or -1 (no expert)
 };
 

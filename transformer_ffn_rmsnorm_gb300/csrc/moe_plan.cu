@@ -1,14 +1,16 @@
 // moe_plan.cu -- the two ends of the routed block: sorting the (token, slot)
 // pairs by expert, and adding each token's weighted results.
 //
-// The plan counts the pairs of each expert in shared memory, scans the
-// counts, cuts every expert's rows into token tiles of equal width and deals
-// the sorted positions out.  Up to 256 pairs (decode) every CTA of one
-// launch does that for itself and copies a share of x's rows to their sorted
-// places; more pairs are sorted by one CTA and copied by a second kernel (a
-// launch is then small beside the products).  In the large form the order of an expert's
-// rows depends on the order of the warps; the results do not: every column
-// of a product is computed the same way wherever it stands.
+// The plan counts the pairs of each expert, scans the counts, cuts every
+// expert's rows into token tiles of equal width and deals the sorted
+// positions out.  Up to 256 pairs (decode) every CTA of one launch does that
+// for itself and copies a piece of a row of x to its sorted place.  More pairs
+// take three kernels: counts of chunks of pairs (shared-memory atomics, whose
+// old values are the pairs' ranks), one CTA's scan over chunks and experts, and
+// the copy, a warp a row.  (One CTA for the first two took 21 us for 24576
+// pairs, the atomics of 32 warps one after the other.)  In the large form the
+// order of an expert's rows depends on the order of the warps; the results do
+// not: every column of a product is computed the same way wherever it stands.
 //
 // The combination adds a token's k fp32 rows in slot order with fp32 weights
 // and rounds once.  Bound by reading those rows.
@@ -25,6 +27,12 @@ using moe::Tile;
 constexpr int kPlanThreads = 1024;
 
 constexpr int kSmallPairs = 256;   // up to here one launch plans and copies
+constexpr int kChunkThreads = 256, kMaxChunks = 512;
+
+// pairs of a chunk: a multiple of 256, at most kMaxChunks chunks
+constexpr int64_t chunk_pairs(int64_t pairs) {
+    return ((pairs + kMaxChunks - 1) / kMaxChunks + kChunkThreads - 1) / kChunkThreads * kChunkThreads;
+}
 
 struct PlanParams {
     const int32_t *idx;
@@ -34,6 +42,7 @@ struct PlanParams {
     const void *x;
     void *xs;
     int nvec;   // 8-element vectors of a row of x
+    int chunk, chunks;
     bool to_f16, perm;
     unsigned *err;
 };
@@ -101,6 +110,7 @@ __device__ __forceinline__ uint4 convert_vec(const PlanParams &p, const uint4 &v
 
 struct PlanShared {
     int count[moe::kMaxExperts], first[moe::kMaxExperts], row0[moe::kMaxExperts];
+    int part[kPlanThreads];
     int warp[3][32];
     int widest;
 };
@@ -121,7 +131,6 @@ __device__ __forceinline__ void plan_tables(const PlanParams &p, PlanShared &sh)
     if (threadIdx.x == 0) {
         p.plan.header[0] = ntiles;
         p.plan.header[1] = sh.widest;
-        p.plan.header[2] = total;
     }
     for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
         // the last expert whose first tile is at or before q (one without
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanP
         const int nt = lead ? (count + p.cut.tile - 1) / p.cut.tile : 0;
         s_lead[i] = lead ? e : 0x7fffffff;
         s_tiles[i] = nt;
-        const int total = __syncthreads_count(e >= 0);
+        __syncthreads();
         if (lead) {
             int first = 0;
             for (int j = 0; j < p.pairs; ++j) first += s_lead[j] < e ? s_tiles[j] : 0;
@@ -203,7 +212,6 @@ __global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanP
         if (i == 0) {
             p.plan.header[0] = s_ntiles;
             p.plan.header[1] = s_widest;
-            p.plan.header[2] = total;
         }
     } else {
         __syncthreads();
@@ -217,80 +225,85 @@ __global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanP
     if (bad) atomicOr(p.err, DEVERR_RANGE);
 }
 
-// Many pairs: one CTA.  A pair's rank among its expert's is the counter's
-// value when it came (a few experts: counted by warp ballots, so that the
-// counters are not hit 32 times a warp).
-__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const PlanParams p) {
+// Many pairs: a CTA counts a chunk's pairs by expert; a pair's rank in the
+// chunk is the counter's value when it came.
+__global__ void __launch_bounds__(kChunkThreads) moe_count_kernel(const PlanParams p) {
+    __shared__ int s_count[moe::kMaxExperts];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    for (int e = threadIdx.x; e < p.experts; e += kChunkThreads) s_count[e] = 0;
+    __syncthreads();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
+    for (int j = threadIdx.x; j < p.chunk; j += kChunkThreads) {
+        const int64_t i = i0 + j;
+        if (i >= p.pairs) break;
+        const int e = p.idx[i];
+        p.plan.pos[i] = e >= 0 && e < p.experts ? atomicAdd(&s_count[e], 1) : -1;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kChunkThreads)
+        p.plan.hist[static_cast<int64_t>(blockIdx.x) * p.experts + e] = s_count[e];
+}
+
+// One CTA: the tables, and in place of each chunk's count of an expert the
+// sorted row of the chunk's first pair there.  Up to 32 threads an expert,
+// each a run of chunks.
+__global__ void __launch_bounds__(kPlanThreads) moe_scan_kernel(const PlanParams p) {
     __shared__ PlanShared sh;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    constexpr int kBatch = 8;   // index loads in flight a thread
-    const int lane = threadIdx.x & 31;
+    const int per = min(32, kPlanThreads / p.experts);
+    const int e = threadIdx.x % p.experts, g = threadIdx.x / p.experts;
+    const bool on = g < per;
+    const int c0 = on ? p.chunks * g / per : 0, c1 = on ? p.chunks * (g + 1) / per : 0;
     sh.count[threadIdx.x] = 0;
     if (threadIdx.x == 0) sh.widest = 0;
+    int sum = 0;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += p.plan.hist[static_cast<int64_t>(c) * p.experts + e];
+    sh.part[threadIdx.x] = sum;
     __syncthreads();
-    auto load = [&](int i) {
-        const int e = i < p.pairs ? p.idx[i] : -1;
-        return e < p.experts ? e : -1;
-    };
-    for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x) < p.pairs; i0 += kBatch * kPlanThreads) {
-        int e[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) e[b] = load(i0 + b * kPlanThreads);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kPlanThreads;
-            int rank = 0;
-            if (p.experts <= 16) {
-                for (int x = 0; x < p.experts; ++x) {
-                    const unsigned m = __ballot_sync(0xffffffffu, e[b] == x);
-                    int base = 0;
-                    if (m && lane == 0) base = atomicAdd(&sh.count[x], __popc(m));
-                    base = __shfl_sync(0xffffffffu, base, 0);
-                    if (e[b] == x) rank = base + __popc(m & ((1u << lane) - 1u));
-                }
-            } else if (e[b] >= 0) {
-                rank = atomicAdd(&sh.count[e[b]], 1);
-            }
-            if (i < p.pairs) p.plan.pos[i] = e[b] >= 0 ? rank : -1;
-        }
+    int before = 0;
+    if (on) {
+        for (int q = 0; q < g; ++q) before += sh.part[q * p.experts + e];
+        if (g == per - 1) sh.count[e] = before + sum;
     }
     __syncthreads();
     plan_tables(p, sh);
-    for (int i0 = threadIdx.x; i0 < p.pairs; i0 += kBatch * kPlanThreads) {
-        int e[kBatch], rank[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kPlanThreads;
-            e[b] = load(i);
-            rank[b] = i < p.pairs ? p.plan.pos[i] : -1;   // written by this thread above
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kPlanThreads;
-            if (i >= p.pairs || e[b] < 0) continue;
-            const int at = sh.row0[e[b]] + rank[b];
-            p.plan.pos[i] = at;
-            p.plan.row_token[at] = i / p.k;
-        }
+    int row = sh.row0[e] + before;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+        int *h = p.plan.hist + static_cast<int64_t>(c) * p.experts + e;
+        const int n = *h;
+        *h = row;
+        row += n;
     }
 }
 
-// The sorted copy of x's rows, after moe_plan_kernel: a row per CTA.
+// A warp per pair: its sorted row, and x's row copied there.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const PlanParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int r = blockIdx.x;
-    if (r >= p.plan.header[2]) return;
-    const uint4 *src = static_cast<const uint4 *>(p.x) + static_cast<int64_t>(p.plan.row_token[r]) * p.nvec;
-    uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(r) * p.nvec;
+    const int lane = threadIdx.x & 31;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (i >= p.pairs) return;
+    const int rank = p.plan.pos[i];
+    if (rank < 0) return;
+    const int at = p.plan.hist[i / p.chunk * p.experts + p.idx[i]] + rank;
+    __syncwarp();   // every lane has read the rank
+    if (lane == 0) p.plan.pos[i] = at;
+    const uint4 *src = static_cast<const uint4 *>(p.x) + i / p.k * p.nvec;
+    uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(at) * p.nvec;
     bool bad = false;
-    for (int c0 = threadIdx.x; c0 < p.nvec; c0 += 2 * blockDim.x) {
-        const int c1 = c0 + blockDim.x;
-        const uint4 a = src[c0], b = c1 < p.nvec ? src[c1] : make_uint4(0, 0, 0, 0);
-        dst[c0] = convert_vec<T>(p, a, bad);
-        if (c1 < p.nvec) dst[c1] = convert_vec<T>(p, b, bad);
+    for (int v0 = lane; v0 < p.nvec; v0 += 8 * 32) {
+        uint4 v[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            if (v0 + 32 * b < p.nvec) v[b] = src[v0 + 32 * b];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            if (v0 + 32 * b < p.nvec) dst[v0 + 32 * b] = convert_vec<T>(p, v[b], bad);
     }
     if (bad) atomicOr(p.err, DEVERR_RANGE);
 }
@@ -354,11 +367,17 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p)
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
+size_t hist_bytes(int64_t pairs, int64_t experts) {
+    if (pairs <= kSmallPairs) return 0;
+    const int64_t chunk = chunk_pairs(pairs);
+    return align256(static_cast<size_t>((pairs + chunk - 1) / chunk) * experts * sizeof(int));
+}
+
 }  // namespace
 
 size_t moe_plan_bytes(int64_t pairs, int64_t experts, int tile) {
     return 256 + align256(static_cast<size_t>(moe::max_tiles(pairs, experts, tile)) * sizeof(Tile)) +
-           2 * align256(static_cast<size_t>(pairs) * sizeof(int));
+           hist_bytes(pairs, experts) + align256(static_cast<size_t>(pairs) * sizeof(int));
 }
 
 Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile) {
@@ -368,8 +387,8 @@ Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile) {
     b += 256;
     p.tiles = reinterpret_cast<Tile *>(b);
     b += align256(static_cast<size_t>(moe::max_tiles(pairs, experts, tile)) * sizeof(Tile));
-    p.row_token = reinterpret_cast<int *>(b);
-    b += align256(static_cast<size_t>(pairs) * sizeof(int));
+    p.hist = reinterpret_cast<int *>(b);
+    b += hist_bytes(pairs, experts);
     p.pos = reinterpret_cast<int *>(b);
     return p;
 }
@@ -389,12 +408,15 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t s) {
     }
     {
         LaunchScope scope(K_MOE_PLAN, s);
-        e = launch_dependent(moe_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+        e = launch_dependent(moe_count_kernel, dim3(static_cast<unsigned>(p.chunks)), dim3(kChunkThreads), 0, s, p);
+    }
+    if (e == cudaSuccess) {
+        LaunchScope scope(K_MOE_PLAN, s);
+        e = launch_dependent(moe_scan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
     }
     if (e != cudaSuccess) return e;
-    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(256, (p.nvec + 31) / 32 * 32));
     LaunchScope scope(K_MOE_PLAN, s);
-    e = launch_dependent(moe_gather_kernel<T>, dim3(static_cast<unsigned>(p.pairs)), dim3(threads), 0, s, p);
+    e = launch_dependent(moe_gather_kernel<T>, dim3(static_cast<unsigned>((p.pairs + 7) / 8)), dim3(256), 0, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -412,6 +434,8 @@ cudaError_t launch_moe_plan(const int32_t *idx, int64_t rows, int k, int experts
     p.x = x;
     p.xs = xs;
     p.nvec = static_cast<int>(d / 8);
+    p.chunk = static_cast<int>(chunk_pairs(p.pairs));
+    p.chunks = (p.pairs + p.chunk - 1) / p.chunk;
     p.to_f16 = to_f16;
     p.perm = perm;
     p.err = device_status_word();
