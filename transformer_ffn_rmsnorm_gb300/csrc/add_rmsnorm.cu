@@ -281,10 +281,12 @@ cudaError_t launch_out(const AddNormParams &p, cudaStream_t s) {
         e = launch_dependent(add_rmsnorm_generic_kernel<T, OUT>, grid, dim3(256), 0, s, p);
     } else {
         // few rows: as many threads as the row has vectors (shortest path to
-        // the answer); many rows: two vectors a thread, more CTAs an SM
-        const int want = p.rows <= 2 * static_cast<int64_t>(sm_count()) ? 1 : 2;
-        int vpt = 1;
-        while (vpt < want || nvec > vpt * 1024) vpt <<= 1;
+        // the answer); many rows: four vectors a thread, which keeps most bytes in
+        // flight for a CTA's barrier (16384 x 4096 fp16 to e4m3: one vector
+        // 106, two 73, four 69 us; copy speed is 69).  At 64 registers a
+        // thread: with g kept as well (128) four were slower than two.
+        int vpt = p.rows <= 2 * static_cast<int64_t>(sm_count()) ? 1 : 4;
+        while (nvec > vpt * 1024) vpt <<= 1;
         const dim3 block(static_cast<unsigned>(((nvec + vpt - 1) / vpt + 31) / 32 * 32));
         switch (vpt) {
             case 1: e = launch_dependent(add_rmsnorm_kernel<T, 1, OUT>, grid, block, 0, s, p); break;
