@@ -187,9 +187,11 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
  *   FFN_PREPARED_WEIGHTS the weights are ffn_prepare_weights output (fp16 of
  *   w * 2^8) and the products run on fp16 operands: a bf16 x must lie in
  *   fp16's range (a finite value beyond it becomes infinite and records
- *   FFN_ERR_RANGE in the device status word), and |h| below 1.6e7.  No other flag.
- *   h = silu(G) * U is rounded once to the operand type; everything else is
- *   fp32, results are added in slot order and rounded once.
+ *   FFN_ERR_RANGE in the device status word), and |h| below 1.6e7.  No other
+ *   flag.
+ *   h = silu(G) * U is rounded once to the operand type (FFN_F16 without
+ *   prepared weights: |h| up to 65504); everything else is fp32, a token's
+ *   results are added in slot order, then res, and rounded once.
  *   d % 8 == 0, ffn % 8 == 0, 1 <= experts <= 1024, 1 <= k <= 32; rows * k,
  *   experts * d and experts * ffn at most 2^30.  rows == 0 launches nothing.
  *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned (sorted
