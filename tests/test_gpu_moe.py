@@ -228,6 +228,39 @@ def test_captured_with_other_experts_at_replay(env):
         assert torch.equal(y1, ffn.ffn_moe_forward(x2[:1], idx2[:1], w2[:1], wg, wu, wd))
 
 
+@pytest.mark.parametrize("rows,d,f,experts,k", [(40000, 64, 72, 100, 8), (5000, 64, 64, 1000, 4), (64, 64, 64, 1024, 32),
+                                                (300, 64, 64, 7, 1), (70000, 8, 8, 3, 2), (2, 4096, 8, 3, 3)])
+def test_many_pairs_and_many_experts(env, rows, d, f, experts, k):
+    """Chunks of more than 256 pairs, a thread an expert in the scan, fewer
+    pairs than experts, tiny and lopsided sizes; skipped slots among them."""
+    torch, _ = env
+    args = list(make(torch, rows, d, f, experts, k, torch.float16))
+    args[1][::7, 0] = -1
+    run(env, args)
+
+
+def test_host_threads(env):
+    """Calls from several host threads, each on its own stream and workspace."""
+    import threading
+    torch, ffn = env
+    sets = [make(torch, 40 * (i + 1), 256, 512, 4, 2, torch.bfloat16, seed=i) for i in range(4)]
+    want = [ffn.ffn_moe_forward(*a[:6], res=a[6]) for a in sets]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i] = ffn.ffn_moe_forward(*sets[i][:6], res=sets[i][6], stream=s)
+        s.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 @pytest.mark.parametrize("rows,experts", [(96, 2), (128, 3), (40, 1), (20, 8), (300, 4)])
 def test_many_calls_in_a_row(env, rows, experts):
     """Calls queued back to back: each one's kernels start while the ones

@@ -207,6 +207,35 @@ def test_repeatable_streams_and_graph(env):
     check(torch, y, *reference(torch, x, idx, w, values, res))
 
 
+@pytest.mark.parametrize("rows,d,f,experts,k", [(9000, 32, 64, 40, 4), (30, 32, 32, 500, 8), (400, 96, 32, 3, 1),
+                                                (1, 4096, 96, 2, 2)])
+def test_many_calls_in_a_row(env, rows, d, f, experts, k):
+    """Rows of one to a few 128-value groups, so that every unit is one stage or
+    two and the rings turn fast; queued back to back."""
+    torch, ffn = env
+    x, idx, w, packed, values, res = make(torch, rows, d, f, experts, k)
+    want = run(env, (x, idx, w, packed, values, res))
+    ws = ffn.workspace(ffn.ffn_moe_q4_workspace_bytes(rows, d, f, experts, k), "cuda")
+    y = torch.empty_like(x)
+    for _ in range(300):
+        ffn.ffn_moe_forward_q4(x, idx, w, *packed, ffn=f, res=res, out=y, ws=ws)
+    torch.cuda.synchronize()
+    ffn.ffn_device_status()
+    assert torch.equal(y, want)
+
+
+def test_range_is_reported(env):
+    torch, ffn = env
+    from transformer_ffn_rmsnorm_gb300 import _lib
+    x, idx, w, packed, values, res = make(torch, 4, 64, 64, 4, 2)
+    ffn.ffn_device_status()
+    x[2, 3] = -1e6
+    ffn.ffn_moe_forward_q4(x, idx, w, *packed, ffn=64)
+    with pytest.raises(ffn.FFNError) as err:
+        ffn.ffn_device_status()
+    assert err.value.status == _lib.FFN_ERR_RANGE
+
+
 def test_refused(env):
     torch, ffn = env
     x, idx, w, packed, values, res = make(torch, 4, 64, 64, 4, 2)

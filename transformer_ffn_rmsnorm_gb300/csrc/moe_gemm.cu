@@ -23,6 +23,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "moe.cuh"
@@ -304,7 +305,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
                    cudaStream_t s) {
     constexpr int kFRows = MODE == GATEUP ? 128 : 256;
     const auto kern = &moe_gemm_kernel<MODE, BF16>;
-    static int configured_device = -1, slots = 0;   // co-resident CTA pairs
+    static std::atomic<int> configured_device{-1}, pair_slots{0};   // (host threads may call at the same time)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -319,7 +320,10 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = attr;
-    if (configured_device != dev) {
+    int slots = 0;   // co-resident CTA pairs
+    if (configured_device.load(std::memory_order_acquire) == dev) {
+        slots = pair_slots.load(std::memory_order_relaxed);
+    } else {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
@@ -327,7 +331,8 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
         e = cudaOccupancyMaxActiveClusters(&slots, kern, &cfg);
         if (e != cudaSuccess) return e;
         if (slots < 1) return cudaErrorLaunchOutOfResources;
-        configured_device = dev;
+        pair_slots.store(slots, std::memory_order_relaxed);
+        configured_device.store(dev, std::memory_order_release);
     }
     Params p{};
     p.header = plan.header;

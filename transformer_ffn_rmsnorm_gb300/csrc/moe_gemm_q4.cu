@@ -35,6 +35,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "moe.cuh"
 
@@ -473,14 +474,14 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
                    const uint16_t *s0, const uint16_t *s1, int splits, int64_t pairs, int64_t experts, int64_t wrows,
                    int64_t K, void *out, float acc_scale, float out_scale, cudaStream_t s) {
     const auto kern = &moe_gemm_q4_kernel<MODE>;
-    static int configured_device = -1;
+    static std::atomic<int> configured_device{-1};   // (host threads may call at the same time)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (configured_device != dev) {
+    if (configured_device.load(std::memory_order_acquire) != dev) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
         if (e != cudaSuccess) return e;
-        configured_device = dev;
+        configured_device.store(dev, std::memory_order_release);
     }
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;
     Params p{};

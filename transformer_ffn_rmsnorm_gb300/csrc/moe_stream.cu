@@ -18,6 +18,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "moe.cuh"
@@ -252,14 +253,14 @@ cudaError_t launch(const Plan &plan, const void *w0, const void *w1, const void 
                    cudaStream_t s) {
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;
     const auto kern = &moe_stream_kernel<MODE, BF16>;
-    static int configured_device = -1;
+    static std::atomic<int> configured_device{-1};   // (host threads may call at the same time)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (configured_device != dev) {
+    if (configured_device.load(std::memory_order_acquire) != dev) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
         if (e != cudaSuccess) return e;
-        configured_device = dev;
+        configured_device.store(dev, std::memory_order_release);
     }
     CUtensorMap m0, m1;
     moe::RowMaps mb;
