@@ -7,19 +7,23 @@
 // A unit of work is 128 weight rows (gate/up: 64 rows of W_gate and the same
 // 64 of W_up) of one expert against one token tile of n <= 128 columns, the
 // weights on the M side as in moe_gemm.cu.  The weights travel HBM -> shared
-// memory as 4 bits (TMA, 128 bytes of a row, the values of two stages; their scales, whose
-// row pitch need not be a multiple of 16 bytes, by cp.async), from
-// there through registers, where they become fp16, into tensor
-// memory (tcgen05.st), and tcgen05.mma takes its A operand from there.  Through
-// shared memory the fp16 form would cost 4 bytes a weight (stored and read
-// back) beside the 0.6 of the 4-bit form; so it costs none.
+// memory as 4 bits (a stage is 256 values: TMA, 128 bytes of a row; their
+// scales, whose row pitch need not be a multiple of 16 bytes, by cp.async),
+// from there through registers, where they become fp16, into tensor memory
+// (tcgen05.st), and tcgen05.mma takes its A operand from there.  Through shared
+// memory the fp16 form would cost 4 bytes a weight (stored and read back)
+// beside the 0.6 of the 4-bit form; so it costs none.
 //
-// What bounds it: few tokens: HBM, if the dequantisation keeps up.  A stage (128 rows of 128
-// values, 9 KB) is 430 cycles of this SM's share of HBM; its dequantisation is four
-// warps of about 260 instructions, and the wait, the loads, the arithmetic and
-// the store of one warp follow one another, so two groups of four warps
-// take stages in turn, one of each group to a scheduler (a third changed nothing).  More tokens: the activations from L2 (32 KB a
-// stage at 128 columns), then the tensor pipe.
+// What bounds it: few tokens: HBM, if the dequantisation keeps up.  A stage
+// (128 rows of 256 values, 18 KB) is 860 cycles of this SM's share of HBM; its
+// dequantisation is four warps of about 520 instructions, and the wait, the
+// loads, the arithmetic and the store of one warp follow one another, so two
+// groups of four warps take stages in turn, one of each group to a scheduler.
+// Stages of 128 values cost the issuing warp and the barriers as much a stage
+// (16 tokens, 4096 -> 14336, 8 experts: gate/up 143 us, 115 with 256; down 80
+// and 68).  More tokens: the activations from L2 (64 KB a stage at 128
+// columns), then the tensor pipe (3000 tokens: 1052 -> 978 and 553 -> 518 us;
+// rows of 1408 values, whose sixth stage is half empty, down 167 -> 173).
 //
 // Arithmetic: a nibble pair becomes fp16 1024 + u (or 1024 + 16 u, the high
 // nibbles where they stand), u - 8 exactly by one subtraction (one fma), and
@@ -30,8 +34,8 @@
 //
 // Roles: warp 0 loads nibbles, warp 3 scales, warp 2 tokens; warp 1 issues the
 // MMAs; warps 4-11 dequantise (warp w fills TMEM lanes 32 (w % 4) .. of every
-// second stage); warps 12-15 are the epilogue.  Every wait is
-// bounded (1 s) as in gemm_tcgen05.cu.
+// second stage); warps 12-15 are the epilogue.  Every wait is bounded (1 s) as
+// in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -45,25 +49,32 @@ namespace {
 using moe::Plan;
 using moe::Unit;
 
-constexpr int kRows = 128, kK = 128, kTile = kMoeCutQ4.tile, kGran = kMoeCutQ4.gran;
-constexpr uint32_t kRawBytes = kRows * 128, kScaleBytes = kRows * 16;   // nibbles and scales of two stages' values
-constexpr uint32_t kBBytes = kTile * kK * 2;                            // room for a stage's tokens
-constexpr int kRawStages = 6, kStages = 3;   // a stage: A in tensor memory, tokens in shared memory, one barrier
-constexpr uint32_t kRawOff = kStages * kBBytes;
-constexpr uint32_t kScaleOff = kRawOff + kRawStages * kRawBytes;
-constexpr size_t kSmemBytes = kScaleOff + kRawStages * kScaleBytes + 1024;
+constexpr int kRows = 128, kK = 256, kTile = kMoeCutQ4.tile, kGran = kMoeCutQ4.gran;
+constexpr uint32_t kRawBytes = kRows * 128, kScaleBytes = kRows * 16;   // nibbles and scales of a stage (256 values)
+// Two rings: the stages (A in tensor memory, tokens in shared memory, one
+// barrier for both) and the raw slots (nibbles and scales).  Where no tile of
+// the call is wider than 64 columns they are three and six long, else two and
+// four: what 512 columns of tensor memory and 227 KB hold.
+constexpr int kNarrow = 64;
+constexpr int kMaxStages = 3, kMaxRaw = 6, kMinStages = 2, kMinRaw = 4;
+constexpr uint32_t rings_bytes(int tile, int stages, int raw) {
+    return stages * tile * kK * 2 + raw * (kRawBytes + kScaleBytes);
+}
+constexpr size_t kSmemBytes =
+    std::max(rings_bytes(kNarrow, kMaxStages, kMaxRaw), rings_bytes(kTile, kMinStages, kMinRaw)) + 1024;
 static_assert(kSmemBytes > 114 * 1024 && kSmemBytes < 218 * 1024,
               "one CTA per SM (each allocates all of tensor memory), beside 8 KB of static shared memory");
-constexpr uint32_t kACol = 256, kAColsPerStage = 64;   // columns 0-255: two accumulators; then the A stages
+constexpr uint32_t kACols = 128;   // tensor memory columns of a stage's A, after the two accumulators
 constexpr int kDequantWarps = 4, kGroups = 2, kEpiWarps = 4;   // warps of a stage; groups of them taking turns
 constexpr int kThreads = 32 * (4 + kGroups * kDequantWarps + kEpiWarps);
 // A wait tells phases apart by parity alone, so no group may come to a barrier
 // a phase too early.  A group that comes for stage m has stored stage m -
 // kGroups, for which the MMAs had consumed every stage up to m - kGroups -
-// kStages: the slot's use before the last (m - 2 kStages) and the raw slot's
-// last use (m - kRawStages where raw slots hold a single stage, as in rows of
-// one group) must be among those.
-static_assert(kGroups <= kStages && kGroups + kStages <= kRawStages, "waits by parity");
+// slots: the slot's use before the last (m - 2 slots) and the raw slot's last
+// use (m - raws) must be among those.
+static_assert(kGroups <= kMinStages && kGroups <= kMaxStages && kGroups + kMaxStages <= kMaxRaw &&
+                  kGroups + kMinStages <= kMinRaw,
+              "waits by parity");
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 enum Mode { GATEUP = 0, DOWN = 1 };
@@ -138,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ moe::RowMaps maps_b, const Params p) {
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;   // features of a unit
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_rfull[kRawStages], bar_rempty[kRawStages];
-    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
+    __shared__ __align__(8) uint64_t bar_rfull[kMaxRaw], bar_rempty[kMaxRaw];
+    __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
     __shared__ float s_swap[MODE == GATEUP ? 2 : 1][2][8][64];
     __shared__ uint32_t s_tmem_base;
@@ -149,11 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     auto bar = [](uint64_t *b) { return ptx::smem_u32(b); };
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRawStages; ++s) {
+        for (int s = 0; s < kMaxRaw; ++s) {
             ptx::mbar_init(bar(&bar_rfull[s]), 1 + 32);        // the nibbles' bytes, the scale warp's lanes
-            ptx::mbar_init(bar(&bar_rempty[s]), 2 * kDequantWarps);   // of both halves
+            ptx::mbar_init(bar(&bar_rempty[s]), kDequantWarps);
         }
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(bar(&bar_full[s]), 1 + kDequantWarps);   // the tokens' bytes, the weights' warps
             ptx::mbar_init(bar(&bar_empty[s]), 1);
         }
@@ -185,13 +196,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     ptx::griddep_wait();   // the plan, x, h: written by kernels before this one
-    // unit v is split v % splits of tile unit v / splits: raw slots [lo, hi) of
-    // two stages each, but for an odd row's last
+    // unit v is split v % splits of tile unit v / splits: stages [lo, hi); an
+    // odd row's last stage has 128 values
     const int units = __ldcg(p.header) * p.nf * p.splits;
-    const int nraw = (p.ngrp + 1) / 2;
-    auto lo_of = [&](int v) { return nraw * (v % p.splits) / p.splits; };
-    auto hi_of = [&](int v) { return nraw * (v % p.splits + 1) / p.splits; };
-    auto stages_of = [&](int v) { return min(2 * hi_of(v), p.ngrp) - 2 * lo_of(v); };
+    const int nst = (p.ngrp + 1) / 2;
+    auto lo_of = [&](int v) { return nst * (v % p.splits) / p.splits; };
+    auto hi_of = [&](int v) { return nst * (v % p.splits + 1) / p.splits; };
+    auto half_of = [&](int st) { return 2 * st + 1 == p.ngrp; };
+    const bool narrow = __ldcg(p.header + 1) <= kNarrow;
+    const int slots = narrow ? kMaxStages : kMinStages, raws = narrow ? kMaxRaw : kMinRaw;
+    const uint32_t acc_cols = narrow ? kNarrow : kTile, a_col = 2 * acc_cols;
+    // 64 values of a stage's tokens (at most kNarrow or kTile columns); all of them
+    const uint32_t b_sub = (narrow ? kNarrow : kTile) * 128, b_slot = 4 * b_sub;
+    const uint32_t raw_off = slots * b_slot, scale_off = raw_off + raws * kRawBytes;
     auto walk_units = [&]() { return moe::Walk<kGran>(p.tiles, p.nf, p.splits, units, u0, ustep); };
 
     if (warp == 0) {
@@ -209,14 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (ptx::elect_one()) {
-                    const uint32_t full = bar(&bar_rfull[s]), dst = base + kRawOff + s * kRawBytes;
+                    const uint32_t full = bar(&bar_rfull[s]), dst = base + raw_off + s * kRawBytes;
                     ptx::mbar_arrive_expect_tx(full, kRawBytes);
                     ptx::tma_load_2d(dst, &map_w0, full, r * 128, wrow);   // past the row's end zero fill
                     if (MODE == GATEUP) ptx::tma_load_2d(dst + kRawBytes / 2, &map_w1, full, r * 128, wrow);
                 }
                 __syncwarp();
                 ++produced;
-                if (++s == kRawStages) {
+                if (++s == raws) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -243,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t dst = base + kScaleOff + s * kScaleBytes + lane * 16;
-                const bool last = 2 * r + 1 == p.ngrp;   // one stage, and no more scales in the row
+                const uint32_t dst = base + scale_off + s * kScaleBytes + lane * 16;
+                const bool last = half_of(r);   // no more scales in the row
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (wide) {
@@ -255,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 cp_async_arrive(bar(&bar_rfull[s]));
-                if (++s == kRawStages) {
+                if (++s == raws) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -269,25 +286,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = walk.at(u);
-            for (int g = 2 * lo_of(u), ge = g + stages_of(u); g < ge; ++g) {
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 if (ptx::elect_one()) {
-                    const uint32_t full = bar(&bar_full[s]);
-                    ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * kK * 2);
+                    const uint32_t full = bar(&bar_full[s]), dst = base + s * b_slot;
+                    const int nsub = half_of(g) ? 2 : 4;
+                    ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(t.n) * 128 * nsub);
+                    moe::for_row_boxes(maps_b, t.n, [&](const CUtensorMap *m, int r) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)   // 64 values each; past the row's end zero fill
-                        moe::for_row_boxes(maps_b, t.n, [&](const CUtensorMap *m, int r) {
-                            ptx::tma_load_2d(base + s * kBBytes + j * (kBBytes / 2) + r * 128, m, full, g * kK + j * 64,
-                                             t.row0 + r);
-                        });
+                        for (int j = 0; j < 4; ++j)   // 64 values each; past the row's end zero fill
+                            if (j < nsub)
+                                ptx::tma_load_2d(dst + j * b_sub + r * 128, m, full, g * kK + j * 64, t.row0 + r);
+                    });
                 }
                 __syncwarp();
                 ++produced;
-                if (++s == kStages) {
+                if (++s == slots) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -295,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // -------------------------------------------------- MMA issuer
-        // (the next stage's barrier is looked at before this stage's MMAs are
-        // issued: a wait that has nothing to wait for costs 100 cycles, as
-        // much as four of them)
+        // (256 values at a time, and the next stage's barrier is looked at
+        // before this stage's MMAs are issued: going round once costs some 400
+        // cycles beside the MMAs, what 128 values may take)
         int s = 0, acc = 0;
         uint32_t ph = 0, pacc = 0;
         bool ready = false;
@@ -310,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            const uint32_t d = tmem + acc * 128;
-            const int n = stages_of(u);
-            for (int g = 0; g < n; ++g) {
+            const uint32_t d = tmem + acc * acc_cols;
+            const int g0 = lo_of(u), ge = hi_of(u);
+            for (int g = g0; g < ge; ++g) {
                 if (!__all_sync(0xffffffffu, ready)) {
                     got = ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, kWaitNs);
                     if (!__all_sync(0xffffffffu, got)) {
@@ -322,19 +340,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const int at = s;
-                if (++s == kStages) {
+                if (++s == slots) {
                     s = 0;
                     ph ^= 1u;
                 }
                 ready = ptx::mbar_test(bar(&bar_full[s]), ph);
                 if (ptx::elect_one()) {
-                    const uint32_t a = tmem + kACol + at * kAColsPerStage;
-                    const uint64_t bd = ptx::sdesc_k_sw128(base + at * kBBytes);
+                    const uint32_t a = tmem + a_col + at * kACols;
+                    const uint64_t bd = ptx::sdesc_k_sw128(base + at * b_slot);
+                    const uint32_t sub = b_sub >> 4;
 #pragma unroll
-                    for (int k = 0; k < kK / 16; ++k)   // 32 bytes of k further: 2 in the address field
-                        mma_ts(d, a + 8 * k, bd + (k >> 2) * (kBBytes / 32) + 2 * (k & 3), idesc, (g | k) != 0);
+                    for (int k = 0; k < 8; ++k)   // 32 bytes of k further: 2 in the address field
+                        mma_ts(d, a + 8 * k, bd + (k >> 2) * sub + 2 * (k & 3), idesc, g != g0 || k != 0);
+                    if (!half_of(g)) {
+#pragma unroll
+                        for (int k = 8; k < 16; ++k)
+                            mma_ts(d, a + 8 * k, bd + (k >> 2) * sub + 2 * (k & 3), idesc, true);
+                    }
                     ptx::tc_commit(bar(&bar_empty[at]));
-                    if (g == n - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
+                    if (g == ge - 1) ptx::tc_commit(bar(&bar_tfull[acc]));
                 }
                 __syncwarp();
             }
@@ -351,68 +375,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this warp's rows are 32q .. 32q + 31; its group takes every kGroups-th stage
         const int q = warp & 3, group = (warp - 4) / kDequantWarps;
         const int row = 32 * q + lane;
-        const uint32_t a0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + kACol;
-        uint32_t raw0 = 0, stage0 = 0;   // raw slots and stages of the units before
-        uint32_t mine = group;           // this group's next stage
+        const uint32_t a0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + a_col;
+        int turn = 0, s = 0, slot = 0;   // of the next stage: whose it is, its raw and its ring slot
+        uint32_t ph = 0, pslot = 0;
         for (int u = u0; u < units && ok; u += ustep) {
-            const int n = stages_of(u);
-            for (; mine < stage0 + n; mine += kGroups) {
-                const int i = static_cast<int>(mine - stage0);
-                const uint32_t raw = raw0 + (i >> 1), s = raw % kRawStages, slot = mine % kStages;
-                bool got = ptx::mbar_wait(bar(&bar_rfull[s]), (raw / kRawStages) & 1u, abort_flag, kWaitNs);
+            for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
+                const bool mine = turn == group;
+                const int cs = s, cslot = slot;
+                const uint32_t cph = ph, cpslot = pslot;
+                if (++turn == kGroups) turn = 0;
+                if (++s == raws) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++slot == slots) {
+                    slot = 0;
+                    pslot ^= 1u;
+                }
+                if (!mine) continue;
+                bool got = ptx::mbar_wait(bar(&bar_rfull[cs]), cph, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                const uint32_t src = base + kRawOff + s * kRawBytes + row * 128;
-                uint4 w[4];   // words of canonical bytes 4t .. 4t + 3 of the four blocks
+                const uint32_t src = base + raw_off + cs * kRawBytes + row * 128;
+                const uint32_t to = a0 + cslot * kACols;
+                const int halves = half_of(g) ? 1 : 2;
+                uint32_t sc[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(sc[0]), "=r"(sc[1]), "=r"(sc[2]), "=r"(sc[3])
+                             : "r"(base + scale_off + cs * kScaleBytes + row * 16));
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[t].x), "=r"(w[t].y), "=r"(w[t].z), "=r"(w[t].w)
-                                 : "r"(src + (((4 * (i & 1) + t) ^ (row & 7)) << 4)));
-                uint32_t sc[2];
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                             : "=r"(sc[0]), "=r"(sc[1])
-                             : "r"(base + kScaleOff + s * kScaleBytes + row * 16 + 8 * (i & 1)));
-                __syncwarp();
-                if (lane == 0) {   // everything is in registers; a slot with one stage is released for both
-                    ptx::mbar_arrive(bar(&bar_rempty[s]));
-                    if (i == n - 1 && (n & 1)) ptx::mbar_arrive(bar(&bar_rempty[s]));
-                }
-                // all of the arithmetic before the wait: a slot's way round (MMAs,
-                // release, store, MMAs) is what the products wait for otherwise
-                uint32_t o[2][32];
+                for (int hh = 0; hh < 2; ++hh) {   // 128 values
+                    if (hh >= halves) break;
+                    uint4 w[4];   // words of canonical bytes 4t .. 4t + 3 of the four blocks
 #pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    const __half2 sp = *reinterpret_cast<const __half2 *>(&sc[blk >> 1]);
-                    const __half2 s2 = blk & 1 ? __high2half2(sp) : __low2half2(sp);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        uint32_t v[4];
-                        dequant_word(blk == 0 ? w[t].x : blk == 1 ? w[t].y : blk == 2 ? w[t].z : w[t].w, s2, v);
-                        uint32_t *to = &o[blk >> 1][16 * (blk & 1) + 2 * t];
-                        to[0] = v[0];
-                        to[1] = v[1];
-                        to[8] = v[2];
-                        to[9] = v[3];
+                    for (int t = 0; t < 4; ++t)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[t].x), "=r"(w[t].y), "=r"(w[t].z), "=r"(w[t].w)
+                                     : "r"(src + (((4 * hh + t) ^ (row & 7)) << 4)));
+                    if (hh == halves - 1) {   // everything is in registers
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(&bar_rempty[cs]));
                     }
+                    uint32_t o[2][32];
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk) {
+                        const __half2 sp = *reinterpret_cast<const __half2 *>(&sc[2 * hh + (blk >> 1)]);
+                        const __half2 s2 = blk & 1 ? __high2half2(sp) : __low2half2(sp);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            uint32_t v[4];
+                            dequant_word(blk == 0 ? w[t].x : blk == 1 ? w[t].y : blk == 2 ? w[t].z : w[t].w, s2, v);
+                            uint32_t *x = &o[blk >> 1][16 * (blk & 1) + 2 * t];
+                            x[0] = v[0];
+                            x[1] = v[1];
+                            x[8] = v[2];
+                            x[9] = v[3];
+                        }
+                    }
+                    if (hh == 0) {   // (the first half's arithmetic before the wait)
+                        got = ptx::mbar_wait(bar(&bar_empty[cslot]), cpslot ^ 1u, abort_flag, kWaitNs);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                    }
+                    __syncwarp();
+                    tmem_st_x32(to + 64 * hh, o[0]);
+                    tmem_st_x32(to + 64 * hh + 32, o[1]);
                 }
-                got = ptx::mbar_wait(bar(&bar_empty[slot]), ((mine / kStages) & 1u) ^ 1u, abort_flag, kWaitNs);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                tmem_st_x32(a0 + slot * kAColsPerStage, o[0]);
-                tmem_st_x32(a0 + slot * kAColsPerStage + 32, o[1]);
+                if (!ok) break;
                 tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(&bar_full[slot]));
+                if (lane == 0) ptx::mbar_arrive(bar(&bar_full[cslot]));
             }
-            stage0 += n;
-            raw0 += hi_of(u) - lo_of(u);
         }
     } else {
         // ---------------------------------------------------------- epilogue
@@ -429,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 128;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
             if constexpr (MODE == GATEUP)
                 moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<__half *>(p.out), s_swap,
                                                    0, 16, 1, p.acc_scale, p.out_scale);
@@ -453,14 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // loads still in flight (only after an abandoned wait) land before shared memory is released
     if (warp == 0 && lane == 0)
-        for (uint32_t s = 0; s < kRawStages; ++s)
-            if (produced > s)
-                ptx::mbar_wait(bar(&bar_rfull[s]), ((produced - s + kRawStages - 1) / kRawStages - 1) & 1u, never,
-                               kWaitNs);
+        for (int s = 0; s < raws; ++s)
+            if (produced > static_cast<uint32_t>(s))
+                ptx::mbar_wait(bar(&bar_rfull[s]), ((produced - s + raws - 1) / raws - 1) & 1u, never, kWaitNs);
     if (warp == 2 && lane == 0)
-        for (uint32_t s = 0; s < kStages; ++s)
-            if (produced > s)
-                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + kStages - 1) / kStages - 1) & 1u, never, kWaitNs);
+        for (int s = 0; s < slots; ++s)
+            if (produced > static_cast<uint32_t>(s))
+                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + slots - 1) / slots - 1) & 1u, never, kWaitNs);
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
@@ -491,7 +529,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     p.s1 = s1;
     p.nf = static_cast<int>((wrows + kFRows - 1) / kFRows);
     p.wrows = static_cast<int>(wrows);
-    p.ngrp = static_cast<int>((K + kK - 1) / kK);
+    p.ngrp = static_cast<int>((K + 127) / 128);
     p.splits = splits;
     p.split_stride = pairs * wrows;
     p.out = out;
@@ -507,7 +545,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
 
 // nibbles: 128 bytes of box_rows rows, rows of whole 128-value groups
 bool map_q4(CUtensorMap *m, const uint8_t *qs, int64_t K, int64_t rows, uint32_t box_rows) {
-    const int64_t pitch = 64 * ((K + kK - 1) / kK);
+    const int64_t pitch = 64 * ((K + 127) / 128);
     return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 128, box_rows,
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
