@@ -224,6 +224,29 @@ def test_many_calls_in_a_row(env, rows, d, f, experts, k):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("rows,d,f,experts,k", [(40, 640, 1408, 16, 1), (64, 2048, 4768, 24, 2), (700, 640, 4768, 12, 1),
+                                                (900, 1664, 672, 24, 2), (5, 1024, 8192, 4, 2), (66, 1056, 4064, 40, 3)])
+def test_long_rows_and_unequal_loads(env, rows, d, f, experts, k):
+    """A call's widest tile decides how many stages are in flight: even and odd
+    numbers of 128-value groups in a row, one expert with most of the tokens
+    beside many with one, a split reduction, several units one after another;
+    the same bits in every call, whether the weights come from memory or from
+    cache."""
+    torch, ffn = env
+    idx = torch.rand(rows, experts, generator=torch.Generator().manual_seed(rows)).topk(k, dim=1).indices
+    idx[experts:, 0] = experts // 2   # (a second slot may name it too)
+    x, idx, w, packed, values, res = make(torch, rows, d, f, experts, k, idx=idx.cuda())
+    want = run(env, (x, idx, w, packed, values, res))
+    flush = torch.empty(200 << 20, dtype=torch.uint8, device="cuda")
+    got = torch.empty(300, *x.shape, dtype=x.dtype, device="cuda")
+    for i in range(300):
+        if i % 2:
+            flush.fill_(i % 5)
+        ffn.ffn_moe_forward_q4(x, idx, w, *packed, ffn=f, res=res, out=got[i])
+    assert bool((got == want).all()), int((got != want).flatten(1).any(dim=1).sum())
+    ffn.ffn_device_status()
+
+
 def test_range_is_reported(env):
     torch, ffn = env
     from transformer_ffn_rmsnorm_gb300 import _lib

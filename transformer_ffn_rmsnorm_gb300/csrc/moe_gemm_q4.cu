@@ -414,10 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w[t].x), "=r"(w[t].y), "=r"(w[t].z), "=r"(w[t].w)
                                      : "r"(src + (((4 * hh + t) ^ (row & 7)) << 4)));
-                    if (hh == halves - 1) {   // everything is in registers
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar(&bar_rempty[cs]));
-                    }
                     uint32_t o[2][32];
 #pragma unroll
                     for (int blk = 0; blk < 4; ++blk) {
@@ -450,7 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(&bar_full[cslot]));
+                if (lane == 0) {
+                    // (the raw slot only here, where what was loaded from it has
+                    // been used: released right after the second half's loads,
+                    // with the first half's stores still in flight, it was
+                    // filled again before they were served, in up to a tenth
+                    // of the calls)
+                    ptx::mbar_arrive(bar(&bar_full[cslot]));
+                    ptx::mbar_arrive(bar(&bar_rempty[cs]));
+                }
             }
         }
     } else {
@@ -470,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
             if constexpr (MODE == GATEUP)
-                moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<__half *>(p.out), s_swap,
-                                                   0, 16, 1, p.acc_scale, p.out_scale);
+                moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<__half *>(p.out),
+                                                   s_swap, 0, 16, 1, p.acc_scale, p.out_scale);
             else
                 moe::store_epilogue(taddr, q, lane, t, p.wrows,
                                     static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
