@@ -352,7 +352,8 @@ ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64
     const bool stream = !q4 && m->pairs <= kMoeStreamRows * std::min(m->pairs, experts);
     m->cut = q4 ? kMoeCutQ4 : stream ? kMoeCutStream : kMoeCutPair;
     m->splits = q4 || stream ? moe_down_splits(m->pairs, experts, d, ffn) : 1;
-    if (moe::max_tiles(m->pairs, experts, m->cut.tile) * ((std::max(d, ffn) + 63) / 64) > most / 8) return FFN_ERR_SHAPE;
+    if (moe::max_tiles(m->pairs, experts, m->cut.tile) * ((std::max(d, ffn) + 63) / 64) > most / 8)
+        return FFN_ERR_SHAPE;
     const size_t p = static_cast<size_t>(m->pairs);
     m->plan = rows ? moe_plan_bytes(m->pairs, experts, m->cut.tile) : 0;
     m->xs = align256(p * d * 2);
@@ -431,7 +432,8 @@ ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *
                                     d, dtype, op != static_cast<int>(dtype), false, s);
     if (m.cut.tile == kMoeCutStream.tile) {
         if (e == cudaSuccess)
-            e = launch_moe_gateup_stream(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale, s);
+            e = launch_moe_gateup_stream(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale,
+                                         s);
         if (e == cudaSuccess)
             e = launch_moe_down_stream(op, plan, h, w_down, part, m.splits, m.pairs, d, ffn, experts,
                                        w_unscale / h_scale, s);
@@ -467,7 +469,8 @@ ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const floa
     ffn_status st = plan_moe(rows, d, ffn, experts, k, true, &m);
     if (st != FFN_OK) return st;
     if (rows == 0) return FFN_OK;
-    const size_t gd = static_cast<size_t>(experts) * ffn * q4_groups(d), gf = static_cast<size_t>(experts) * d * q4_groups(ffn);
+    const size_t gd = static_cast<size_t>(experts) * ffn * q4_groups(d),
+                 gf = static_cast<size_t>(experts) * d * q4_groups(ffn);
     const Range weights[6] = {{w_gate.qs, gd * 64}, {w_up.qs, gd * 64}, {w_down.qs, gf * 64},
                               {w_gate.scales, gd * 8}, {w_up.scales, gd * 8}, {w_down.scales, gf * 8}};
     st = check_moe(x, topk_idx, topk_w, weights, 6, res, y, rows, d, k, m, workspace, workspace_bytes);

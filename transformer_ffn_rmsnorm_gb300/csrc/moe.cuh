@@ -156,7 +156,8 @@ __device__ __forceinline__ void store_epilogue(uint32_t taddr, int q, int lane, 
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (f < wrows && c + i < t.valid) dst[static_cast<int64_t>(c + i) * wrows] = __uint_as_float(r[i]) * acc_scale;
+            if (f < wrows && c + i < t.valid)
+                dst[static_cast<int64_t>(c + i) * wrows] = __uint_as_float(r[i]) * acc_scale;
     }
 }
 
@@ -215,11 +216,9 @@ cudaError_t launch_moe_down_q4(const moe::Plan &plan, const void *h, const uint8
                                cudaStream_t s);
 
 // Splits of the down product's reduction on the single-CTA kernels (units of
-// 128 weight rows, stages of 128 values): with few experts in use the units
-// rarely fill whole waves of multiprocessors, and shorter ones waste less of
-// the last wave.  A function of the sizes alone, so that the workspace query
-// and the call agree: the fewest splits within 2 % of the least waves / splits,
-// at most 8 and none shorter than 4 stages.
+// 128 weight rows, stages of 128 values): at most 8, none shorter than 4
+// stages.  A function of the sizes alone, so that the workspace query and the
+// call agree.
 int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn);
 
 }  // namespace ffn

@@ -19,7 +19,8 @@
 //
 // Roles: warp 0 loads, warp 1 issues the MMAs (the even CTA's), warps 2-9 read
 // the accumulators (lane = weight row, column = token): for a fixed column a
-// warp's 32 lanes store 32 neighbouring features.  Every wait is bounded as in gemm_tcgen05.cu.
+// warp's 32 lanes store 32 neighbouring features.  Every wait is bounded as in
+// gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -223,7 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(p.err, DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&bar_drain), 0x1);   // every MMA ends before TMEM is freed
+        // every MMA ends before TMEM is freed
+        if (ptx::elect_one()) ptx::tc_commit_pair(ptx::smem_u32(&bar_drain), 0x1);
         ptx::mbar_wait(ptx::smem_u32(&bar_drain), 0, never, kWaitNs);
     } else if (warp >= 2) {
         // ---------------------------------------------------------- epilogue

@@ -456,10 +456,10 @@ cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *pa
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Splits of the down product's reduction: where few units leave a last round
-// part empty, splitting fills it, but a unit has a fixed cost (its epilogue,
-// the pipeline's fill: about three stages of 128 values) and every split a row
-// a pair for the combine kernel to add (about three, and the rows' traffic).
+// Where few units leave a last round part empty, splitting fills it, but a unit
+// has a fixed cost (its epilogue, the pipeline's fill: about a stage of 128
+// values) and every split a row a pair for the combine kernel to add (about
+// three stages, and the rows' traffic).
 // Down and combine of a call, 1 token, 4 of 32 Q4 experts of 5120 x 2176: one
 // split 28.8 us, two 28.1, three 27.9, four 32.3; 16 tokens, 2 of 8 of 4096 x
 // 14336: one 79.8, two 73.7, four 72.1, seven 78.5.
@@ -471,8 +471,8 @@ int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn) {
     double least = 0.;
     for (int s = 1; s <= 8 && stages / s >= 4; ++s) {
         const double rounds = static_cast<double>((units * s + kSms - 1) / kSms);
-        const double t = rounds * (static_cast<double>(stages) / s + 3.) +
-                         (s - 1) * (3. + static_cast<double>(pairs * d) / 160000.);
+        const double t = rounds * (static_cast<double>(stages) / s + 1.) +
+                         (s - 1) * (3. + static_cast<double>(pairs * d) / 800000.);
         if (s == 1 || t < least) {
             best = s;
             least = t;

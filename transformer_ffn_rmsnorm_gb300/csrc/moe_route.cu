@@ -19,11 +19,12 @@
 // candidates computed in 64 bits and compared again.  (FP64 runs at a small
 // fraction of the FP32 rate on this GPU: a 64-bit exponential for every
 // score would be most of the kernel.)  Groups are decided the same way.
-//   DELTA, in units of 2^-24 of s <= 1 (the approximate division is within 2 ulp, 4 units): sigmoid: expf 2, its sum with 1 one, the
-//   division 4: 7, taken as 8.  softmax: l - max rounds by |l - max|
-//   2^-24, which moves exp(l - max) by at most 1 (x e^-x < 1), expf 2; the
-//   denominator adds terms with those errors over at most 10 levels (a
-//   lane's 32 in pairs, then 32 lanes): 13; the division 4: 20, taken as 32.
+//   DELTA, in units of 2^-24 of s <= 1 (the approximate division is within 2
+//   ulp, 4 units): sigmoid: expf 2, its sum with 1 one, the division 4: 7,
+//   taken as 8.  softmax: l - max rounds by |l - max| 2^-24, which moves
+//   exp(l - max) by at most 1 (x e^-x < 1), expf 2; the denominator adds terms
+//   with those errors over at most 10 levels (a lane's 32 in pairs, then 32
+//   lanes): 13; the division 4: 20, taken as 32.
 #include "ffn_internal.cuh"
 
 namespace ffn {
@@ -177,7 +178,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 7 : 4) moe_route_
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, o);
     }
-    auto score32 = [&](float z) { return p.sigmoid ? __fdividef(1.f, 1.f + expf(-z)) : __fdividef(expf(z - top), denom); };
+    auto score32 = [&](float z) {
+        return p.sigmoid ? __fdividef(1.f, 1.f + expf(-z)) : __fdividef(expf(z - top), denom);
+    };
     auto bias_of = [&](int e) { return p.bias ? clean_bias(__ldg(p.bias + e)) : 0.f; };
 
     Exact ex;

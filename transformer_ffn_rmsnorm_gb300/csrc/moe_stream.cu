@@ -13,8 +13,8 @@
 // fills the last wave (moe_down_splits).  Four stages of 128 values keep 128
 // KB of weights in flight per SM.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-7 are the epilogue.  Every wait is bounded (1 s) as
-// in gemm_tcgen05.cu.
+// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-7 are the epilogue.
+// Every wait is bounded (1 s) as in gemm_tcgen05.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
             if constexpr (MODE == GATEUP)
-                moe::swiglu_epilogue<T, false>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<T *>(p.out), s_swap, 0, 16,
-                                               1, p.acc_scale, p.out_scale);
+                moe::swiglu_epilogue<T, false>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<T *>(p.out), s_swap,
+                                               0, 16, 1, p.acc_scale, p.out_scale);
             else
                 moe::store_epilogue(taddr, q, lane, t, p.wrows,
                                     static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
