@@ -187,11 +187,13 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
  *   FFN_PREPARED_WEIGHTS the weights are ffn_prepare_weights output (fp16 of
  *   w * 2^8) and the products run on fp16 operands: a bf16 x must lie in
  *   fp16's range (a finite value beyond it becomes infinite and records
- *   FFN_ERR_RANGE in the device status word), and |h| below 1.6e7.  No other
- *   flag.
- *   h = silu(G) * U is rounded once to the operand type (FFN_F16 without
- *   prepared weights: |h| up to 65504); everything else is fp32, a token's
- *   results are added in slot order, then res, and rounded once.
+ *   FFN_ERR_RANGE in the device status word; one below 2^-14 is rounded to a
+ *   multiple of 2^-24).  No other flag.
+ *   h = silu(G) * U is rounded to the operand type.  Where that is fp16, a
+ *   (token, slot) pair's row of h is held times a power of two that brings its
+ *   largest value to 2^-12 .. 2^15, so h may be of any size; values far below
+ *   the row's largest are rounded to 2^-24 of that scale.  Everything else is
+ *   fp32, a token's results are added in slot order, then res, and rounded once.
  *   d % 8 == 0, ffn % 8 == 0, 1 <= experts <= 1024, 1 <= k <= 32; rows * k,
  *   experts * d and experts * ffn at most 2^30.  rows == 0 launches nothing.
  *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned (sorted
@@ -344,9 +346,8 @@ ffn_status ffn_block_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, si
  *   ffn % 32 == 0; the other limits, the skipped slots, y = res in place and
  *   the workspace (ffn_moe_q4_workspace_bytes) as in ffn_moe_forward.
  *   The products run on fp16 operands: w = (u - 8) * s rounded once to fp16
- *   (|8 s| must be finite in fp16), x rounded to fp16 (beyond its range:
- *   FFN_ERR_RANGE in the device status word), h stored times 2^-8 (|h| below
- *   1.6e7); accumulation in fp32.
+ *   (|8 s| must be finite in fp16), x and h in fp16 as with
+ *   FFN_PREPARED_WEIGHTS there; accumulation in fp32.
  * ---------------------------------------------------------------------- */
 ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, size_t *bytes);
 ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const float *topk_w, ffn_q4_weight w_gate,

@@ -327,9 +327,32 @@ struct MoePlan {
     int64_t pairs;
     moe::Cut cut;
     int splits;                  // of the down product's reduction
-    size_t plan, xs, h, part;    // bytes, in this order
-    size_t total() const { return plan + xs + h + part; }
+    size_t plan, xs, h, part, scale, level;    // bytes, in this order
+    size_t total() const { return plan + xs + h + part + scale + level; }
 };
+
+// the parts of a call's workspace
+struct MoeSpace {
+    moe::Plan plan;
+    void *xs, *h;
+    float *part;
+};
+MoeSpace carve_moe(void *workspace, int64_t experts, const MoePlan &m) {
+    char *b = static_cast<char *>(workspace);
+    MoeSpace s;
+    s.plan = moe_plan_carve(b, m.pairs, experts, m.cut.tile);
+    s.xs = b + m.plan;
+    s.h = b + m.plan + m.xs;
+    b += m.plan + m.xs + m.h;
+    s.part = reinterpret_cast<float *>(b);
+    b += m.part;
+    if (m.level) {
+        s.plan.scale = reinterpret_cast<float *>(b);
+        s.plan.level = reinterpret_cast<uint4 *>(b + m.scale);
+        s.plan.nlevel = static_cast<int>(m.level / static_cast<size_t>(m.pairs) / 16);
+    }
+    return s;
+}
 
 // Rows an expert has on average (of those in use, at most) up to which 16-bit
 // weights stream through single CTAs.  Whole calls, us, single CTAs / pairs:
@@ -339,7 +362,7 @@ struct MoePlan {
 // 48 203 / 209, 96 257 / 230.
 constexpr int64_t kMoeStreamRows = 24;
 
-ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, bool q4, MoePlan *m) {
+ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, bool q4, bool half, MoePlan *m) {
     if (rows < 0 || d < 1 || ffn < 1 || experts < 1 || experts > moe::kMaxExperts || k < 1 || k > 32)
         return FFN_ERR_SHAPE;
     const int64_t step = q4 ? 32 : 8;
@@ -359,6 +382,8 @@ ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64
     m->xs = align256(p * d * 2);
     m->h = align256(p * ffn * 2);
     m->part = align256(p * d * 4 * m->splits);
+    m->scale = half ? align256(p * 4) : 0;   // h in fp16: its rows' scales and its blocks' levels
+    m->level = half ? p * static_cast<size_t>((ffn + 511) / 512 * 16) : 0;
     return FFN_OK;
 }
 
@@ -387,7 +412,7 @@ ffn_status plan_moe16(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int
                       uint32_t flags, MoePlan *m) {
     if (dtype != FFN_F16 && dtype != FFN_BF16) return FFN_ERR_DTYPE;
     if (flags & ~FFN_PREPARED_WEIGHTS) return FFN_ERR_FLAGS;
-    return plan_moe(rows, d, ffn, experts, k, false, m);
+    return plan_moe(rows, d, ffn, experts, k, false, dtype == FFN_F16 || (flags & FFN_PREPARED_WEIGHTS), m);
 }
 
 }  // namespace
@@ -419,29 +444,24 @@ ffn_status ffn_moe_forward(const void *x, const int32_t *topk_idx, const float *
     if (st != FFN_OK) return st;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    char *ws = static_cast<char *>(workspace);
-    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, m.cut.tile);
-    void *xs = ws + m.plan, *h = ws + m.plan + m.xs;
-    float *part = reinterpret_cast<float *>(ws + m.plan + m.xs + m.h);
-    // prepared weights: fp16 operands; the weights' 2^8 is undone on G and U,
-    // h is stored times 2^-8 and the two cancel in the down product
+    const auto [plan, xs, h, part] = carve_moe(workspace, experts, m);
+    // prepared weights: fp16 operands; the weights' 2^8 is undone in each product
     const bool prepared = (flags & FFN_PREPARED_WEIGHTS) != 0;
     const int op = prepared ? static_cast<int>(DT_F16) : static_cast<int>(dtype);
-    const float w_unscale = prepared ? 1.f / kPreparedScale : 1.f, h_scale = prepared ? 1.f / 256.f : 1.f;
+    const float w_unscale = prepared ? 1.f / kPreparedScale : 1.f;
     cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), m.cut, plan, x, xs,
                                     d, dtype, op != static_cast<int>(dtype), false, s);
     if (m.cut.tile == kMoeCutStream.tile) {
         if (e == cudaSuccess)
-            e = launch_moe_gateup_stream(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale,
-                                         s);
+            e = launch_moe_gateup_stream(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, s);
         if (e == cudaSuccess)
             e = launch_moe_down_stream(op, plan, h, w_down, part, m.splits, m.pairs, d, ffn, experts,
-                                       w_unscale / h_scale, s);
+                                       w_unscale, s);
     } else {
         if (e == cudaSuccess)
-            e = launch_moe_gateup(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, h_scale, s);
+            e = launch_moe_gateup(op, plan, xs, w_gate, w_up, h, m.pairs, d, ffn, experts, w_unscale, s);
         if (e == cudaSuccess)
-            e = launch_moe_down(op, plan, h, w_down, part, m.pairs, d, ffn, experts, w_unscale / h_scale, s);
+            e = launch_moe_down(op, plan, h, w_down, part, m.pairs, d, ffn, experts, w_unscale, s);
     }
     if (e == cudaSuccess)
         e = launch_moe_combine(plan, topk_w, part, m.splits, res, y, rows, static_cast<int>(k), d, dtype, s);
@@ -452,7 +472,7 @@ ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int6
                                       size_t *bytes) {
     if (!bytes) return FFN_ERR_NULL;
     MoePlan m;
-    const ffn_status st = plan_moe(rows, d, ffn, experts, k, true, &m);
+    const ffn_status st = plan_moe(rows, d, ffn, experts, k, true, true, &m);
     if (st != FFN_OK) return st;
     *bytes = m.total();
     return FFN_OK;
@@ -466,7 +486,7 @@ ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const floa
         (rows != 0 && (!x || !topk_idx || !topk_w || !y)))
         return FFN_ERR_NULL;
     MoePlan m;
-    ffn_status st = plan_moe(rows, d, ffn, experts, k, true, &m);
+    ffn_status st = plan_moe(rows, d, ffn, experts, k, true, true, &m);
     if (st != FFN_OK) return st;
     if (rows == 0) return FFN_OK;
     const size_t gd = static_cast<size_t>(experts) * ffn * q4_groups(d),
@@ -477,18 +497,14 @@ ffn_status ffn_moe_forward_q4(const void *x, const int32_t *topk_idx, const floa
     if (st != FFN_OK) return st;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    char *ws = static_cast<char *>(workspace);
-    const moe::Plan plan = moe_plan_carve(ws, m.pairs, experts, m.cut.tile);
-    void *xs = ws + m.plan, *h = ws + m.plan + m.xs;
-    float *part = reinterpret_cast<float *>(ws + m.plan + m.xs + m.h);
+    const auto [plan, xs, h, part] = carve_moe(workspace, experts, m);
     cudaError_t e = launch_moe_plan(topk_idx, rows, static_cast<int>(k), static_cast<int>(experts), m.cut, plan, x, xs,
                                     d, DT_BF16, true, true, s);
-    // h is stored times 2^-8, which keeps it clear of fp16 overflow
     if (e == cudaSuccess)
         e = launch_moe_gateup_q4(plan, xs, w_gate.qs, w_gate.scales, w_up.qs, w_up.scales, h, m.pairs, d, ffn, experts,
-                                 1.f / 256.f, s);
+                                 s);
     if (e == cudaSuccess)
-        e = launch_moe_down_q4(plan, h, w_down.qs, w_down.scales, part, m.splits, m.pairs, d, ffn, experts, 256.f, s);
+        e = launch_moe_down_q4(plan, h, w_down.qs, w_down.scales, part, m.splits, m.pairs, d, ffn, experts, s);
     if (e == cudaSuccess)
         e = launch_moe_combine(plan, topk_w, part, m.splits, res, y, rows, static_cast<int>(k), d, DT_BF16, s);
     return from_cuda(e);

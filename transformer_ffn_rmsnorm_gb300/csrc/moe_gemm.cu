@@ -60,7 +60,8 @@ struct Params {
     int wrows;         // weight rows of an expert (ffn or d)
     int nkb;           // 64-wide k blocks
     void *out;         // h (operand type) or part (fp32), [pairs x wrows]
-    float acc_scale, out_scale;
+    float acc_scale;
+    moe::Levels levels;    // of h, where it is fp16
     unsigned *err;
 };
 
@@ -139,6 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = walk.at(u);
+            if constexpr (MODE == DOWN && !BF16) {
+                if (t.odd && !moe::level_tile(p.levels, p.tiles, t, lane, abort_flag, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+            }
             const int half = t.n >> 1;   // this CTA's columns, a multiple of 16
             const int wrow = t.expert * p.wrows + t.f * kFRows + static_cast<int>(rank) * (kFRows / 2);
             const int brow = t.row0 + static_cast<int>(rank) * half;
@@ -233,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part = (warp - 2) >> 2;       // which of every two 16-column chunks
         bool ok = true;
         auto walk = walk_units();
+        if constexpr (MODE == DOWN && !BF16)
+            moe::level_ahead(p.levels, p.tiles, blockIdx.x * kEpiWarps + warp - 2, gridDim.x * kEpiWarps, lane);
         int acc = 0;
         uint32_t acc_ph = 0;
         for (int u = u0; u < units; u += ustep) {
@@ -247,21 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int f0 = t.f * kFRows + static_cast<int>(rank) * (kFRows / 2);
             if constexpr (MODE == GATEUP) {
                 moe::swiglu_epilogue<T, false>(taddr, q, lane, t, f0, p.wrows, static_cast<T *>(p.out), s_swap[part],
-                                               16 * part, 16 * (kEpiWarps / 4), 1 + part, p.acc_scale, p.out_scale);
+                                               16 * part, 16 * (kEpiWarps / 4), 1 + part, p.acc_scale, p.levels,
+                                               p.tiles);
             } else {
-                const int f = f0 + q * 32 + lane;
-                float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(t.row0) * p.wrows + f;
-                for (int c = 16 * part; c < t.n; c += 16 * (kEpiWarps / 4)) {
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
-                    ptx::tmem_ld_wait();
-                    float *to = dst + static_cast<int64_t>(c) * p.wrows;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (f < p.wrows && c + i < t.valid) *to = __uint_as_float(r[i]) * p.acc_scale;
-                        to += p.wrows;
-                    }
-                }
+                moe::store_epilogue(taddr, t, f0 + q * 32 + lane, 16 * part, 16 * (kEpiWarps / 4), p.wrows,
+                                    static_cast<float *>(p.out), p.acc_scale, BF16 ? nullptr : p.levels.scale);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -301,10 +300,15 @@ bool map_16(CUtensorMap *m, const void *ptr, bool bf16, int64_t inner, int64_t r
                          rows, inner * 2, kBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool map_rows(moe::RowMaps *m, const void *ptr, bool bf16, int64_t inner, int64_t rows) {
+    for (int i = 0; i < 4; ++i)
+        if (!map_16(&m->m[i], ptr, bf16, inner, rows, 128u >> i)) return false;
+    return true;
+}
+
 template <int MODE, bool BF16>
-cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const moe::RowMaps &b, int64_t pairs,
-                   int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, float out_scale,
-                   cudaStream_t s) {
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const void *rows, int64_t pairs,
+                   int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, cudaStream_t s) {
     constexpr int kFRows = MODE == GATEUP ? 128 : 256;
     const auto kern = &moe_gemm_kernel<MODE, BF16>;
     static std::atomic<int> configured_device{-1}, pair_slots{0};   // (host threads may call at the same time)
@@ -336,6 +340,8 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
         pair_slots.store(slots, std::memory_order_relaxed);
         configured_device.store(dev, std::memory_order_release);
     }
+    moe::RowMaps b;
+    if (!map_rows(&b, rows, BF16, K, pairs)) return cudaErrorInvalidValue;
     Params p{};
     p.header = plan.header;
     p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
@@ -344,7 +350,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     p.nkb = static_cast<int>((K + kBK - 1) / kBK);
     p.out = out;
     p.acc_scale = acc_scale;
-    p.out_scale = out_scale;
+    p.levels = moe::levels_of(plan, rows, K);
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
     const int64_t most = moe::max_tiles(pairs, experts, kTile) * p.nf;
@@ -356,35 +362,25 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-bool map_rows(moe::RowMaps *m, const void *ptr, bool bf16, int64_t inner, int64_t rows) {
-    for (int i = 0; i < 4; ++i)
-        if (!map_16(&m->m[i], ptr, bf16, inner, rows, 128u >> i)) return false;
-    return true;
-}
-
 }  // namespace
 
 cudaError_t launch_moe_gateup(int op, const Plan &plan, const void *xs, const void *wg, const void *wu, void *h,
-                              int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale, float out_scale,
-                              cudaStream_t s) {
+                              int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s) {
     const bool bf = op == DT_BF16;
     CUtensorMap w0, w1;
-    moe::RowMaps b;
-    if (!map_16(&w0, wg, bf, d, experts * ffn, kBM / 2) || !map_16(&w1, wu, bf, d, experts * ffn, kBM / 2) ||
-        !map_rows(&b, xs, bf, d, pairs))
+    if (!map_16(&w0, wg, bf, d, experts * ffn, kBM / 2) || !map_16(&w1, wu, bf, d, experts * ffn, kBM / 2))
         return cudaErrorInvalidValue;
-    return bf ? launch<GATEUP, true>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s)
-              : launch<GATEUP, false>(plan, w0, w1, b, pairs, experts, ffn, d, h, acc_scale, out_scale, s);
+    return bf ? launch<GATEUP, true>(plan, w0, w1, xs, pairs, experts, ffn, d, h, acc_scale, s)
+              : launch<GATEUP, false>(plan, w0, w1, xs, pairs, experts, ffn, d, h, acc_scale, s);
 }
 
 cudaError_t launch_moe_down(int op, const Plan &plan, const void *h, const void *wd, float *part, int64_t pairs,
                             int64_t d, int64_t ffn, int64_t experts, float acc_scale, cudaStream_t s) {
     const bool bf = op == DT_BF16;
     CUtensorMap w;
-    moe::RowMaps b;
-    if (!map_16(&w, wd, bf, ffn, experts * d, kBM) || !map_rows(&b, h, bf, ffn, pairs)) return cudaErrorInvalidValue;
-    return bf ? launch<DOWN, true>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s)
-              : launch<DOWN, false>(plan, w, w, b, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+    if (!map_16(&w, wd, bf, ffn, experts * d, kBM)) return cudaErrorInvalidValue;
+    return bf ? launch<DOWN, true>(plan, w, w, h, pairs, experts, d, ffn, part, acc_scale, s)
+              : launch<DOWN, false>(plan, w, w, h, pairs, experts, d, ffn, part, acc_scale, s);
 }
 
 }  // namespace ffn

@@ -89,7 +89,7 @@ struct Params {
     int splits;                // of the reduction (down)
     int64_t split_stride;      // floats from one split of part to the next
     void *out;
-    float acc_scale, out_scale;
+    moe::Levels levels;    // of h, where it is fp16
     unsigned *err;
 };
 
@@ -286,6 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = walk.at(u);
+            if constexpr (MODE == DOWN) {
+                if (t.odd && !moe::level_tile(p.levels, p.tiles, t, lane, abort_flag, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+            }
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -463,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t pacc = 0;
         auto walk = walk_units();
+        if constexpr (MODE == DOWN) moe::level_ahead(p.levels, p.tiles, blockIdx.x * kEpiWarps + q, gridDim.x * kEpiWarps, lane);
         for (int u = u0; u < units; u += ustep) {
             const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
@@ -475,10 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
             if constexpr (MODE == GATEUP)
                 moe::swiglu_epilogue<__half, true>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<__half *>(p.out),
-                                                   s_swap, 0, 16, 1, p.acc_scale, p.out_scale);
+                                                   s_swap, 0, 16, 1, 1.f, p.levels, p.tiles);
             else
-                moe::store_epilogue(taddr, q, lane, t, p.wrows,
-                                    static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
+                moe::store_epilogue(taddr, t, t.f * 128 + 32 * q + lane, 0, 16, p.wrows,
+                                    static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, 1.f,
+                                    p.levels.scale);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(&bar_tempty[acc]));
@@ -511,10 +519,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+bool map_rows(moe::RowMaps *m, const void *ptr, int64_t inner, int64_t rows) {
+    for (int i = 0; i < 4; ++i)
+        if (!encode_tma_2d(&m->m[i], ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner, rows, inner * 2, 64, 128u >> i,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+            return false;
+    return true;
+}
+
 template <int MODE>
-cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const moe::RowMaps &b,
+cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w1, const void *rows,
                    const uint16_t *s0, const uint16_t *s1, int splits, int64_t pairs, int64_t experts, int64_t wrows,
-                   int64_t K, void *out, float acc_scale, float out_scale, cudaStream_t s) {
+                   int64_t K, void *out, cudaStream_t s) {
     const auto kern = &moe_gemm_q4_kernel<MODE>;
     static std::atomic<int> configured_device{-1};   // (host threads may call at the same time)
     int dev = 0;
@@ -526,6 +542,8 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
         configured_device.store(dev, std::memory_order_release);
     }
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;
+    moe::RowMaps b;
+    if (!map_rows(&b, rows, K, pairs)) return cudaErrorInvalidValue;
     Params p{};
     p.header = plan.header;
     p.tiles = reinterpret_cast<const int4 *>(plan.tiles);
@@ -537,8 +555,7 @@ cudaError_t launch(const Plan &plan, const CUtensorMap &w0, const CUtensorMap &w
     p.splits = splits;
     p.split_stride = pairs * wrows;
     p.out = out;
-    p.acc_scale = acc_scale;
-    p.out_scale = out_scale;
+    p.levels = moe::levels_of(plan, rows, K);
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
     const int64_t grid = std::min<int64_t>(sm_count(), moe::max_tiles(pairs, experts, kTile) * p.nf * splits);
@@ -553,34 +570,21 @@ bool map_q4(CUtensorMap *m, const uint8_t *qs, int64_t K, int64_t rows, uint32_t
     return encode_tma_2d(m, qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, pitch, rows, pitch, 128, box_rows,
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
-bool map_rows(moe::RowMaps *m, const void *ptr, int64_t inner, int64_t rows) {
-    for (int i = 0; i < 4; ++i)
-        if (!encode_tma_2d(&m->m[i], ptr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, inner, rows, inner * 2, 64, 128u >> i,
-                           CU_TENSOR_MAP_SWIZZLE_128B))
-            return false;
-    return true;
-}
-
 }  // namespace
 
 cudaError_t launch_moe_gateup_q4(const Plan &plan, const void *xs, const uint8_t *qg, const uint16_t *sg,
                                  const uint8_t *qu, const uint16_t *su, void *h, int64_t pairs, int64_t d, int64_t ffn,
-                                 int64_t experts, float out_scale, cudaStream_t s) {
+                                 int64_t experts, cudaStream_t s) {
     CUtensorMap w0, w1;
-    moe::RowMaps b;
-    if (!map_q4(&w0, qg, d, experts * ffn, 64) || !map_q4(&w1, qu, d, experts * ffn, 64) ||
-        !map_rows(&b, xs, d, pairs))
-        return cudaErrorInvalidValue;
-    return launch<GATEUP>(plan, w0, w1, b, sg, su, 1, pairs, experts, ffn, d, h, 1.f, out_scale, s);
+    if (!map_q4(&w0, qg, d, experts * ffn, 64) || !map_q4(&w1, qu, d, experts * ffn, 64)) return cudaErrorInvalidValue;
+    return launch<GATEUP>(plan, w0, w1, xs, sg, su, 1, pairs, experts, ffn, d, h, s);
 }
 
 cudaError_t launch_moe_down_q4(const Plan &plan, const void *h, const uint8_t *qd, const uint16_t *sd, float *part,
-                               int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
-                               cudaStream_t s) {
+                               int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, cudaStream_t s) {
     CUtensorMap w;
-    moe::RowMaps b;
-    if (!map_q4(&w, qd, ffn, experts * d, 128) || !map_rows(&b, h, ffn, pairs)) return cudaErrorInvalidValue;
-    return launch<DOWN>(plan, w, w, b, sd, sd, splits, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+    if (!map_q4(&w, qd, ffn, experts * d, 128)) return cudaErrorInvalidValue;
+    return launch<DOWN>(plan, w, w, h, sd, sd, splits, pairs, experts, d, ffn, part, s);
 }
 
 }  // namespace ffn

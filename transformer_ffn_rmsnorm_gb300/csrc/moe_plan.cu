@@ -131,6 +131,7 @@ __device__ __forceinline__ void plan_tables(const PlanParams &p, PlanShared &sh)
     if (threadIdx.x == 0) {
         p.plan.header[0] = ntiles;
         p.plan.header[1] = sh.widest;
+        p.plan.header[2] = 0;
     }
     for (int q = threadIdx.x; q < ntiles; q += kPlanThreads) {
         // the last expert whose first tile is at or before q (one without
@@ -148,7 +149,7 @@ __device__ __forceinline__ void plan_tables(const PlanParams &p, PlanShared &sh)
         t.count = (t.rows + p.cut.tile - 1) / p.cut.tile;
         t.cols = width(t.rows, t.count);
         t.row0 = sh.row0[lo];
-        t.pad0 = t.pad1 = 0;
+        t.done = t.odd = 0;
         p.plan.tiles[q] = t;
     }
 }
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanP
             t.count = nt;
             t.cols = ((count + nt - 1) / nt + p.cut.gran - 1) / p.cut.gran * p.cut.gran;
             t.row0 = at;
-            t.pad0 = t.pad1 = 0;
+            t.done = t.odd = 0;
             for (int q = 0; q < nt; ++q) p.plan.tiles[first + q] = t;
             atomicMax(&s_ntiles, first + nt);
             atomicMax(&s_widest, t.cols);
@@ -212,11 +213,17 @@ __global__ void __launch_bounds__(kSmallPairs) moe_plan_small_kernel(const PlanP
         if (i == 0) {
             p.plan.header[0] = s_ntiles;
             p.plan.header[1] = s_widest;
+            p.plan.header[2] = 0;
         }
     } else {
         __syncthreads();
     }
     if (s_token < 0) return;
+    if (p.plan.scale && blockIdx.x == 0) {
+        if (i == 0) p.plan.scale[r] = 1.f;
+        for (int c = i; c < p.plan.nlevel; c += kSmallPairs)
+            p.plan.level[static_cast<int64_t>(r) * p.plan.nlevel + c] = make_uint4(0, 0, 0, 0);
+    }
     const uint4 *src = static_cast<const uint4 *>(p.x) + static_cast<int64_t>(s_token) * p.nvec;
     uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(r) * p.nvec;
     bool bad = false;
@@ -293,6 +300,11 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const PlanParams p) {
     const int at = p.plan.hist[i / p.chunk * p.experts + p.idx[i]] + rank;
     __syncwarp();   // every lane has read the rank
     if (lane == 0) p.plan.pos[i] = at;
+    if (p.plan.scale) {
+        if (lane == 0) p.plan.scale[at] = 1.f;
+        for (int c = lane; c < p.plan.nlevel; c += 32)
+            p.plan.level[static_cast<int64_t>(at) * p.plan.nlevel + c] = make_uint4(0, 0, 0, 0);
+    }
     const uint4 *src = static_cast<const uint4 *>(p.x) + i / p.k * p.nvec;
     uint4 *dst = static_cast<uint4 *>(p.xs) + static_cast<int64_t>(at) * p.nvec;
     bool bad = false;
@@ -390,6 +402,9 @@ Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile) {
     p.hist = reinterpret_cast<int *>(b);
     b += hist_bytes(pairs, experts);
     p.pos = reinterpret_cast<int *>(b);
+    p.scale = nullptr;
+    p.level = nullptr;
+    p.nlevel = 0;
     return p;
 }
 

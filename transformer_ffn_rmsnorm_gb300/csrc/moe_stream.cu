@@ -50,7 +50,8 @@ struct Params {
     int splits;            // of the reduction (down)
     int64_t split_stride;  // floats from one split of part to the next
     void *out;
-    float acc_scale, out_scale;
+    float acc_scale;
+    moe::Levels levels;    // of h, where it is fp16
     unsigned *err;
 };
 
@@ -115,6 +116,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto walk = walk_units();
         for (int u = u0; u < units && ok; u += ustep) {
             const Unit t = walk.at(u);
+            if constexpr (MODE == DOWN && !BF16) {
+                if (t.odd && !moe::level_tile(p.levels, p.tiles, t, lane, abort_flag, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+            }
             const int wrow = t.expert * p.wrows + t.f * kFRows;
             for (int g = lo_of(u), ge = hi_of(u); g < ge; ++g) {
                 const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, kWaitNs);
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t pacc = 0;
         auto walk = walk_units();
+        if constexpr (MODE == DOWN && !BF16) moe::level_ahead(p.levels, p.tiles, blockIdx.x * 4 + q, gridDim.x * 4, lane);
         for (int u = u0; u < units; u += ustep) {
             const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
@@ -210,10 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
             if constexpr (MODE == GATEUP)
                 moe::swiglu_epilogue<T, false>(taddr, q, lane, t, t.f * 64, p.wrows, static_cast<T *>(p.out), s_swap,
-                                               0, 16, 1, p.acc_scale, p.out_scale);
+                                               0, 16, 1, p.acc_scale, p.levels, p.tiles);
             else
-                moe::store_epilogue(taddr, q, lane, t, p.wrows,
-                                    static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale);
+                moe::store_epilogue(taddr, t, t.f * 128 + 32 * q + lane, 0, 16, p.wrows,
+                                    static_cast<float *>(p.out) + (u % p.splits) * p.split_stride, p.acc_scale,
+                                    BF16 ? nullptr : p.levels.scale);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(&bar_tempty[acc]));
@@ -249,8 +258,7 @@ bool map_16(CUtensorMap *m, const void *ptr, bool bf16, int64_t inner, int64_t r
 
 template <int MODE, bool BF16>
 cudaError_t launch(const Plan &plan, const void *w0, const void *w1, const void *b, int splits, int64_t pairs,
-                   int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, float out_scale,
-                   cudaStream_t s) {
+                   int64_t experts, int64_t wrows, int64_t K, void *out, float acc_scale, cudaStream_t s) {
     constexpr int kFRows = MODE == GATEUP ? 64 : 128;
     const auto kern = &moe_stream_kernel<MODE, BF16>;
     static std::atomic<int> configured_device{-1};   // (host threads may call at the same time)
@@ -277,7 +285,7 @@ cudaError_t launch(const Plan &plan, const void *w0, const void *w1, const void 
     p.split_stride = pairs * wrows;
     p.out = out;
     p.acc_scale = acc_scale;
-    p.out_scale = out_scale;
+    p.levels = moe::levels_of(plan, b, K);
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
     const int64_t grid = std::min<int64_t>(sm_count(), moe::max_tiles(pairs, experts, kTile) * p.nf * splits);
@@ -290,18 +298,18 @@ cudaError_t launch(const Plan &plan, const void *w0, const void *w1, const void 
 
 cudaError_t launch_moe_gateup_stream(int op, const Plan &plan, const void *xs, const void *wg, const void *wu, void *h,
                                      int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
-                                     float out_scale, cudaStream_t s) {
+                                     cudaStream_t s) {
     return op == DT_BF16
-               ? launch<GATEUP, true>(plan, wg, wu, xs, 1, pairs, experts, ffn, d, h, acc_scale, out_scale, s)
-               : launch<GATEUP, false>(plan, wg, wu, xs, 1, pairs, experts, ffn, d, h, acc_scale, out_scale, s);
+               ? launch<GATEUP, true>(plan, wg, wu, xs, 1, pairs, experts, ffn, d, h, acc_scale, s)
+               : launch<GATEUP, false>(plan, wg, wu, xs, 1, pairs, experts, ffn, d, h, acc_scale, s);
 }
 
 cudaError_t launch_moe_down_stream(int op, const Plan &plan, const void *h, const void *wd, float *part, int splits,
                                    int64_t pairs, int64_t d, int64_t ffn, int64_t experts, float acc_scale,
                                    cudaStream_t s) {
     return op == DT_BF16
-               ? launch<DOWN, true>(plan, wd, wd, h, splits, pairs, experts, d, ffn, part, acc_scale, 1.f, s)
-               : launch<DOWN, false>(plan, wd, wd, h, splits, pairs, experts, d, ffn, part, acc_scale, 1.f, s);
+               ? launch<DOWN, true>(plan, wd, wd, h, splits, pairs, experts, d, ffn, part, acc_scale, s)
+               : launch<DOWN, false>(plan, wd, wd, h, splits, pairs, experts, d, ffn, part, acc_scale, s);
 }
 
 }  // namespace ffn
