@@ -196,8 +196,11 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
  *   fp32, a token's results are added in slot order, then res, and rounded once.
  *   d % 8 == 0, ffn % 8 == 0, 1 <= experts <= 1024, 1 <= k <= 32; rows * k,
  *   experts * d and experts * ffn at most 2^30.  rows == 0 launches nothing.
- *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned (sorted
- *   positions, h, one fp32 row per (token, slot) pair); not shared by calls
+ *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned: per (token,
+ *   slot) pair a 16-bit copy of x's row, a 16-bit row of h and one fp32 row of
+ *   results (up to 8 for at most 1024 pairs, whose down product may be split),
+ *   beside the sorted positions.  The query's answer never falls as rows grow: a
+ *   workspace sized for a batch serves every smaller one.  Not shared by calls
  *   that may run at the same time.  The whole call is on `stream` and never
  *   waits for the device: it can be captured in a graph, and which experts
  *   are used is read when it runs.

@@ -145,3 +145,46 @@ def test_moe_forward_q4_refusals(lib):
     for bad in (x, c, sc, ctypes.c_void_p(res.value + 16)):
         assert call(y=bad) == _lib.FFN_ERR_ALIAS
     assert call(rows=0) == _lib.FFN_OK and need(rows=0) == (_lib.FFN_OK, 0)
+
+
+def workspace_query(lib, q4, flags=0):
+    def need(rows, d, ffn, experts, k):
+        out = ctypes.c_size_t(0)
+        if q4:
+            st = lib.ffn_moe_q4_workspace_bytes(rows, d, ffn, experts, k, ctypes.byref(out))
+        else:
+            st = lib.ffn_moe_workspace_bytes(rows, d, ffn, experts, k, _lib.FFN_BF16, flags, ctypes.byref(out))
+        assert st == _lib.FFN_OK
+        return out.value
+    return need
+
+
+@pytest.mark.parametrize("form", ["bf16", "prepared", "q4"])
+@pytest.mark.parametrize("d,ffn,experts,k", [(4096, 14336, 8, 2), (5120, 2176, 32, 4), (2048, 1408, 64, 6),
+                                             (64, 512, 1024, 1), (32, 32, 1, 1), (256, 4096, 3, 32)])
+def test_workspace_serves_every_smaller_batch(lib, form, d, ffn, experts, k):
+    """The query never falls as the rows grow, across the changes of the split
+    count, of single CTAs to pairs and of the plan's chunks; and a call of fewer
+    rows takes what the query gives for more (it gets as far as the alignment
+    of its input, which is checked after the workspace)."""
+    need = workspace_query(lib, form == "q4", _lib.FFN_PREPARED_WEIGHTS if form == "prepared" else 0)
+    marks = [1024 // k, 24 * experts // k, 131072 // k, 262144 // k, 393216 // k, 131072 * 5 // k]
+    rows = sorted({r for r in range(1, 700)} | {max(1, m + i) for m in marks for i in range(-3, 4)} | set(range(700, 4000, 97)))
+    sizes = [need(r, d, ffn, experts, k) for r in rows]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])), [r for r, a, b in zip(rows, sizes, sizes[1:]) if a > b]
+
+    x, idx, w, a, b, c, res, y, ws = ptrs(9)
+    ws = ctypes.c_void_p(1 << 50)
+    far = [ctypes.c_void_p((i + 1) << 44) for i in range(16)]
+    odd = ctypes.c_void_p((1 << 43) + 2)
+
+    def status(r, bytes_):
+        if form == "q4":
+            m = [_lib.Q4Weight(far[i].value, far[i + 3].value) for i in range(3)]
+            return lib.ffn_moe_forward_q4(odd, far[6], far[7], *m, None, far[8], r, d, ffn, experts, k, ws, bytes_, None)
+        return lib.ffn_moe_forward(odd, far[6], far[7], far[0], far[1], far[2], None, far[8], r, d, ffn, experts, k,
+                                   _lib.FFN_BF16, _lib.FFN_PREPARED_WEIGHTS if form == "prepared" else 0, ws, bytes_, None)
+    for top in (rows[-1], 456, 97, 512, 1024 // k + 1, 24 * experts // k + 1, 131072 // k + 1):
+        for r in [r for r in rows if r <= top][::7] + [top]:
+            assert status(r, need(top, d, ffn, experts, k)) == _lib.FFN_ERR_ALIGN, (r, top)
+        assert status(top, 0) == _lib.FFN_ERR_WORKSPACE

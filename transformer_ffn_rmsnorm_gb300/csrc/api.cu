@@ -387,6 +387,25 @@ ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64
     return FFN_OK;
 }
 
+// Bytes for any number of rows up to `rows`, as a workspace sized for a batch
+// serves every smaller one.  The need itself is not monotonic: fewer rows may be
+// cut into more tiles (single CTAs), and their down product split.
+size_t moe_workspace(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64_t k, bool q4, MoePlan m) {
+    if (rows == 0) return 0;
+    m.plan = moe_plan_bytes_upto(m.pairs, experts, m.cut.tile);
+    int64_t single = m.pairs;   // the most pairs of single CTAs
+    if (!q4) {
+        single = std::min(m.pairs, kMoeStreamRows * experts / k * k);
+        if (single > 0) m.plan = std::max(m.plan, moe_plan_bytes_upto(single, experts, kMoeCutStream.tile));
+    }
+    const size_t row = static_cast<size_t>(d) * 4;
+    for (int64_t p = std::min(single, kMoeSplitPairs / k * k); p > 0; p -= k) {
+        if (align256(static_cast<size_t>(p) * row * kMoeMaxSplits) <= m.part) break;
+        m.part = std::max(m.part, align256(static_cast<size_t>(p) * row * moe_down_splits(p, experts, d, ffn)));
+    }
+    return m.total();
+}
+
 // the checks that follow the sizes: pointers given, their alignment, overlaps
 ffn_status check_moe(const void *x, const int32_t *idx, const float *w, const Range *weights, int nweights,
                      const void *res, const void *y, int64_t rows, int64_t d, int64_t k, const MoePlan &m,
@@ -425,7 +444,7 @@ ffn_status ffn_moe_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int64_t
     MoePlan m;
     const ffn_status st = plan_moe16(rows, d, ffn, experts, k, dtype, flags, &m);
     if (st != FFN_OK) return st;
-    *bytes = m.total();
+    *bytes = moe_workspace(rows, d, ffn, experts, k, false, m);
     return FFN_OK;
 }
 
@@ -474,7 +493,7 @@ ffn_status ffn_moe_q4_workspace_bytes(int64_t rows, int64_t d, int64_t ffn, int6
     MoePlan m;
     const ffn_status st = plan_moe(rows, d, ffn, experts, k, true, true, &m);
     if (st != FFN_OK) return st;
-    *bytes = m.total();
+    *bytes = moe_workspace(rows, d, ffn, experts, k, true, m);
     return FFN_OK;
 }
 

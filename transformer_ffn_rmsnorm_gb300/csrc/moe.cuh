@@ -406,6 +406,8 @@ __device__ __forceinline__ bool epilogue_vote(bool got, int id) {
 }  // namespace moe
 
 size_t moe_plan_bytes(int64_t pairs, int64_t experts, int tile);
+// what every number of pairs up to `pairs` fits into
+size_t moe_plan_bytes_upto(int64_t pairs, int64_t experts, int tile);
 moe::Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile);
 // Sorts the pairs of idx [rows x k] into token tiles and writes their rows of
 // x [rows x d] (type dt) in sorted order to xs [pairs x d]: as they are, or as
@@ -442,9 +444,11 @@ cudaError_t launch_moe_down_q4(const moe::Plan &plan, const void *h, const uint8
                                int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, cudaStream_t s);
 
 // Splits of the down product's reduction on the single-CTA kernels (units of
-// 128 weight rows, stages of 128 values): at most 8, none shorter than 4
-// stages.  A function of the sizes alone, so that the workspace query and the
-// call agree.
+// 128 weight rows, counted in stages of 128 values): at most kMoeMaxSplits, none
+// shorter than 4 stages, 1 beyond kMoeSplitPairs pairs.  A function of the sizes
+// alone, so that the workspace query and the call agree.
+constexpr int kMoeMaxSplits = 8;
+constexpr int64_t kMoeSplitPairs = 1024;
 int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn);
 
 }  // namespace ffn

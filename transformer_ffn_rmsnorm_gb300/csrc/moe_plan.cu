@@ -392,6 +392,13 @@ size_t moe_plan_bytes(int64_t pairs, int64_t experts, int tile) {
            hist_bytes(pairs, experts) + align256(static_cast<size_t>(pairs) * sizeof(int));
 }
 
+// (the number of chunks falls by half where they grow by 256 pairs)
+size_t moe_plan_bytes_upto(int64_t pairs, int64_t experts, int tile) {
+    const int64_t full = static_cast<int64_t>(kMaxChunks) * kChunkThreads;
+    return moe_plan_bytes(pairs, experts, tile) - hist_bytes(pairs, experts) +
+           std::max(hist_bytes(pairs, experts), hist_bytes(std::min(pairs, full), experts));
+}
+
 Plan moe_plan_carve(void *base, int64_t pairs, int64_t experts, int tile) {
     char *b = static_cast<char *>(base);
     Plan p;
@@ -481,10 +488,10 @@ cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *pa
 int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn) {
     const int64_t units = std::min(pairs, experts) * ((d + 127) / 128), stages = (ffn + 127) / 128;
     constexpr int64_t kSms = 152;   // (not the current device's: the workspace depends on it)
-    if (pairs > 1024) return 1;   // tiles enough, and each split writes a row a pair
+    if (pairs > kMoeSplitPairs) return 1;   // tiles enough, and each split writes a row a pair
     int best = 1;
     double least = 0.;
-    for (int s = 1; s <= 8 && stages / s >= 4; ++s) {
+    for (int s = 1; s <= kMoeMaxSplits && stages / s >= 4; ++s) {
         const double rounds = static_cast<double>((units * s + kSms - 1) / kSms);
         const double t = rounds * (static_cast<double>(stages) / s + 1.) +
                          (s - 1) * (3. + static_cast<double>(pairs * d) / 800000.);
