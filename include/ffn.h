@@ -21,7 +21,8 @@
  * - Arguments are validated on the host before any launch.  A violation
  *   returns an error status and launches nothing.  rows == 0 (an empty batch)
  *   is valid and launches nothing (x, y and n may then be NULL).  Pointers
- *   must be 16-byte aligned.
+ *   must be 16-byte aligned, but for a router's logits, indices and weights
+ *   (to their element's size).
  * - After launching, a failed launch is reported as FFN_ERR_CUDA.  A kernel
  *   that gives up a bounded wait records FFN_ERR_TIMEOUT in a device status
  *   word that ffn_device_status() reads; no C++ exception crosses this ABI.
@@ -42,7 +43,7 @@ typedef enum {
     FFN_ERR_NULL = 1,       /* a required pointer is NULL                          */
     FFN_ERR_SHAPE = 2,      /* a size is out of range or breaks a divisibility rule */
     FFN_ERR_DTYPE = 3,      /* unknown or unsupported storage type                 */
-    FFN_ERR_ALIGN = 4,      /* a pointer is not 16-byte aligned                    */
+    FFN_ERR_ALIGN = 4,      /* a pointer is not aligned (16 bytes; see above)       */
     FFN_ERR_WORKSPACE = 5,  /* workspace NULL or smaller than the query returned   */
     FFN_ERR_ALIAS = 6,      /* an output overlaps an input it may not overlap      */
     FFN_ERR_CUDA = 7,       /* a CUDA runtime call failed                          */

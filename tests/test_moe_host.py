@@ -188,3 +188,32 @@ def test_workspace_serves_every_smaller_batch(lib, form, d, ffn, experts, k):
         for r in [r for r in rows if r <= top][::7] + [top]:
             assert status(r, need(top, d, ffn, experts, k)) == _lib.FFN_ERR_ALIGN, (r, top)
         assert status(top, 0) == _lib.FFN_ERR_WORKSPACE
+
+
+def test_rows_of_a_batch_need_no_16_bytes(lib):
+    """Logits, indices and weights are read one by one: slices of their rows are
+    taken (a call of too small a workspace gets as far as that, and a call of
+    logits that overlap the outputs as far as the overlap)."""
+    x, idx, w, wg, wu, wd, res, y, ws = ptrs(9)
+
+    def at(p, n):
+        return ctypes.c_void_p(p.value + n)
+
+    def route(logits=x, bias=res, i=idx, wt=w, dtype=_lib.FFN_F32):
+        return lib.ffn_moe_route(logits, bias, i, wt, 4, 63, 6, 1, 1, 1.0, dtype, 0, None)
+    for dtype, size in ((_lib.FFN_F32, 4), (_lib.FFN_F16, 2), (_lib.FFN_BF16, 2)):
+        assert route(logits=at(x, 63 * size), i=at(x, 64 * size), dtype=dtype) == _lib.FFN_ERR_ALIAS
+        assert route(logits=at(x, size // 2), dtype=dtype) == _lib.FFN_ERR_ALIGN
+    assert route(i=at(idx, 24), wt=at(idx, 28)) == _lib.FFN_ERR_ALIAS
+    for name in ("i", "wt"):
+        assert route(**{name: at(idx, 2)}) == _lib.FFN_ERR_ALIGN
+
+    def forward(i=idx, wt=w, out=y):
+        return lib.ffn_moe_forward(x, i, wt, wg, wu, wd, res, out, 4, 64, 128, 8, 6, _lib.FFN_BF16, 0, ws, 1 << 27, None)
+
+    def forward_q4(i=idx, wt=w, out=y):
+        m = [_lib.Q4Weight((20 + n) << 28, (24 + n) << 28) for n in range(3)]
+        return lib.ffn_moe_forward_q4(x, i, wt, *m, res, out, 4, 64, 128, 8, 6, ws, 1 << 27, None)
+    for f in (forward, forward_q4):
+        assert f(i=at(idx, 24), wt=at(w, 24), out=x) == _lib.FFN_ERR_ALIAS
+        assert f(i=at(idx, 2)) == _lib.FFN_ERR_ALIGN and f(wt=at(w, 1)) == _lib.FFN_ERR_ALIGN

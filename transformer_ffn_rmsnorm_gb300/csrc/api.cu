@@ -64,7 +64,8 @@ size_t dtype_size(ffn_dtype dt) { return dt == FFN_F32 ? 4 : 2; }
 
 bool valid_dtype(ffn_dtype dt) { return dt == FFN_F32 || dt == FFN_F16 || dt == FFN_BF16; }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned16(const void *p) { return aligned(p, 16); }
 
 // 64-byte groups of four Q4 blocks in a device-layout row of `in` weights
 int64_t q4_groups(int64_t in) { return (in + 127) / 128; }
@@ -226,7 +227,7 @@ const char *ffn_status_string(ffn_status s) {
         case FFN_ERR_NULL: return "a required pointer is NULL";
         case FFN_ERR_SHAPE: return "a size is out of range or breaks a divisibility rule";
         case FFN_ERR_DTYPE: return "unknown or unsupported storage type";
-        case FFN_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case FFN_ERR_ALIGN: return "a pointer is not aligned (to 16 bytes, or to its elements where those are read one by one)";
         case FFN_ERR_WORKSPACE: return "workspace missing or too small";
         case FFN_ERR_ALIAS: return "an output overlaps an input";
         case FFN_ERR_CUDA: return "a CUDA runtime call failed";
@@ -305,7 +306,9 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
     if (groups < 1 || groups > 32 || experts % groups || topk_groups < 1 || topk_groups > groups) return FFN_ERR_SHAPE;
     if (k > topk_groups * (experts / groups)) return FFN_ERR_SHAPE;
     if (rows == 0) return FFN_OK;
-    if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w)) return FFN_ERR_ALIGN;
+    // (logits, indices and weights are read and written one by one: any rows of a batch will do)
+    if (!aligned(logits, dtype_size(dtype)) || !aligned16(bias) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return FFN_ERR_ALIGN;
     const Range rl{logits, static_cast<size_t>(rows) * experts * dtype_size(dtype)},
         rb{bias, static_cast<size_t>(experts) * 4}, ri{topk_idx, static_cast<size_t>(rows) * k * 4},
         rw{topk_w, static_cast<size_t>(rows) * k * 4};
@@ -411,9 +414,9 @@ ffn_status check_moe(const void *x, const int32_t *idx, const float *w, const Ra
                      const void *res, const void *y, int64_t rows, int64_t d, int64_t k, const MoePlan &m,
                      void *workspace, size_t workspace_bytes) {
     if (!workspace || workspace_bytes < m.total()) return FFN_ERR_WORKSPACE;
-    for (const void *p : {x, static_cast<const void *>(idx), static_cast<const void *>(w), res, y,
-                          static_cast<const void *>(workspace)})
+    for (const void *p : {x, res, y, static_cast<const void *>(workspace)})
         if (!aligned16(p)) return FFN_ERR_ALIGN;
+    if (!aligned(idx, 4) || !aligned(w, 4)) return FFN_ERR_ALIGN;   // (read one by one)
     const size_t xb = static_cast<size_t>(rows) * d * 2, ib = static_cast<size_t>(rows) * k * 4;
     const Range ry{y, xb}, rws{workspace, m.total()};
     for (int i = 0; i < nweights; ++i) {
