@@ -217,3 +217,18 @@ def test_rows_of_a_batch_need_no_16_bytes(lib):
     for f in (forward, forward_q4):
         assert f(i=at(idx, 24), wt=at(w, 24), out=x) == _lib.FFN_ERR_ALIAS
         assert f(i=at(idx, 2)) == _lib.FFN_ERR_ALIGN and f(wt=at(w, 1)) == _lib.FFN_ERR_ALIGN
+
+
+def test_q4_scales_of_another_16_bit_type_are_refused():
+    """bf16 scales have other bits than fp16's and would be read as those."""
+    import torch
+    from transformer_ffn_rmsnorm_gb300 import ffn
+    qs = torch.zeros(3, 32, 64, dtype=torch.uint8)
+    sc = torch.ones(3, 32, 4)
+    for dtype in (torch.bfloat16, torch.float32):
+        with pytest.raises(TypeError):
+            ffn._moe_q4_weight("w_gate", (qs, sc.to(dtype)), 3, 32, 128, -1)
+    for good in (sc.half(), sc.half().view(torch.int16), sc.half().view(torch.uint16)):
+        ffn._moe_q4_weight("w_gate", (qs, good), 3, 32, 128, -1)
+    with pytest.raises(ValueError):
+        ffn._moe_q4_weight("w_gate", (qs, sc.half()[:2]), 3, 32, 128, -1)

@@ -243,12 +243,15 @@ def ffn_moe_q4_workspace_bytes(rows: int, d: int, ffn: int, experts: int, k: int
     return out.value
 
 
+_F16_BITS = (torch.float16, torch.int16, torch.uint16)   # (bf16 has other bits)
+
+
 def _moe_q4_weight(name, w, experts, out, inn, dev):
     qs, sc = w
     groups = -(-inn // 128)
     _expect(name + " qs", qs, (experts, out, 64 * groups), torch.uint8, dev)
-    if sc.element_size() != 2:
-        raise TypeError(f"{name} scales must be fp16 or their 16-bit patterns")
+    if sc.dtype not in _F16_BITS:
+        raise TypeError(f"{name} scales must be fp16 or their 16-bit patterns, are {sc.dtype}")
     _expect(name + " scales", sc, (experts, out, 4 * groups), sc.dtype, dev)
     return Q4Weight(qs.data_ptr(), sc.data_ptr())
 
