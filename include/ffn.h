@@ -195,8 +195,10 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
  *   largest value to 2^-12 .. 2^15, so h may be of any size; values far below
  *   the row's largest are rounded to 2^-24 of that scale.  Everything else is
  *   fp32, a token's results are added in slot order, then res, and rounded once.
- *   d % 8 == 0, ffn % 8 == 0, 1 <= experts <= 1024, 1 <= k <= 32; rows * k,
- *   experts * d and experts * ffn at most 2^30.  rows == 0 launches nothing.
+ *   d % 8 == 0, ffn % 8 == 0, both at most 2^24, 1 <= experts <= 1024, 1 <= k <=
+ *   32; rows * k, experts * d and experts * ffn at most 2^30, and units of work,
+ *   (rows * k / 256 + min(rows * k, experts)) * ceil(max(d, ffn) / 64) (Q4: rows *
+ *   k / 128), at most 2^27; else FFN_ERR_SHAPE.  rows == 0 launches nothing.
  *   workspace: ffn_moe_workspace_bytes(...) bytes, 16-byte aligned: per (token,
  *   slot) pair a 16-bit copy of x's row, a 16-bit row of h and one fp32 row of
  *   results (up to 8 for at most 1024 pairs, whose down product may be split),

@@ -232,3 +232,20 @@ def test_q4_scales_of_another_16_bit_type_are_refused():
         ffn._moe_q4_weight("w_gate", (qs, good), 3, 32, 128, -1)
     with pytest.raises(ValueError):
         ffn._moe_q4_weight("w_gate", (qs, sc.half()[:2]), 3, 32, 128, -1)
+
+
+def test_rows_too_long_for_a_bounded_wait_are_refused(lib):
+    """A unit of the products reads whole rows of weights within the kernels'
+    limit of a second a wait: up to 2^24 values."""
+    out = ctypes.c_size_t(0)
+
+    def need16(d, ffn):
+        return lib.ffn_moe_workspace_bytes(1, d, ffn, 1, 1, _lib.FFN_BF16, 0, ctypes.byref(out))
+
+    def need4(d, ffn):
+        return lib.ffn_moe_q4_workspace_bytes(1, d, ffn, 1, 1, ctypes.byref(out))
+    top = 1 << 24
+    for need in (need16, need4):
+        assert need(top, 64) == _lib.FFN_OK and need(64, top) == _lib.FFN_OK
+        assert need(top + 32, 64) == _lib.FFN_ERR_SHAPE and need(64, top + 32) == _lib.FFN_ERR_SHAPE
+        assert need(1 << 30, 32) == _lib.FFN_ERR_SHAPE

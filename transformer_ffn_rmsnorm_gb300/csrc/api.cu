@@ -372,7 +372,11 @@ ffn_status plan_moe(int64_t rows, int64_t d, int64_t ffn, int64_t experts, int64
     if (d % step || ffn % step) return FFN_ERR_SHAPE;
     // sorted rows, weight rows and units of work are 32-bit
     const int64_t most = int64_t{1} << 30;
-    if (rows > most || d > most || ffn > most || rows * k > most) return FFN_ERR_SHAPE;
+    if (rows > most || rows * k > most) return FFN_ERR_SHAPE;
+    // One multiprocessor goes through a whole row of d or ffn weights between
+    // two waits of a second; at 2^24 that takes it 0.1 to 0.15 s (a stage of 128
+    // values, 32 to 48 KB, at its share of the memory's rate: 0.7 to 1.1 us).
+    if (d > int64_t{1} << 24 || ffn > int64_t{1} << 24) return FFN_ERR_SHAPE;
     if (experts * d > most || experts * ffn > most) return FFN_ERR_SHAPE;
     m->pairs = rows * k;
     const bool stream = !q4 && m->pairs <= kMoeStreamRows * std::min(m->pairs, experts);
