@@ -49,7 +49,7 @@ typedef enum {
     FFN_ERR_CUDA = 7,       /* a CUDA runtime call failed                          */
     FFN_ERR_TIMEOUT = 8,    /* a kernel abandoned a bounded wait                   */
     FFN_ERR_FLAGS = 9,      /* contradictory or unknown flag bits                  */
-    FFN_ERR_RANGE = 10      /* a weight does not fit the prepared (fp16) format    */
+    FFN_ERR_RANGE = 10      /* a weight or an input is beyond fp16's range         */
 } ffn_status;
 
 typedef enum { FFN_F32 = 0, FFN_F16 = 1, FFN_BF16 = 2 } ffn_dtype;
@@ -190,7 +190,9 @@ ffn_status ffn_moe_route(const void *logits, const float *bias, int32_t *topk_id
  *   fp16's range (a finite value beyond it becomes infinite and records
  *   FFN_ERR_RANGE in the device status word; one below 2^-14 is rounded to a
  *   multiple of 2^-24).  No other flag.
- *   h = silu(G) * U is rounded to the operand type.  Where that is fp16, a
+ *   h = silu(G) * U is rounded to the operand type: for FFN_BF16 without prepared
+ *   weights to one bf16 term (8 bits; the dense block's default has two; prepared
+ *   weights or FFN_F16 keep 11 bits).  Where that type is fp16, a
  *   (token, slot) pair's row of h is held times a power of two that brings its
  *   largest value to 2^-12 .. 2^15, so h may be of any size; values far below
  *   the row's largest are rounded to 2^-24 of that scale.  Everything else is

@@ -161,7 +161,8 @@ def test_rows_of_all_sizes_in_one_tile(env, kind, rows):
     buf, out = xs.clone(), torch.empty_like(xs)
     if kind == "prepared":
         weights = [ffn.ffn_prepare_weights(m) for m in weights]
-        ws = ffn.workspace(ffn.ffn_moe_workspace_bytes(rows, d, f, experts, k, xs.dtype, ffn.FFN_PREPARED_WEIGHTS), "cuda")
+        need = ffn.ffn_moe_workspace_bytes(rows, d, f, experts, k, xs.dtype, ffn.FFN_PREPARED_WEIGHTS)
+        ws = ffn.workspace(need, "cuda")
         def go(): ffn.ffn_moe_forward(buf, idx, w, *weights, flags=ffn.FFN_PREPARED_WEIGHTS, out=out, ws=ws)
     elif kind == "q4":
         ws = ffn.workspace(ffn.ffn_moe_q4_workspace_bytes(rows, d, f, experts, k), "cuda")
@@ -280,3 +281,27 @@ def test_many_calls_with_rows_of_all_sizes(env, kind):
     for j in range(3):
         part = torch.stack([got[i] for i in range(200) if i // 2 % 3 == j])
         assert bool((part == want[j]).all()), int((part != want[j]).flatten(1).any(dim=1).sum())
+
+
+@pytest.mark.parametrize("rows,d,f,experts", [(5, 128, 4768, 2), (40, 256, 14336, 2), (300, 128, 4768, 3),
+                                              (700, 64, 8224, 2), (33, 1056, 2080, 1)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_rows_of_all_sizes(env, kind, rows, d, f, experts):
+    """More levels a row than a warp reads at once, and down products that are
+    split, so that several blocks need the same rows."""
+    torch, ffn = env
+    fg = torch.ones(f, device="cuda")
+    fg[f // 3:f // 2] = 2.0 ** -8
+    fg[f // 2:f // 2 + 640] = 0.0
+    x, idx, w, weights, values = make(torch, kind, rows, d, f, experts, 1, feature_gain=fg)
+    sizes = torch.tensor([0.02, 1.0, 0.0, 3.0, 0.004], device="cuda")
+    size = sizes[torch.arange(rows, device="cuda") % len(sizes)]
+    x = (x * size[:, None]).to(storage(torch, kind))
+    y = call(env, kind, x, idx, w, weights, f)
+    ref, bound = reference(torch, kind, x, idx, w, values)
+    some = size > 0
+    check_rows(torch, y[some], ref[some], bound[some])
+    assert bool((y[~some] == 0).all())
+    for _ in range(10):
+        assert torch.equal(call(env, kind, x, idx, w, weights, f), y)
+    ffn.ffn_device_status()

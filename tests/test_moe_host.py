@@ -169,7 +169,8 @@ def test_workspace_serves_every_smaller_batch(lib, form, d, ffn, experts, k):
     of its input, which is checked after the workspace)."""
     need = workspace_query(lib, form == "q4", _lib.FFN_PREPARED_WEIGHTS if form == "prepared" else 0)
     marks = [1024 // k, 24 * experts // k, 131072 // k, 262144 // k, 393216 // k, 131072 * 5 // k]
-    rows = sorted({r for r in range(1, 700)} | {max(1, m + i) for m in marks for i in range(-3, 4)} | set(range(700, 4000, 97)))
+    near = {max(1, m + i) for m in marks for i in range(-3, 4)}
+    rows = sorted(set(range(1, 700)) | near | set(range(700, 4000, 97)))
     sizes = [need(r, d, ffn, experts, k) for r in rows]
     assert all(a <= b for a, b in zip(sizes, sizes[1:])), [r for r, a, b in zip(rows, sizes, sizes[1:]) if a > b]
 

@@ -227,13 +227,13 @@ const char *ffn_status_string(ffn_status s) {
         case FFN_ERR_NULL: return "a required pointer is NULL";
         case FFN_ERR_SHAPE: return "a size is out of range or breaks a divisibility rule";
         case FFN_ERR_DTYPE: return "unknown or unsupported storage type";
-        case FFN_ERR_ALIGN: return "a pointer is not aligned (to 16 bytes, or to its elements where those are read one by one)";
+        case FFN_ERR_ALIGN: return "a pointer is not aligned (to 16 bytes; index and weight lists to their elements)";
         case FFN_ERR_WORKSPACE: return "workspace missing or too small";
         case FFN_ERR_ALIAS: return "an output overlaps an input";
         case FFN_ERR_CUDA: return "a CUDA runtime call failed";
         case FFN_ERR_TIMEOUT: return "a kernel abandoned a bounded wait";
         case FFN_ERR_FLAGS: return "contradictory or unknown flags";
-        case FFN_ERR_RANGE: return "a weight is outside the prepared format's range";
+        case FFN_ERR_RANGE: return "a weight or an input is outside fp16's range";
     }
     return "unknown status";
 }

@@ -112,9 +112,10 @@ __device__ __forceinline__ void for_row_boxes(const RowMaps &maps, int rows, F l
 }
 
 // silu(gate) * up * scale in fp32.  The division is the approximate one (2 ulp,
-// and 0 for a denominator beyond 2^126, where silu is below 1e-36): next to the
-// 16-bit rounding of h nothing, and a third of the instructions of the
-// correctly rounded reciprocal, in epilogues that the MMAs wait for.
+// and 0 for a denominator beyond 2^126, where silu is below 1e-36), and so is the
+// exponential (2 + 1.17 |gate| ulp, 105 at the end of its range): together at
+// most 1.3e-5 of the value, a fortieth of fp16's half step, and a third of the
+// instructions of the accurate forms in epilogues that the MMAs wait for.
 __device__ __forceinline__ float swiglu(float gate, float up, float scale) {
     return __fdividef(gate, 1.0f + __expf(-gate)) * (up * scale);
 }
@@ -175,8 +176,11 @@ __device__ __forceinline__ int level_of(uint32_t bits) {
 // f0.  Of every 16 columns (from c0, `step` on) the gate warps finish the
 // first eight and the up warps the others; each side hands over what the
 // other needs, through `swap` and named barrier `id`.  PERM: h's columns 1
-// and 2 of every four exchanged.  h feeds the next product: one rounding to
-// its operand type.
+// and 2 of every four exchanged.  h feeds the next product, in its operand type.
+// For bf16 that is one term, 8 bits, where the dense block has two: there the
+// normalised input is rounded as well, here it comes as bf16, and what h's
+// rounding (half a step is 2^-8) adds to y, about 0.17 % rms, is what y's own
+// adds; a second term would double the down product's MMAs and loads of h.
 template <typename T, bool PERM>
 __device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane, const Unit &t, int f0, int wrows, T *h,
                                                 float (*swap)[2][8][64], int c0, int step, int id, float acc_scale,
@@ -237,9 +241,10 @@ __device__ __forceinline__ void swiglu_epilogue(uint32_t taddr, int q, int lane,
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = __floats2half2_rn(hv[2 * i], hv[2 * i + 1]);
-                if (mine != 0 && cm + lane < t.valid)   // (lanes 0 to 7)
-                    reinterpret_cast<int8_t *>(lv.level + static_cast<int64_t>(t.row0 + cm + lane) * lv.nlevel)[f >> 5] =
-                        static_cast<int8_t>(mine);
+                if (mine != 0 && cm + lane < t.valid) {   // (lanes 0 to 7)
+                    uint4 *of_row = lv.level + static_cast<int64_t>(t.row0 + cm + lane) * lv.nlevel;
+                    reinterpret_cast<int8_t *>(of_row)[f >> 5] = static_cast<int8_t>(mine);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -384,8 +389,9 @@ __device__ __forceinline__ void store_epilogue(uint32_t taddr, const Unit &t, in
     float *dst = part + static_cast<int64_t>(t.row0) * wrows + f;
     for (int c = c0; c < t.n; c += step) {
         float *to = dst + static_cast<int64_t>(c) * wrows;
-        if (t.odd && scale) store_columns<true>(taddr + c, to, scale + t.row0 + c, f < wrows, t.valid - c, wrows, acc_scale);
-        else store_columns<false>(taddr + c, to, nullptr, f < wrows, t.valid - c, wrows, acc_scale);
+        const bool live = f < wrows;
+        if (t.odd && scale) store_columns<true>(taddr + c, to, scale + t.row0 + c, live, t.valid - c, wrows, acc_scale);
+        else store_columns<false>(taddr + c, to, nullptr, live, t.valid - c, wrows, acc_scale);
     }
 }
 
@@ -444,9 +450,10 @@ cudaError_t launch_moe_down_q4(const moe::Plan &plan, const void *h, const uint8
                                int splits, int64_t pairs, int64_t d, int64_t ffn, int64_t experts, cudaStream_t s);
 
 // Splits of the down product's reduction on the single-CTA kernels (units of
-// 128 weight rows, counted in stages of 128 values): at most kMoeMaxSplits, none
-// shorter than 4 stages, 1 beyond kMoeSplitPairs pairs.  A function of the sizes
-// alone, so that the workspace query and the call agree.
+// 128 weight rows, counted in stages of 128 values; the Q4 kernel cuts between
+// its stages of 256): at most kMoeMaxSplits, none shorter than 4 stages, 1 beyond
+// kMoeSplitPairs pairs.  A function of the sizes alone, so that the workspace
+// query and the call agree.
 constexpr int kMoeMaxSplits = 8;
 constexpr int64_t kMoeSplitPairs = 1024;
 int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn);

@@ -85,7 +85,7 @@ struct Params {
     const uint16_t *s0, *s1;   // scales of W_gate and W_up, or of W_down
     int nf;                    // feature tiles of 64 (gate/up) or 128 rows
     int wrows;                 // weight rows of an expert (ffn or d)
-    int ngrp;                  // 128-value groups of a row: stages of 128 values
+    int ngrp;                  // 128-value groups of a row; a stage is two
     int splits;                // of the reduction (down)
     int64_t split_stride;      // floats from one split of part to the next
     void *out;
@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t pacc = 0;
         auto walk = walk_units();
-        if constexpr (MODE == DOWN) moe::level_ahead(p.levels, p.tiles, blockIdx.x * kEpiWarps + q, gridDim.x * kEpiWarps, lane);
+        if constexpr (MODE == DOWN)
+            moe::level_ahead(p.levels, p.tiles, blockIdx.x * kEpiWarps + q, gridDim.x * kEpiWarps, lane);
         for (int u = u0; u < units; u += ustep) {
             const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);

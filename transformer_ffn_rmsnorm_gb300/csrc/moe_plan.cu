@@ -12,6 +12,9 @@
 // order of an expert's rows depends on the order of the warps; the results do
 // not: every column of a product is computed the same way wherever it stands.
 //
+// Where h is fp16, the copy also sets the row's levels to 0 and its scale to 1
+// (moe.cuh).
+//
 // The combination adds a token's k fp32 rows in slot order with fp32 weights
 // and rounds once.  Bound by reading those rows.
 #include <algorithm>
@@ -482,9 +485,10 @@ cudaError_t launch_moe_combine(const Plan &plan, const float *w, const float *pa
 // has a fixed cost (its epilogue, the pipeline's fill: about a stage of 128
 // values) and every split a row a pair for the combine kernel to add (about
 // three stages, and the rows' traffic).
-// Down and combine of a call, 1 token, 4 of 32 Q4 experts of 5120 x 2176: one
-// split 28.8 us, two 28.1, three 27.9, four 32.3; 16 tokens, 2 of 8 of 4096 x
-// 14336: one 79.8, two 73.7, four 72.1, seven 78.5.
+// Down plus combine, each timed by itself between events (in a call they overlap
+// a little, and each figure holds some 5 us of launch): 1 token, 4 of 32 Q4
+// experts of 5120 x 2176: one split 28.8 us, two 28.1, three 27.9, four 32.3; 16
+// tokens, 2 of 8 of 4096 x 14336: one 79.8, two 73.7, four 72.1, seven 78.5.
 int moe_down_splits(int64_t pairs, int64_t experts, int64_t d, int64_t ffn) {
     const int64_t units = std::min(pairs, experts) * ((d + 127) / 128), stages = (ffn + 127) / 128;
     constexpr int64_t kSms = 152;   // (not the current device's: the workspace depends on it)

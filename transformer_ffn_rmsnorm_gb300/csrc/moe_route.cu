@@ -9,7 +9,10 @@
 // One warp per token: lane l holds experts l, l + 32, ... in registers,
 // sorted (up to 8 of them; more are scanned each time), and the k largest
 // come out one by one: a warp maximum over the lanes' largest, a warp minimum
-// over the indices that have it.  Bound by the instructions a token takes.
+// over the indices that have it.  Bound by issue and, in a single wave, by the
+// latency of one token's reductions: 630 warp instructions a token at 16384 x
+// 128 bf16, 8 of them (issue 67 % active, 38 % of the warps), 1886 at 4097 x 256
+// with groups and a bias (55 %, 35 %); HBM and L2 are below 6 %.
 //
 // The chosen set is that of the formula in 64 bits although the scores are
 // computed in 32.  Without a bias nothing has to be computed: the order is

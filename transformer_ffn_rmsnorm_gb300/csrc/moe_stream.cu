@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t pacc = 0;
         auto walk = walk_units();
-        if constexpr (MODE == DOWN && !BF16) moe::level_ahead(p.levels, p.tiles, blockIdx.x * 4 + q, gridDim.x * 4, lane);
+        if constexpr (MODE == DOWN && !BF16)
+            moe::level_ahead(p.levels, p.tiles, blockIdx.x * 4 + q, gridDim.x * 4, lane);
         for (int u = u0; u < units; u += ustep) {
             const Unit t = walk.at(u);
             const bool got = ptx::mbar_wait(bar(&bar_tfull[acc]), pacc, abort_flag, kWaitNs);
