@@ -285,6 +285,7 @@ cudaError_t launch_out(const AddNormParams &p, cudaStream_t s) {
         // flight for a CTA's barrier (16384 x 4096 fp16 to e4m3: one vector
         // 106, two 73, four 69 us; copy speed is 69).  At 64 registers a
         // thread: with g kept as well (128) four were slower than two.
+        // Measured at 4096 columns; rows of 256 make CTAs of one warp.
         int vpt = p.rows <= 2 * static_cast<int64_t>(sm_count()) ? 1 : 4;
         while (nvec > vpt * 1024) vpt <<= 1;
         const dim3 block(static_cast<unsigned>(((nvec + vpt - 1) / vpt + 31) / 32 * 32));
