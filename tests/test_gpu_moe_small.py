@@ -305,3 +305,33 @@ def test_long_rows_of_all_sizes(env, kind, rows, d, f, experts):
     for _ in range(10):
         assert torch.equal(call(env, kind, x, idx, w, weights, f), y)
     ffn.ffn_device_status()
+
+
+@pytest.mark.parametrize("kind", ["prepared", "float16"])
+def test_a_rows_scale_does_not_depend_on_its_neighbours(env, kind):
+    """The largest h of a row just below 2^-12, where rounding to fp16 reaches it
+    (h = 32 U, U = 2^-17 (1 - 2^-13)), beside one of 2^-26, which is 0 at the
+    scale of 2^-12 and not at the next: the same bits alone, beside smaller rows
+    and beside larger ones."""
+    torch, ffn = env
+    d, f = 64, 64
+    dt = storage(torch, kind)
+    gate, up, down = (torch.zeros(1, o, i, device="cuda") for o, i in ((f, d), (f, d), (d, f)))
+    gate[0, :, 0] = 32.0
+    up[0, 0, 0], up[0, 0, 1], up[0, 1, 2] = 2.0 ** -17, -2.0 ** -20, 2.0 ** -20
+    down[0, :, 0], down[0, ::2, 1] = 1.0, 128.0   # (prepared weights are below 256)
+    x = torch.zeros(9, d, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -10, 2.0 ** -11
+    x[1:] *= 2.0 ** -4
+    weights = [m.to(dt) for m in (gate, up, down)]
+    idx = torch.zeros(9, 1, dtype=torch.int32, device="cuda")
+    w = torch.full((9, 1), 2.0 ** 10, device="cuda")
+
+    def first(rows):
+        return call(env, kind, rows.to(dt), idx[:len(rows)], w[:len(rows)], weights, f)[0]
+    alone = first(x[:1])
+    assert torch.equal(first(x), alone)
+    large = x.clone()
+    large[1:] *= 256
+    assert torch.equal(first(large), alone)
+    assert bool((alone.double() - 2.0 ** -2).abs().max() <= 2.0 ** -9)

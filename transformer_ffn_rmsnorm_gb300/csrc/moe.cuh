@@ -159,12 +159,14 @@ constexpr int kLevelStep = 16, kMaxLevel = 7, kNoLevel = 127;           // kNoLe
 __device__ __forceinline__ float level_scale(int level) {               // -7 .. 7
     return __uint_as_float(static_cast<uint32_t>(127 + kLevelStep * level) << 23);
 }
-// of a block whose largest magnitude has these bits
+// Of a block whose largest magnitude has these bits.  Level 0 begins where the
+// value rounded to fp16 is 2^-12 (at 2^-12 - 2^-24), as in the epilogue's check
+// of eight columns at once: a row's levels do not depend on the rows beside it.
 __device__ __forceinline__ int level_of(uint32_t bits) {
     if (bits == 0u) return kNoLevel;
     if (bits >= 0x7f800000u) return 0;   // infinity, NaN: nothing to keep
     const int e = static_cast<int>(bits >> 23);   // biased by 127
-    if (e < 115) return min((114 - e) / kLevelStep + 1, kMaxLevel);
+    if (bits < 0x397ff000u) return min((114 - e) / kLevelStep + 1, kMaxLevel);
     if (e >= 142) return max(-((e - 142) / kLevelStep + 1), -kMaxLevel);
     return 0;
 }
