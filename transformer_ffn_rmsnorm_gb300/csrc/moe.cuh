@@ -354,12 +354,14 @@ __device__ __forceinline__ bool level_tile(const Levels &lv, const int4 *tiles, 
     return true;
 }
 
-// Warp w of n idle ones: all odd tiles, from one of its own on.
+// Warp w of n idle ones: the odd tiles from one of its own on.  At most 128, as
+// accumulators wait for it for no more than a second; that is all of 77000, and
+// the others are levelled by who loads them.
 __device__ __forceinline__ void level_ahead(const Levels &lv, const int4 *tiles, int w, int n, int lane) {
     if (__ldcg(lv.header + 2) == 0) return;
     const int count = __ldcg(lv.header);
     const int first = static_cast<int>(static_cast<int64_t>(count) * w / n);
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < min(count, 128); ++i) {
         const int at = first + i < count ? first + i : first + i - count;
         const int4 a = __ldcg(tiles + 2 * at), b = __ldcg(tiles + 2 * at + 1);
         const int valid = min(a.w, b.y - (at - a.y) * a.w);
