@@ -22,7 +22,7 @@
  *   returns an error status and launches nothing.  rows == 0 (an empty batch)
  *   is valid and launches nothing (x, y and n may then be NULL).  Pointers
  *   must be 16-byte aligned, but for a router's logits, indices and weights
- *   (to their element's size).
+ *   (to their element's size) and what an entry names.
  * - After launching, a failed launch is reported as FFN_ERR_CUDA.  A kernel
  *   that gives up a bounded wait records FFN_ERR_TIMEOUT in a device status
  *   word that ffn_device_status() reads; no C++ exception crosses this ABI.
@@ -52,7 +52,8 @@ typedef enum {
     FFN_ERR_RANGE = 10      /* a weight or an input is beyond fp16's range         */
 } ffn_status;
 
-typedef enum { FFN_F32 = 0, FFN_F16 = 1, FFN_BF16 = 2 } ffn_dtype;
+/* FFN_E4M3 (one byte, the "fn" encoding of ffn_fp8_weight) is a type of ffn_moe_sort's rows only */
+typedef enum { FFN_F32 = 0, FFN_F16 = 1, FFN_BF16 = 2, FFN_E4M3 = 3 } ffn_dtype;
 
 /* flags for ffn_block_forward / ffn_block_forward_q4 */
 #define FFN_AUTO 0u
@@ -427,6 +428,121 @@ ffn_status ffn_block_forward_fp8(const void *x, const void *g, ffn_fp8_weight w_
                                  ffn_fp8_weight w_up, ffn_fp8_weight w_down, void *y, int64_t rows,
                                  int64_t d, int64_t ffn, float eps, uint32_t flags, void *workspace,
                                  size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * e4m3 with block scales: the 8-bit layer that ffn_add_rmsnorm_e4m3 (group 128)
+ * begins, dense or with routed experts, for prompts and single tokens:
+ *
+ *   ffn_add_rmsnorm_e4m3 -> [ffn_moe_route -> ffn_moe_sort ->] ffn_gateup_e4m3
+ *     -> ffn_linear_e4m3 [-> ffn_moe_unsort]
+ *
+ * No page describes it.  Activations are codes [rows x in] with a float scale for
+ * each 128 columns of a row, [rows x ceil(in / 128)]; a weight is codes [out x
+ * in] (the encoding of ffn_fp8_weight) with a float scale for each 128 x 128
+ * block, [ceil(out / 128) x ceil(in / 128)], blocks at the edges smaller; the
+ * weights of several experts follow each other, codes and scales.  Scales and
+ * offsets are aligned to 4 bytes: any rows of a batch will do.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    const uint8_t *codes;
+    const float *scales;
+} ffn_e4m3_weight;
+
+/* ------------------------------------------------------------------------
+ * ffn_quantize_e4m3 -- a matrix (or `batch` of them, one after the other) to
+ * codes and scales: a = max(max |x|, 2^-100) over the block, scale = a / 448, q
+ * = e4m3(x * (448 / a)), nearest even, as in ffn_add_rmsnorm_e4m3.
+ *   block_rows 1: a scale for each `group` (32, 64 or 128) columns of a row,
+ *   scales [batch x rows x ceil(d / group)]; any d.
+ *   block_rows 128: a scale for each 128 x 128 block (group 128), scales [batch x
+ *   ceil(rows / 128) x ceil(d / 128)]; d % 16 == 0.  With FFN_QUANT_TRANSPOSE
+ *   codes and scales of each matrix are written transposed, [d x rows] and
+ *   [ceil(d / 128) x ceil(rows / 128)] (rows % 16 == 0): the same values as the
+ *   weight of dX = dY W for ffn_linear_e4m3.
+ *   x of `dtype`; x, q and scales do not overlap.  A NaN in a block makes its
+ *   scale NaN; an infinity makes it infinite, itself NaN and the block's other
+ *   values 0.  FFN_ERR_FLAGS for another flag or a transposed block of rows,
+ *   FFN_ERR_SHAPE for another block, or more than 2^30 scales.
+ * ---------------------------------------------------------------------- */
+#define FFN_QUANT_TRANSPOSE 1u
+ffn_status ffn_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t batch, int64_t rows, int64_t d,
+                             int64_t block_rows, int64_t group, ffn_dtype dtype, uint32_t flags, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_linear_e4m3 -- y[r, o] = [res[r, o] +] sum over blocks b of 128 inputs of
+ *   x_scales[r, b] * w.scales[o / 128, b] * sum_{i in b} x[r, i] * w.codes[o, i]
+ *   The products of codes are exact and added in fp32 block by block, the blocks
+ *   in fp32 (for few rows in up to 8 parts, added in a fixed order: the same bits
+ *   every run), res last; one rounding to `dtype` (any).
+ *   offsets NULL: w is one matrix, experts 1.  Else offsets [experts + 1] int32
+ *   on the device, read when the call runs: rows offsets[e] .. offsets[e + 1] - 1
+ *   are multiplied with expert e's matrix (ffn_moe_sort's offsets); rows of no
+ *   expert, and their places in y, are not touched.  Offsets beyond 0 .. rows
+ *   count as the nearest of the two, an end before its start as the start.
+ *   res [rows x out] of `dtype` or NULL; y may equal res and overlaps nothing else.
+ *   in % 16 == 0, out % 8 == 0, both at most 2^24, 1 <= experts <= 1024, rows and
+ *   experts * out at most 2^30, (rows / 32 + min(rows, experts)) * ceil(out / 128)
+ *   at most 2^27; else FFN_ERR_SHAPE.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_linear_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w, const int32_t *offsets,
+                           const void *res, void *y, int64_t rows, int64_t in, int64_t out, int64_t experts,
+                           ffn_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_gateup_e4m3 -- the block's first half: h = silu(W_gate x) * (W_up x), both
+ * products as in ffn_linear_e4m3, h in fp32 and quantised as ffn_quantize_e4m3 does
+ * with a scale for each 128 of its features: q [rows x ffn], scales [rows x
+ * ceil(ffn / 128)], what ffn_linear_e4m3 takes as x.  w_gate, w_up [experts x ffn
+ * x d]; offsets, limits (in = d, out = ffn) and untouched rows as there.  q and
+ * scales overlap nothing.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w_gate, ffn_e4m3_weight w_up,
+                           const int32_t *offsets, uint8_t *q, float *scales, int64_t rows, int64_t d, int64_t ffn,
+                           int64_t experts, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_moe_sort -- a routed layer's rows in the order of their experts.  The (token,
+ * slot) pairs whose index is in 0 .. experts - 1 are numbered by expert, then token,
+ * then slot:
+ *   pos [rows x k] int32: the pair's number, -1 for a pair without an expert
+ *   offsets [experts + 1] int32: the number of the expert's first pair; the last
+ *   is the number of pairs that have one
+ *   xs [rows * k x d]: xs[pos[t, j]] = x[t]; rows from offsets[experts] on are left
+ *   as they were.  xs_scales [rows * k x nscales] likewise, with x_scales [rows x
+ *   nscales] (e4m3 rows; both NULL without).
+ *   x, xs of `dtype`, FFN_E4M3 among them; d * the type's size % 16 == 0.
+ *   topk_idx [rows x k] as ffn_moe_route writes it.  1 <= experts <= 1024, 1 <= k <=
+ *   32, rows * k and d at most 2^30, nscales at most d.  Index and scale lists are
+ *   aligned to 4 bytes.  Nothing overlaps.
+ *   workspace: ffn_moe_sort_workspace_bytes(...), at most 2 MB (0 up to 256 pairs);
+ *   the answer never falls as rows grow.  The whole call is on `stream` and never
+ *   waits for the device.  rows == 0 writes offsets alone.
+ *   Its gradient, dx[t] = the sum of dxs over t's pairs, is ffn_moe_unsort of dxs
+ *   with w and res NULL.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_moe_sort_workspace_bytes(int64_t rows, int64_t experts, int64_t k, size_t *bytes);
+ffn_status ffn_moe_sort(const void *x, const float *x_scales, const int32_t *topk_idx, void *xs, float *xs_scales,
+                        int32_t *pos, int32_t *offsets, int64_t rows, int64_t d, int64_t nscales, int64_t experts,
+                        int64_t k, ffn_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ffn_moe_unsort -- y[t] = [res[t] +] sum_j w[t, j] * ys[pos[t, j]]: each token's
+ * results back from the order of the experts, weighted and added in fp32 in slot
+ * order, then res, rounded once.
+ *   ys [rows * k x d], pos and w [rows x k] (w fp32, NULL: 1), res (or NULL) and y
+ *   [rows x d]; ys, res, y of `dtype`.  A pair whose position is not in 0 ..
+ *   rows * k - 1 counts nothing, its weight is not read.  y may equal res and
+ *   overlaps nothing else.  d * the type's size % 16 == 0, k and rows as there.
+ * ffn_moe_unsort_backward -- its gradients, from dy [rows x d] (res's is dy
+ * itself): dys[pos[t, j]] = w[t, j] * dy[t] (rows of no pair are left as they
+ * were) and dw[t, j] = the dot product of ys[pos[t, j]] and dy[t], fp32, 0 for a
+ * pair without a position.  dys may equal ys; nothing else overlaps.  Positions
+ * are of different rows, as ffn_moe_sort writes them.
+ * ---------------------------------------------------------------------- */
+ffn_status ffn_moe_unsort(const void *ys, const int32_t *pos, const float *w, const void *res, void *y, int64_t rows,
+                          int64_t d, int64_t k, ffn_dtype dtype, void *stream);
+ffn_status ffn_moe_unsort_backward(const void *dy, const void *ys, const int32_t *pos, const float *w, void *dys,
+                                   float *dw, int64_t rows, int64_t d, int64_t k, ffn_dtype dtype, void *stream);
 
 /* ------------------------------------------------------------------------
  * ffn_block_forward_decode_static -- the decode block (same kernels and

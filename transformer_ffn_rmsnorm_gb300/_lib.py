@@ -23,11 +23,12 @@ STATUS = {
 FFN_OK, FFN_ERR_NULL, FFN_ERR_SHAPE, FFN_ERR_DTYPE, FFN_ERR_ALIGN = 0, 1, 2, 3, 4
 FFN_ERR_WORKSPACE, FFN_ERR_ALIAS, FFN_ERR_CUDA, FFN_ERR_TIMEOUT, FFN_ERR_FLAGS = 5, 6, 7, 8, 9
 FFN_ERR_RANGE = 10
-FFN_F32, FFN_F16, FFN_BF16 = 0, 1, 2
+FFN_F32, FFN_F16, FFN_BF16, FFN_E4M3 = 0, 1, 2, 3
 FFN_AUTO, FFN_GATEUP_FUSED, FFN_GATEUP_UNFUSED, FFN_PATH_GEMM, FFN_PATH_GEMV = 0, 1, 2, 4, 8
 FFN_ACT_SINGLE, FFN_ACT_SPLIT, FFN_PREPARED_WEIGHTS = 16, 32, 64
 FFN_RESIDUAL, FFN_DECODE_ONE_KERNEL = 128, 256
 FFN_ROUTE_SIGMOID, FFN_ROUTE_RENORM = 1, 2
+FFN_QUANT_TRANSPOSE = 1
 
 
 class Q4Weight(ctypes.Structure):
@@ -35,6 +36,10 @@ class Q4Weight(ctypes.Structure):
 
 
 class Fp8Weight(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
+
+
+class E4m3Weight(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
 
 
@@ -85,6 +90,19 @@ SIGNATURES = {
     "ffn_block_forward_q8": (c_int, [c_void_p, c_void_p, Q8Weight, Q8Weight, Q8Weight, c_void_p,
                                      c_int64, c_int64, c_int64, c_float, c_uint32, c_void_p,
                                      c_size_t, c_void_p]),
+    "ffn_quantize_e4m3": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_int64, c_int,
+                                  c_uint32, c_void_p]),
+    "ffn_linear_e4m3": (c_int, [c_void_p, c_void_p, E4m3Weight, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                c_int64, c_int64, c_int, c_void_p]),
+    "ffn_gateup_e4m3": (c_int, [c_void_p, c_void_p, E4m3Weight, E4m3Weight, c_void_p, c_void_p, c_void_p, c_int64,
+                                c_int64, c_int64, c_int64, c_void_p]),
+    "ffn_moe_sort_workspace_bytes": (c_int, [c_int64, c_int64, c_int64, ctypes.POINTER(c_size_t)]),
+    "ffn_moe_sort": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                             c_int64, c_int64, c_int64, c_int, c_void_p, c_size_t, c_void_p]),
+    "ffn_moe_unsort": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int,
+                               c_void_p]),
+    "ffn_moe_unsort_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                        c_int64, c_int, c_void_p]),
     "ffn_block_forward_decode_static": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                                 c_void_p, c_int64, c_int64, c_int64, c_float, c_int,
                                                 c_void_p]),

@@ -18,30 +18,14 @@
 // unsigned integers, where NaN is largest, so a NaN reaches the scale (and
 // q); a row with an infinity has v = NaN there and 0 elsewhere, as the
 // formula says.
-#include "ffn_internal.cuh"
+#include "e4m3.cuh"
 
 namespace ffn {
 namespace {
 
-constexpr float kE4m3Max = 448.f;
 // A row whose squares pass fp32's range is summed again times 2^-96 (fp32 and
 // bf16 values reach 3e38): exact, and far above where squares vanish.
 constexpr float kDown = 1.2621774483536189e-29f;
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// max(a, 2^-100) with NaN kept (both are bit patterns of non-negative floats)
-__device__ __forceinline__ float floor_amax(float a) {
-    const uint32_t b = __float_as_uint(a), lo = __float_as_uint(7.888609052210118e-31f);
-    return __uint_as_float(b > lo ? b : lo);
-}
-
-// two values to e4m3 (lo in the low byte), nearest even, finite values clamped to +-448
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 enum Out { OUT_N = 0, OUT_ROW = 1, OUT_GROUP = 2 };
 

@@ -16,7 +16,9 @@
 
 #include "../../include/ffn.h"
 #include "ffn_internal.cuh"
+#include "linear_e4m3.cuh"
 #include "moe.cuh"
+#include "moe_sort.cuh"
 
 __device__ unsigned g_ffn_status_word;
 
@@ -172,7 +174,8 @@ const char *kernel_name(int kind) {
     static const char *names[K_NUM_KINDS] = {
         "prepare", "rmsnorm", "swiglu", "simt_gateup", "simt_down", "gemv_norm",
         "gemv_gateup", "gemv_down", "gemm_gateup", "gemm_down", "selftest", "splitk_reduce",
-        "gemv_fused", "add_rmsnorm", "moe_route", "moe_plan", "moe_gateup", "moe_down", "moe_combine"};
+        "gemv_fused", "add_rmsnorm", "moe_route", "moe_plan", "moe_gateup", "moe_down", "moe_combine",
+        "quantize", "gateup_e4m3", "linear_e4m3", "moe_sort", "moe_unsort"};
     return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : "unknown";
 }
 
@@ -998,6 +1001,214 @@ ffn_status ffn_timing_read(int kind, uint64_t *launches, double *total_ms) {
     *launches = g_timed_launches[kind];
     *total_ms = g_timed_ms[kind];
     return FFN_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- e4m3 with block scales, sorting
+
+namespace {
+
+constexpr int64_t kMostElements = int64_t{1} << 30;   // of what kernels count in 32 bits
+
+// a product's sizes and pointers but its outputs
+ffn_status check_e4m3(const uint8_t *x, const float *x_scales, const ffn_e4m3_weight *w, int nw, const int32_t *offsets,
+                      int64_t rows, int64_t in, int64_t out, int64_t experts) {
+    if (rows != 0 && (!x || !x_scales)) return FFN_ERR_NULL;
+    for (int i = 0; i < nw; ++i)
+        if (!w[i].codes || !w[i].scales) return FFN_ERR_NULL;
+    if (!offsets && experts != 1) return FFN_ERR_NULL;
+    if (rows < 0 || in < 16 || out < 8 || in % 16 || out % 8 || experts < 1 || experts > moe::kMaxExperts)
+        return FFN_ERR_SHAPE;
+    // one multiprocessor goes through a whole row of `in` between two waits of a second
+    if (rows > kMostElements || in > int64_t{1} << 24 || out > int64_t{1} << 24 || experts * out > kMostElements)
+        return FFN_ERR_SHAPE;
+    // units of work, in tiles of 32 rows and 128 features, times a cluster of up to 8
+    if (moe::max_tiles(rows, experts, 32) * ((out + 127) / 128) > (int64_t{1} << 27)) return FFN_ERR_SHAPE;
+    // (scales and offsets are read one by one)
+    if (!aligned16(x) || !aligned(x_scales, 4) || !aligned(offsets, 4)) return FFN_ERR_ALIGN;
+    for (int i = 0; i < nw; ++i)
+        if (!aligned16(w[i].codes) || !aligned(w[i].scales, 4)) return FFN_ERR_ALIGN;
+    return FFN_OK;
+}
+
+// whether an output overlaps what a product reads
+bool overlaps_e4m3(Range o, const uint8_t *x, const float *x_scales, const ffn_e4m3_weight *w, int nw,
+                   const int32_t *offsets, int64_t rows, int64_t in, int64_t out, int64_t experts) {
+    const size_t nb = static_cast<size_t>((in + 127) / 128), nf = static_cast<size_t>((out + 127) / 128);
+    bool bad = overlaps(o, {x, static_cast<size_t>(rows) * in}) || overlaps(o, {x_scales, rows * nb * 4}) ||
+               overlaps(o, {offsets, static_cast<size_t>(experts + 1) * 4});
+    for (int i = 0; i < nw; ++i)
+        bad = bad || overlaps(o, {w[i].codes, static_cast<size_t>(experts) * out * in}) ||
+              overlaps(o, {w[i].scales, experts * nf * nb * 4});
+    return bad;
+}
+
+e4::Params e4m3_params(const float *x_scales, const int32_t *offsets, int64_t rows, int64_t out, int64_t experts) {
+    e4::Params p{};
+    p.xs = x_scales;
+    p.offsets = offsets;
+    p.rows = static_cast<int>(rows);
+    p.experts = static_cast<int>(experts);
+    p.out = static_cast<int>(out);
+    return p;
+}
+
+// bytes of an element that the sort copies, 0: unknown type
+size_t sort_element(ffn_dtype dt) { return dt == FFN_E4M3 ? 1 : valid_dtype(dt) ? dtype_size(dt) : 0; }
+
+ffn_status check_order(int64_t rows, int64_t d, int64_t k, size_t es) {
+    if (rows < 0 || d < 1 || k < 1 || k > 32 || rows > kMostElements || rows * k > kMostElements) return FFN_ERR_SHAPE;
+    if (d > kMostElements || d * es % 16) return FFN_ERR_SHAPE;
+    return FFN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ffn_status ffn_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t batch, int64_t rows, int64_t d,
+                             int64_t block_rows, int64_t group, ffn_dtype dtype, uint32_t flags, void *stream) {
+    if (batch != 0 && rows != 0 && (!x || !q || !scales)) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    const bool blocks = block_rows == 128, transpose = (flags & FFN_QUANT_TRANSPOSE) != 0;
+    if ((flags & ~FFN_QUANT_TRANSPOSE) || (transpose && !blocks)) return FFN_ERR_FLAGS;
+    if (batch < 0 || rows < 0 || d < 1 || (block_rows != 1 && !blocks)) return FFN_ERR_SHAPE;
+    if (group != 128 && (blocks || (group != 32 && group != 64))) return FFN_ERR_SHAPE;
+    if (d > (INT32_MAX >> 1) || rows > kMostElements || batch > kMostElements) return FFN_ERR_SHAPE;
+    if (blocks && (d % 16 || (transpose && rows % 16))) return FFN_ERR_SHAPE;
+    const int64_t ng = (d + group - 1) / group, nr = blocks ? (rows + 127) / 128 : rows;
+    if (batch * nr > kMostElements || batch * nr * ng > kMostElements) return FFN_ERR_SHAPE;   // launched blocks
+    if (rows == 0 || batch == 0) return FFN_OK;
+    if (!aligned16(x) || !aligned16(q) || !aligned(scales, 4)) return FFN_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(batch) * rows * d;
+    const Range rx{x, n * dtype_size(dtype)}, rq{q, n}, rs{scales, static_cast<size_t>(batch * nr * ng) * 4};
+    if (overlaps(rq, rx) || overlaps(rs, rx) || overlaps(rq, rs)) return FFN_ERR_ALIAS;
+    return from_cuda(launch_quantize_e4m3(x, q, scales, batch, rows, d, group, blocks, transpose, dtype,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+ffn_status ffn_linear_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w, const int32_t *offsets,
+                           const void *res, void *y, int64_t rows, int64_t in, int64_t out, int64_t experts,
+                           ffn_dtype dtype, void *stream) {
+    if (rows != 0 && !y) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    const ffn_status st = check_e4m3(x, x_scales, &w, 1, offsets, rows, in, out, experts);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    if (!aligned16(res) || !aligned16(y)) return FFN_ERR_ALIGN;
+    const size_t yb = static_cast<size_t>(rows) * out * dtype_size(dtype);
+    if (overlaps_e4m3({y, yb}, x, x_scales, &w, 1, offsets, rows, in, out, experts)) return FFN_ERR_ALIAS;
+    if (y != res && overlaps({y, yb}, {res, yb})) return FFN_ERR_ALIAS;   // (or in res's place)
+    e4::Params p = e4m3_params(x_scales, offsets, rows, out, experts);
+    p.ws[0] = w.scales;
+    p.y = y;
+    p.res = res;
+    p.dt = dtype;
+    return from_cuda(launch_e4m3_product(e4::LINEAR, x, w.codes, w.codes, in, p, static_cast<cudaStream_t>(stream)));
+}
+
+ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w_gate, ffn_e4m3_weight w_up,
+                           const int32_t *offsets, uint8_t *q, float *scales, int64_t rows, int64_t d, int64_t ffn,
+                           int64_t experts, void *stream) {
+    if (rows != 0 && (!q || !scales)) return FFN_ERR_NULL;
+    const ffn_e4m3_weight w[2] = {w_gate, w_up};
+    const ffn_status st = check_e4m3(x, x_scales, w, 2, offsets, rows, d, ffn, experts);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    if (!aligned16(q) || !aligned(scales, 4)) return FFN_ERR_ALIGN;
+    const Range rq{q, static_cast<size_t>(rows) * ffn}, rs{scales, static_cast<size_t>(rows) * ((ffn + 127) / 128) * 4};
+    for (const Range &o : {rq, rs})
+        if (overlaps_e4m3(o, x, x_scales, w, 2, offsets, rows, d, ffn, experts)) return FFN_ERR_ALIAS;
+    if (overlaps(rq, rs)) return FFN_ERR_ALIAS;
+    e4::Params p = e4m3_params(x_scales, offsets, rows, ffn, experts);
+    p.ws[0] = w_gate.scales;
+    p.ws[1] = w_up.scales;
+    p.y = q;
+    p.ys = scales;
+    return from_cuda(
+        launch_e4m3_product(e4::GATEUP, x, w_gate.codes, w_up.codes, d, p, static_cast<cudaStream_t>(stream)));
+}
+
+ffn_status ffn_moe_sort_workspace_bytes(int64_t rows, int64_t experts, int64_t k, size_t *bytes) {
+    if (!bytes) return FFN_ERR_NULL;
+    if (experts < 1 || experts > moe::kMaxExperts) return FFN_ERR_SHAPE;
+    const ffn_status st = check_order(rows, 16, k, 1);
+    if (st == FFN_OK) *bytes = moe_sort_workspace(rows * k, experts);
+    return st;
+}
+
+ffn_status ffn_moe_sort(const void *x, const float *x_scales, const int32_t *topk_idx, void *xs, float *xs_scales,
+                        int32_t *pos, int32_t *offsets, int64_t rows, int64_t d, int64_t nscales, int64_t experts,
+                        int64_t k, ffn_dtype dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!offsets || (rows != 0 && (!x || !topk_idx || !xs || !pos))) return FFN_ERR_NULL;
+    if ((x_scales == nullptr) != (xs_scales == nullptr)) return FFN_ERR_NULL;
+    const size_t es = sort_element(dtype);
+    if (!es) return FFN_ERR_DTYPE;
+    if (experts < 1 || experts > moe::kMaxExperts || nscales < 0 || nscales > d || (x_scales && nscales < 1))
+        return FFN_ERR_SHAPE;
+    const ffn_status st = check_order(rows, d, k, es);
+    if (st != FFN_OK) return st;
+    const size_t need = moe_sort_workspace(rows * k, experts);
+    if (need && (!workspace || workspace_bytes < need)) return FFN_ERR_WORKSPACE;
+    if (!aligned16(x) || !aligned16(xs) || !aligned16(workspace)) return FFN_ERR_ALIGN;
+    for (const void *p : {static_cast<const void *>(topk_idx), static_cast<const void *>(pos),
+                          static_cast<const void *>(offsets), static_cast<const void *>(x_scales),
+                          static_cast<const void *>(xs_scales)})
+        if (!aligned(p, 4)) return FFN_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(rows), row = static_cast<size_t>(d) * es, sc = x_scales ? nscales * 4 : 0;
+    const Range in[3] = {{x, n * row}, {topk_idx, n * k * 4}, {x_scales, n * sc}};
+    const Range outs[5] = {{xs, n * k * row}, {xs_scales, n * k * sc}, {pos, n * k * 4},
+                           {offsets, static_cast<size_t>(experts + 1) * 4}, {workspace, need}};
+    for (int i = 0; i < 5; ++i) {
+        for (const Range &r : in)
+            if (overlaps(outs[i], r)) return FFN_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i], outs[j])) return FFN_ERR_ALIAS;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) return from_cuda(cudaMemsetAsync(offsets, 0, static_cast<size_t>(experts + 1) * 4, s));
+    return from_cuda(launch_moe_sort(x, x_scales, topk_idx, xs, xs_scales, pos, offsets, rows,
+                                     static_cast<int64_t>(row), nscales, static_cast<int>(experts),
+                                     static_cast<int>(k), workspace, s));
+}
+
+ffn_status ffn_moe_unsort(const void *ys, const int32_t *pos, const float *w, const void *res, void *y, int64_t rows,
+                          int64_t d, int64_t k, ffn_dtype dtype, void *stream) {
+    if (rows != 0 && (!ys || !pos || !y)) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    const size_t es = dtype_size(dtype);
+    const ffn_status st = check_order(rows, d, k, es);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    if (!aligned16(ys) || !aligned16(res) || !aligned16(y) || !aligned(pos, 4) || !aligned(w, 4)) return FFN_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(rows), row = static_cast<size_t>(d) * es;
+    const Range ry{y, n * row}, rr{res, n * row};
+    for (const Range &in : {Range{ys, n * k * row}, Range{pos, n * k * 4}, Range{w, n * k * 4}})
+        if (overlaps(ry, in)) return FFN_ERR_ALIAS;
+    if (y != res && overlaps(ry, rr)) return FFN_ERR_ALIAS;   // (or in res's place)
+    return from_cuda(launch_moe_unsort(ys, pos, w, res, y, rows, d, static_cast<int>(k), dtype,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+ffn_status ffn_moe_unsort_backward(const void *dy, const void *ys, const int32_t *pos, const float *w, void *dys,
+                                   float *dw, int64_t rows, int64_t d, int64_t k, ffn_dtype dtype, void *stream) {
+    if (rows != 0 && (!dy || !ys || !pos || !w || !dys || !dw)) return FFN_ERR_NULL;
+    if (!valid_dtype(dtype)) return FFN_ERR_DTYPE;
+    const size_t es = dtype_size(dtype);
+    const ffn_status st = check_order(rows, d, k, es);
+    if (st != FFN_OK) return st;
+    if (rows == 0) return FFN_OK;
+    if (!aligned16(dy) || !aligned16(ys) || !aligned16(dys) || !aligned(pos, 4) || !aligned(w, 4) || !aligned(dw, 4))
+        return FFN_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(rows), row = static_cast<size_t>(d) * es;
+    const Range ro{dys, n * k * row}, rw{dw, n * k * 4};
+    for (const Range &in : {Range{dy, n * row}, Range{pos, n * k * 4}, Range{w, n * k * 4}})
+        if (overlaps(ro, in) || overlaps(rw, in)) return FFN_ERR_ALIAS;
+    const Range rys{ys, n * k * row};   // dys may take ys's place: a row is read where it is written
+    if ((dys != ys && overlaps(ro, rys)) || overlaps(rw, rys) || overlaps(ro, rw)) return FFN_ERR_ALIAS;
+    return from_cuda(launch_moe_unsort_backward(dy, ys, pos, w, dys, dw, rows, d, static_cast<int>(k), dtype,
+                                                static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -35,6 +35,11 @@ enum KernelKind : int {
     K_MOE_GATEUP,
     K_MOE_DOWN,
     K_MOE_COMBINE,
+    K_QUANTIZE,
+    K_GATEUP_E4M3,
+    K_LINEAR_E4M3,
+    K_MOE_SORT,
+    K_MOE_UNSORT,
     K_NUM_KINDS
 };
 const char *kernel_name(int kind);

@@ -18,8 +18,8 @@ from . import _lib
 from ._lib import (FFN_AUTO, FFN_BF16, FFN_F16, FFN_F32, FFN_GATEUP_FUSED,  # noqa: F401
                    FFN_GATEUP_UNFUSED, FFN_ACT_SINGLE, FFN_ACT_SPLIT, FFN_PATH_GEMM,
                    FFN_PATH_GEMV, FFN_PREPARED_WEIGHTS, FFN_RESIDUAL, FFN_DECODE_ONE_KERNEL,
-                   FFN_ROUTE_RENORM, FFN_ROUTE_SIGMOID,
-                   Fp8Weight, Q4Weight, Q8Weight)
+                   FFN_ROUTE_RENORM, FFN_ROUTE_SIGMOID, FFN_E4M3, FFN_QUANT_TRANSPOSE,
+                   E4m3Weight, Fp8Weight, Q4Weight, Q8Weight)
 
 _DT = {torch.float32: FFN_F32, torch.float16: FFN_F16, torch.bfloat16: FFN_BF16}
 
@@ -281,6 +281,224 @@ def ffn_moe_forward_q4(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor
             wg, wu, wd, None if res is None else res.data_ptr(), y.data_ptr(), rows, d, ffn, experts, k,
             ws.data_ptr(), ws.numel() * ws.element_size())
     return y
+
+
+def ffn_quantize_e4m3(x: torch.Tensor, block_rows: int = 1, group: int = 128, transpose: bool = False,
+                      out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """(q, scales): torch.float8_e4m3fn codes and fp32 scales of x [..., rows, d].
+
+    block_rows 1: a scale for each `group` (32, 64, 128) columns of a row, scales
+    [..., rows, ceil(d / group)] (activations).  block_rows 128: a scale for each
+    128 x 128 block of each matrix, scales [..., ceil(rows / 128), ceil(d / 128)]
+    (weights); with `transpose` q and scales of the transposed matrices."""
+    if stream is not None:   # outputs made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_quantize_e4m3(x, block_rows, group, transpose, out, scales)
+    if x.dim() < 2 and block_rows != 1:
+        raise ValueError("blocks of rows need a matrix")
+    n, d, dev = _rows_of(x)
+    code = _dtype(x)
+    rows = x.shape[-2] if x.dim() > 1 else 1
+    batch = n // rows if rows else 0
+    shape, ng = x.shape, (-(-d // group) if group > 0 else 1)
+    sshape = shape[:-1] + (ng,) if block_rows == 1 else shape[:-2] + (-(-rows // 128), ng)
+    if transpose and block_rows != 1:
+        shape = shape[:-2] + (d, rows)
+        sshape = sshape[:-2] + (ng, -(-rows // 128))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _expect("out", out, shape, torch.float8_e4m3fn, dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
+    else:
+        _expect("scales", scales, sshape, torch.float32, dev)
+    _launch(_LIB.ffn_quantize_e4m3, "ffn_quantize_e4m3", dev, x.data_ptr(), out.data_ptr(), scales.data_ptr(), batch,
+            rows, d, block_rows, group, code, FFN_QUANT_TRANSPOSE if transpose else 0)
+    return out, scales
+
+
+def _e4m3_inputs(x, x_scales, weights, names, offsets):
+    """Checks what both e4m3 products take; (rows, in, out, experts, device index, weights for the C side)."""
+    rows, inn, dev = _rows_of(x)
+    if x.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"x must be torch.float8_e4m3fn, is {x.dtype}")
+    blocks = -(-inn // 128)
+    _expect("x_scales", x_scales, x.shape[:-1] + (blocks,), torch.float32, dev)
+    q0 = weights[0][0]
+    if q0.dim() != (2 if offsets is None else 3):
+        raise ValueError("weights are [out, in], or [experts, out, in] with offsets")
+    experts, out = (1 if offsets is None else q0.shape[0]), q0.shape[-2]
+    lead = q0.shape[:-2]
+    if offsets is not None:
+        _expect("offsets", offsets, (experts + 1,), torch.int32, dev)
+    ws = []
+    for name, (q, s) in zip(names, weights):
+        _expect(name + " codes", q, lead + (out, inn), torch.float8_e4m3fn, dev)
+        _expect(name + " scales", s, lead + (-(-out // 128), blocks), torch.float32, dev)
+        ws.append(E4m3Weight(q.data_ptr(), s.data_ptr()))
+    return rows, inn, out, experts, dev, ws
+
+
+def ffn_linear_e4m3(x: torch.Tensor, x_scales: torch.Tensor, w, offsets: torch.Tensor | None = None,
+                    res: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = [res +] x W^T of e4m3 codes with block scales.  x [..., in] with
+    x_scales [..., ceil(in / 128)]; w is a (codes [out, in], scales [ceil(out /
+    128), ceil(in / 128)]) pair, or with `offsets` (ffn_moe_sort's) one with a leading
+    dimension of experts, x's rows then in their order; rows of no expert keep
+    what `out` holds.  y has the type of `out`, `res` or `dtype`."""
+    if stream is not None:   # outputs made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_linear_e4m3(x, x_scales, w, offsets, res, dtype, out)
+    rows, inn, o, experts, dev, (wt,) = _e4m3_inputs(x, x_scales, (w,), ("w",), offsets)
+    dt = out.dtype if out is not None else res.dtype if res is not None else dtype
+    if dt not in _DT:
+        raise TypeError(f"unsupported dtype {dt}")
+    shape = x.shape[:-1] + (o,)
+    if res is not None:
+        _expect("res", res, shape, dt, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    else:
+        _expect("out", out, shape, dt, dev)
+    _launch(_LIB.ffn_linear_e4m3, "ffn_linear_e4m3", dev, x.data_ptr(), x_scales.data_ptr(), wt,
+            None if offsets is None else offsets.data_ptr(), None if res is None else res.data_ptr(), out.data_ptr(),
+            rows, inn, o, experts, _DT[dt])
+    return out
+
+
+def ffn_gateup_e4m3(x: torch.Tensor, x_scales: torch.Tensor, w_gate, w_up, offsets: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """(q, scales): h = silu(x W_gate^T) * (x W_up^T) as e4m3 codes [..., ffn] with a
+    scale for each 128 features; x, weights and `offsets` as in ffn_linear_e4m3."""
+    if stream is not None:   # outputs made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_gateup_e4m3(x, x_scales, w_gate, w_up, offsets, out, scales)
+    rows, d, ffn, experts, dev, (wg, wu) = _e4m3_inputs(x, x_scales, (w_gate, w_up), ("w_gate", "w_up"), offsets)
+    lead = x.shape[:-1]
+    if out is None:
+        out = torch.empty(lead + (ffn,), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _expect("out", out, lead + (ffn,), torch.float8_e4m3fn, dev)
+    if scales is None:
+        scales = torch.empty(lead + (-(-ffn // 128),), dtype=torch.float32, device=x.device)
+    else:
+        _expect("scales", scales, lead + (-(-ffn // 128),), torch.float32, dev)
+    _launch(_LIB.ffn_gateup_e4m3, "ffn_gateup_e4m3", dev, x.data_ptr(), x_scales.data_ptr(), wg, wu,
+            None if offsets is None else offsets.data_ptr(), out.data_ptr(), scales.data_ptr(), rows, d, ffn, experts)
+    return out, scales
+
+
+def ffn_moe_sort_workspace_bytes(rows: int, experts: int, k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_LIB.ffn_moe_sort_workspace_bytes(rows, experts, k, ctypes.byref(out)), "ffn_moe_sort_workspace_bytes")
+    return out.value
+
+
+_SORT_DT = {**_DT, torch.float8_e4m3fn: FFN_E4M3}
+
+
+def ffn_moe_sort(x: torch.Tensor, idx: torch.Tensor, experts: int, x_scales: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 pos: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None, stream=None):
+    """(xs, xs_scales, pos, offsets): the rows of x [..., d] (e4m3 codes with
+    x_scales, or a float type; xs_scales is None without) in the order of their
+    experts, xs [rows * k, d]; pos [..., k] names each (token, slot) pair's row
+    there, -1 without an expert, offsets [experts + 1] the experts' first rows."""
+    if stream is not None:   # outputs and workspaces made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_sort(x, idx, experts, x_scales, out, scales, pos, offsets, ws)
+    rows, d, dev = _rows_of(x)
+    if x.dtype not in _SORT_DT:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    k = idx.shape[-1]
+    _expect("idx", idx, x.shape[:-1] + (k,), torch.int32, dev)
+    pairs, ns = rows * k, 0
+    if x_scales is not None:
+        ns = x_scales.shape[-1]
+        _expect("x_scales", x_scales, x.shape[:-1] + (ns,), torch.float32, dev)
+        if scales is None:
+            scales = torch.empty((pairs, ns), dtype=torch.float32, device=x.device)
+        else:
+            _expect("scales", scales, (pairs, ns), torch.float32, dev)
+    elif scales is not None:
+        raise ValueError("scales without x_scales")
+    if out is None:
+        out = torch.empty((pairs, d), dtype=x.dtype, device=x.device)
+    else:
+        _expect("out", out, (pairs, d), x.dtype, dev)
+    if pos is None:
+        pos = torch.empty(idx.shape, dtype=torch.int32, device=x.device)
+    else:
+        _expect("pos", pos, idx.shape, torch.int32, dev)
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=x.device)
+    else:
+        _expect("offsets", offsets, (experts + 1,), torch.int32, dev)
+    if ws is None:
+        ws = workspace(ffn_moe_sort_workspace_bytes(rows, experts, k), x.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous CUDA tensor on the device of the input")
+    _launch(_LIB.ffn_moe_sort, "ffn_moe_sort", dev, x.data_ptr(), None if x_scales is None else x_scales.data_ptr(),
+            idx.data_ptr(), out.data_ptr(), None if scales is None else scales.data_ptr(), pos.data_ptr(),
+            offsets.data_ptr(), rows, d, ns, experts, k, _SORT_DT[x.dtype], ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return out, scales, pos, offsets
+
+
+def ffn_moe_unsort(ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor | None = None,
+                   res: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [..., d] = [res +] the sum over a token's slots of weight * ys[pos]
+    (weights None: 1, the gradient of ffn_moe_sort); ys [rows * k, d], pos and
+    weights [..., k]."""
+    if stream is not None:   # outputs made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_unsort(ys, pos, weights, res, out)
+    _, d, dev = _rows_of(ys)
+    code, k = _dtype(ys), pos.shape[-1]
+    pairs, lead = pos.numel(), pos.shape[:-1]
+    _expect("ys", ys, (pairs, d), ys.dtype, dev)
+    _expect("pos", pos, pos.shape, torch.int32, dev)
+    if weights is not None:
+        _expect("weights", weights, pos.shape, torch.float32, dev)
+    if res is not None:
+        _expect("res", res, lead + (d,), ys.dtype, dev)
+    if out is None:
+        out = torch.empty(lead + (d,), dtype=ys.dtype, device=ys.device)
+    else:
+        _expect("out", out, lead + (d,), ys.dtype, dev)
+    _launch(_LIB.ffn_moe_unsort, "ffn_moe_unsort", dev, ys.data_ptr(), pos.data_ptr(),
+            None if weights is None else weights.data_ptr(), None if res is None else res.data_ptr(), out.data_ptr(),
+            pairs // k if k else 0, d, k, code)
+    return out
+
+
+def ffn_moe_unsort_backward(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                            dys: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
+    """(dys, dw): the gradients of ffn_moe_unsort with respect to ys and weights,
+    from y's.  Rows of ys that no pair names keep what `dys` holds (0 where it is
+    made here); `dys` may be ys."""
+    if stream is not None:   # outputs made here belong to that stream
+        with torch.cuda.stream(stream):
+            return ffn_moe_unsort_backward(dy, ys, pos, weights, dys, dw)
+    rows, d, dev = _rows_of(dy)
+    code, k = _dtype(dy), pos.shape[-1]
+    _expect("pos", pos, dy.shape[:-1] + (k,), torch.int32, dev)
+    _expect("weights", weights, pos.shape, torch.float32, dev)
+    _expect("ys", ys, (rows * k, d), dy.dtype, dev)
+    if dys is None:
+        dys = torch.zeros_like(ys)
+    else:
+        _expect("dys", dys, ys.shape, dy.dtype, dev)
+    if dw is None:
+        dw = torch.empty(pos.shape, dtype=torch.float32, device=dy.device)
+    else:
+        _expect("dw", dw, pos.shape, torch.float32, dev)
+    _launch(_LIB.ffn_moe_unsort_backward, "ffn_moe_unsort_backward", dev, dy.data_ptr(), ys.data_ptr(),
+            pos.data_ptr(), weights.data_ptr(), dys.data_ptr(), dw.data_ptr(), rows, d, k, code)
+    return dys, dw
 
 
 def ffn_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, out: torch.Tensor | None = None,
