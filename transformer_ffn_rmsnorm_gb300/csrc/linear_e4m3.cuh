@@ -82,6 +82,8 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
                                 e4::Params p, cudaStream_t s);
 cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8_t *x, const uint8_t *w0,
                                const uint8_t *w1, int64_t in, const e4::Params &p, cudaStream_t s);
+cudaError_t launch_e4m3_pair(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
+                             const e4::Params &p, cudaStream_t s);
 
 cudaError_t launch_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t batch, int64_t rows, int64_t d,
                                  int64_t group, bool blocks, bool transpose, int dt, cudaStream_t s);

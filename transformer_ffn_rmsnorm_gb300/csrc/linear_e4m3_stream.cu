@@ -437,6 +437,7 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
     p.nkb = static_cast<int>((in + 127) / 128);
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
+    if (p.rows > 128 * static_cast<int64_t>(p.experts)) return launch_e4m3_pair(mode, x, w0, w1, in, p, s);
     const bool wide = p.rows > 32 * static_cast<int64_t>(p.experts);
     int splits = 8;
     while (splits > 1 && 2 * splits > p.nkb) splits >>= 1;
