@@ -48,6 +48,13 @@ struct Unit {
     int expert, f, row0, valid;
 };
 
+// Says that a block's sums have been read.  They are in tensor memory and ordered by
+// the fence before; no write of memory is released, so the arrival does not wait
+// for those on their way (a release at the cluster's scope did, a third of the time).
+__device__ __forceinline__ void arrive_read(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
@@ -291,23 +298,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * 128;
-                uint32_t r[2][32];
-                ptx::tmem_ld_32x32b_x32(taddr, r[0]);
+                uint32_t r[2][16];   // (32 at a time spill)
+                ptx::tmem_ld_32x32b_x16(taddr, r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     ptx::tmem_ld_wait();
-                    if (c < 3) ptx::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
-                    if (c == 3) {
+                    if (c < 7) {
+                        ptx::tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+                    } else {
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (leader) ptx::mbar_arrive(bar(&bar_tempty[a]));
-                            else ptx::mbar_arrive_cluster(lead(bar(&bar_tempty[a])));
-                        }
+                        if (lane == 0) arrive_read(lead(bar(&bar_tempty[a])));
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        fma2(acc[16 * c + i], pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2);
+                    for (int i = 0; i < 8; ++i)
+                        fma2(acc[8 * c + i], pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2);
                 }
                 a ^= 1;
                 if (a == 0) pa ^= 1u;
