@@ -2,24 +2,36 @@
 //
 // CTA pairs (tcgen05 .cta_group::2): a unit of work is 256 rows of x (128 in each
 // CTA, the M operand) against 256 weight rows (linear: 256 features; gate/up:
-// the 128 features of one scale block, gate's rows in the even CTA's half of the N
-// operand, up's in the odd one's).  A block of 128 values is four instructions into
-// one of two accumulators, which together are all of tensor memory.
+// the 128 features of one scale block, gate's rows from the even CTA's memory, up's
+// from the odd one's).  A block of 128 values is multiplied in two halves of N = 128,
+// each into one of four accumulators, which together are all of tensor memory; a
+// gate/up half holds 64 features' gate and up columns, so that they meet in a thread.
 //
-// What bounds it: the tensor pipe, 512 cycles a block and SM, under which the
-// epilogue warps read the block's 128 x 256 sums (256 cycles of tensor-memory
-// reads) and add them, times the row's and the weight block's scale, to registers
-// (128 a thread; two additions an instruction).  With x on the M side a thread's
-// sums share one row, so that one factor serves all 128 of them; on the N side
-// every column would need its own from shared memory, which the operands fill.
+// What bounds it: each block's sums have to leave tensor memory before the block
+// after next may use their place.  The tensor pipe needs 512 cycles a block and SM
+// and reads its accumulators at 75 % of tensor memory's rate, the epilogue warps'
+// loads are the other 25 %, their additions 256 cycles of the FMA pipe (two an
+// instruction); but the way of a half -- instructions issued, sums done, seen,
+// read and added, their leave sent back across the pair, seen -- is about 1500
+// cycles, of which two halves' 512 are hidden: 890 cycles a block.  (4096 tokens,
+// 4096 -> 11008 gate/up: 284 us; without reading and adding 228, with one such
+// handshake in 16 blocks 195.  Two accumulators of N = 256 took 349; 16 warps of 64
+// columns, whose sums do not fit beside what else the registers hold, 441; one warp
+// issuing both halves' MMAs 387.)
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs (the even CTA's), warps 4-11 add the
-// sums (lane = row of x; four warps for each half of the columns) and finish the
-// unit while the next one's first two blocks run.  Every wait is bounded (1 s).
+// With x on the M side a thread's sums share one row, so that one factor serves all
+// of its columns; on the N side every column would need its own from shared memory,
+// which the operands fill.
+//
+// Roles: warp 0 loads, warps 1 and 2 issue the MMAs of a half each (the even CTA's),
+// warp 3 brings the scales of the CTA's rows to shared memory four blocks at a time,
+// warps 4-11 add the sums (lane = row of x; four warps for each half) and finish the
+// unit while the next one's first blocks run.  Every wait is bounded (1 s).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "linear_e4m3.cuh"
 #include "moe.cuh"
@@ -33,15 +45,16 @@ using e4::Params;
 
 constexpr int kRows = 256;                                 // of x in a unit
 constexpr uint32_t kStageBytes = 2 * e4::kTileBytes;       // one CTA's rows of x and of the weights
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8, kThreads = 32 * (4 + kEpiWarps);
-constexpr uint32_t kOutBytes = kEpiWarps * 4096;           // where rows are turned for the stores
-constexpr size_t kSmem = kStages * kStageBytes + kOutBytes + 1024;
-static_assert(kSmem > 114 * 1024 && kSmem < 212 * 1024, "one CTA per SM: each allocates all of tensor memory");
+constexpr size_t kSmem = kStages * kStageBytes + 1024;
+static_assert(kSmem > 114 * 1024 && kSmem < 210 * 1024, "one CTA per SM: each allocates all of tensor memory");
 constexpr uint32_t kTmemCols = 512;
-// Registers of a thread after the warpgroups have shared them out: 168 at launch.
-constexpr int kFewRegs = 56, kManyRegs = 224;
+// Registers of a thread after the warpgroups have shared them out: 168 at launch.  (Where a
+// role spilled, the issuers at 56 and the sums at 208, a block took up to twice the time.)
+constexpr int kFewRegs = 72, kManyRegs = 216;
 static_assert(4 * 32 * kFewRegs + kEpiWarps * 32 * kManyRegs <= kThreads * 168, "register split");
+constexpr int kScaleBlocks = 4;   // blocks whose scales are handed over together
 constexpr int kBand = 16;   // tiles of rows that go through all features together: what they read stays in L2
 
 struct Unit {
@@ -70,16 +83,37 @@ __device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
 __device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
-__device__ __forceinline__ void sts128(uint32_t at, float a, float b, float c, float d) {
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
-}
-__device__ __forceinline__ float4 lds128(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(at)
+// 32 bytes, a whole sector of L2, at an address that is a multiple of it
+__device__ __forceinline__ void st_sector(void *at, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-    return v;
+}
+// 32 bytes of y, v rounded to T (plus res's, if there is one), of which `left`
+// elements, a multiple of 8, are y's.  Rows begin on multiples of 16 bytes.
+template <typename T> __device__ __forceinline__ void store_sector(T *to, const T *res, float *v, int left) {
+    constexpr int N = 32 / sizeof(T);
+    uint4 o[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float f[N / 2];
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) f[e] = v[i * N / 2 + e];
+        if (res && i * N / 2 < left) {
+            float r[N / 2];
+            Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(res + i * N / 2), r);
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) f[e] += r[e];
+        }
+        o[i] = Vec16<T>::pack(f);
+    }
+    if ((reinterpret_cast<uintptr_t>(to) & 31) == 0 && left >= N) {
+        const uint32_t w[8] = {o[0].x, o[0].y, o[0].z, o[0].w, o[1].x, o[1].y, o[1].z, o[1].w};
+        st_sector(to, w);
+    } else {
+        if (left > 0) *reinterpret_cast<uint4 *>(to) = o[0];
+        if (left > N / 2) *reinterpret_cast<uint4 *>(to + N / 2) = o[1];
+    }
 }
 
 template <int MODE>
@@ -88,26 +122,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap map_x, const Params p) {
     constexpr int kFeatures = MODE == GATEUP ? 128 : 256;   // of a unit
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages], bar_tfull[2], bar_tempty[2], bar_drain;
-    __shared__ int s_first[moe::kMaxExperts + 1], s_row0[moe::kMaxExperts], s_rows[moe::kMaxExperts];
+    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages], bar_tfull[4], bar_tempty[4], bar_drain;
+    __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2];
+    __shared__ float s_xs[2][kScaleBlocks][128], s_ws[2][kScaleBlocks][2];
+    // the experts' first tiles and rows, and the rows of their last tiles less one
+    __shared__ int s_first[moe::kMaxExperts + 1], s_row0[moe::kMaxExperts];
+    __shared__ uint8_t s_last[moe::kMaxExperts];
     __shared__ uint32_t s_amax[MODE == GATEUP ? 2 : 1][128];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort, s_never;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t out_base = base + kStages * kStageBytes;
     auto bar = [](uint64_t *b) { return ptx::smem_u32(b); };
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(bar(&bar_full[s]), 1);
-            ptx::mbar_init(bar(&bar_empty[s]), 1);
+            ptx::mbar_init(bar(&bar_empty[s]), 2);   // both halves
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < 4; ++a) {   // accumulator 2 * (block % 2) + half
             ptx::mbar_init(bar(&bar_tfull[a]), 1);
-            ptx::mbar_init(bar(&bar_tempty[a]), 2 * kEpiWarps);
+            ptx::mbar_init(bar(&bar_tempty[a]), kEpiWarps);   // half of the warps, of both CTAs
         }
-        ptx::mbar_init(bar(&bar_drain), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(&bar_sfull[i]), 1);
+            ptx::mbar_init(bar(&bar_sempty[i]), kEpiWarps);
+        }
+        ptx::mbar_init(bar(&bar_drain), 2);
         s_abort = 0;
         s_never = 0;
         ptx::fence_mbar_init();
@@ -139,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e < p.experts) {
                 s_first[e] = before + incl - tiles;
                 s_row0[e] = r.x;
-                s_rows[e] = r.y - r.x;
+                s_last[e] = static_cast<uint8_t>((r.y - r.x + kRows - 1) % kRows);
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
@@ -177,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.f = local / nb;
         const int tt = band * kBand + local - t.f * nb;
         t.row0 = s_row0[lo] + tt * kRows;
-        t.valid = min(kRows, s_rows[lo] - tt * kRows);
+        t.valid = tt == nt - 1 ? s_last[lo] + 1 : kRows;
         return t;
     };
 
@@ -192,7 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = u0; u < units && ok; u += ustep) {
                 const Unit t = unit_of(u);
                 const int xrow = t.row0 + static_cast<int>(rank) * 128;
-                const int wrow = t.expert * p.out + t.f * kFeatures + (MODE == GATEUP ? 0 : static_cast<int>(rank) * 128);
+                // 64 weight rows of each half: gate/up: the CTA's matrix's next; linear: the CTA's part of 128
+                const int wrow =
+                    t.expert * p.out + t.f * kFeatures + (MODE == GATEUP ? 0 : static_cast<int>(rank) * 64);
                 const CUtensorMap *mw = MODE == GATEUP && rank ? &map_w1 : &map_w0;
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, e4::kWaitNs);
@@ -205,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (leader) ptx::mbar_arrive_expect_tx(bar(&bar_full[s]), 2 * kStageBytes);
                         ptx::tma_load_2d_pair(at, &map_x, full, kb * 128, xrow);
                         ptx::tma_load_2d_pair(at + e4::kTileBytes, mw, full, kb * 128, wrow);
+                        ptx::tma_load_2d_pair(at + e4::kTileBytes + 64 * 128, mw, full, kb * 128,
+                                              wrow + (MODE == GATEUP ? 64 : 128));
                     }
                     __syncwarp();
                     ++produced;
@@ -218,29 +263,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 atomicOr(p.err, DEVERR_TIMEOUT);
                 *abort_flag = 1;
             }
-        } else if (warp == 1 && leader) {
-            // -------------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc = e4::idesc_e4m3(256, 256);
+        } else if (leader && warp <= 2) {
+            // -------------------------------------------------------- MMA issuers
+            // One warp for each half of a block.  What a block needs besides its accumulator is
+            // looked at before that, so that the instructions follow its release at once.
+            constexpr uint32_t idesc = e4::idesc_e4m3(256, 128);
+            const int half = warp - 1;
+            const uint64_t ad0 = ptx::sdesc_k_sw128(base),
+                           bd0 = ptx::sdesc_k_sw128(base + e4::kTileBytes + half * 64 * 128);
             bool ok = true;
             int s = 0, a = 0;
             uint32_t ph = 0, pa = 0;
             for (int u = u0; u < units && ok; u += ustep) {
                 for (int kb = 0; kb < p.nkb; ++kb) {
-                    bool got = ptx::mbar_wait(bar(&bar_tempty[a]), pa ^ 1u, abort_flag, e4::kWaitNs);
-                    got = got && ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, e4::kWaitNs);
+                    const int acc = 2 * a + half;
+                    const uint64_t ad = ad0 + s * (kStageBytes >> 4), bd = bd0 + s * (kStageBytes >> 4);
+                    bool got = ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, e4::kWaitNs);
+                    got = got && ptx::mbar_wait(bar(&bar_tempty[acc]), pa ^ 1u, abort_flag, e4::kWaitNs);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
-                        const uint32_t at = base + s * kStageBytes;
-                        const uint64_t ad = ptx::sdesc_k_sw128(at), bd = ptx::sdesc_k_sw128(at + e4::kTileBytes);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 bytes of k further: 2 in the address field
-                            e4::mma_e4m3_pair(tmem + a * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                            e4::mma_e4m3_pair(tmem + acc * 128, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                        ptx::tc_commit_pair(bar(&bar_tfull[acc]), 0x3);
                         ptx::tc_commit_pair(bar(&bar_empty[s]), 0x3);
-                        ptx::tc_commit_pair(bar(&bar_tfull[a]), 0x3);
                     }
                     __syncwarp();
                     if (++s == kStages) {
@@ -257,115 +307,144 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (ptx::elect_one()) ptx::tc_commit_pair(bar(&bar_drain), 0x1);   // every MMA ends before TMEM is freed
             ptx::mbar_wait(bar(&bar_drain), 0, never, e4::kWaitNs);
+        } else if (warp == 3) {
+            // -------------------------------------------------------- scales
+            // of the CTA's rows (four a lane) and of the unit's two weight blocks
+            bool ok = true;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int u = u0; u < units && ok; u += ustep) {
+                const Unit t = unit_of(u);
+                const float *xs = p.xs + static_cast<int64_t>(t.row0) * p.nkb;
+                const int first = static_cast<int>(rank) * 128 + lane, last = t.valid - 1;
+                int at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) at[i] = min(first + 32 * i, last) * p.nkb;
+                // lane 0: gate or the first half's block, lane 1: up or the second's
+                const int nb = MODE == GATEUP ? t.f : min(2 * t.f + (lane & 1), p.nf - 1);
+                const float *ws = (MODE == GATEUP && (lane & 1) ? p.ws[1] : p.ws[0]) +
+                                  (static_cast<int64_t>(t.expert) * p.nf + nb) * p.nkb;
+                for (int k0 = 0; k0 < p.nkb; k0 += kScaleBlocks) {
+                    const bool got = ptx::mbar_wait(bar(&bar_sempty[s]), ph ^ 1u, abort_flag, e4::kWaitNs);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j0 = 0; j0 < kScaleBlocks; j0 += 2) {
+                        float v[2][4], w[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int kb = min(k0 + j0 + j, p.nkb - 1);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[j][i] = __ldg(xs + at[i] + kb);
+                            w[j] = __ldg(ws + kb);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s_xs[s][j0 + j][32 * i + lane] = v[j][i];
+                            if (lane < 2) s_ws[s][j0 + j][lane] = w[j];
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(&bar_sfull[s]));
+                    s ^= 1;
+                    if (s == 0) ph ^= 1u;
+                }
+            }
+            if (!ok && lane == 0) {
+                atomicOr(p.err, DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---------------------------------------------------------- sums
-        const int q = warp & 3, part = (warp - 4) >> 2;
-        const uint32_t own = out_base + static_cast<uint32_t>(warp - 4) * 4096u;   // this warp's place to turn rows
-        int a = 0;
-        uint32_t pa = 0;
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        int a = 0, sc = 0;
+        uint32_t pa = 0, psc = 0;
         for (int u = u0; u < units; u += ustep) {
-            const Unit t = unit_of(u);
-            const int local = static_cast<int>(rank) * 128 + 32 * q + lane;   // this lane's row of the unit
-            const int nb = MODE == GATEUP ? t.f : min(2 * t.f + part, p.nf - 1);
-            const float *xs = p.xs + static_cast<int64_t>(t.row0 + (local < t.valid ? local : 0)) * p.nkb;
-            const float *ws = (MODE == GATEUP && part ? p.ws[1] : p.ws[0]) +
-                              (static_cast<int64_t>(t.expert) * p.nf + nb) * p.nkb;
-            // scales two blocks ahead
-            float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
-            if (p.nkb > 1) {
-                x1 = __ldg(xs + 1);
-                w1 = __ldg(ws + 1);
-            }
-            uint64_t acc[64];
+            uint64_t acc[64];   // two columns each; gate/up: 64 of gate, then 64 of up
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            bool ok = true;
+            bool ok = true, done = false;   // done: this block's sums are known to be there
             for (int kb = 0; kb < p.nkb; ++kb) {
-                const uint32_t sb = __float_as_uint(x0 * w0);
-                const uint64_t s2 = pack2(sb, sb);
-                x0 = x1;
-                w0 = w1;
-                if (kb + 2 < p.nkb) {
-                    x1 = __ldg(xs + kb + 2);
-                    w1 = __ldg(ws + kb + 2);
-                }
-                const bool got = ptx::mbar_wait(bar(&bar_tfull[a]), pa, abort_flag, e4::kWaitNs);
+                const int j = kb & (kScaleBlocks - 1);
+                bool got = true;
+                if (j == 0) got = ptx::mbar_wait(bar(&bar_sfull[sc]), psc, abort_flag, e4::kWaitNs);
+                const float x = s_xs[sc][j][32 * q + lane];
+                const float w0 = s_ws[sc][j][MODE == GATEUP ? 0 : half];
+                const uint32_t s0 = __float_as_uint(x * w0),
+                               s1 = MODE == GATEUP ? __float_as_uint(x * s_ws[sc][j][1]) : s0;
+                const uint64_t two0 = pack2(s0, s0), two1 = pack2(s1, s1);
+                const int buf = 2 * a + half;
+                got = got && (done || ptx::mbar_wait(bar(&bar_tfull[buf]), pa, abort_flag, e4::kWaitNs));
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * 128;
-                uint32_t r[2][16];   // (32 at a time spill)
-                ptx::tmem_ld_32x32b_x16(taddr, r[0]);
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 128;
+                // 16 columns at a time (gate/up: 32, which linear's registers do not hold), loaded
+                // under the additions before
+                constexpr int kCols = MODE == GATEUP ? 32 : 16;
+                uint32_t r[2][kCols];
+                ptx::tmem_ld_cols<kCols>(taddr, r[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 128 / kCols; ++c) {
                     ptx::tmem_ld_wait();
-                    if (c < 7) {
-                        ptx::tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+                    if (c < 128 / kCols - 1) {
+                        ptx::tmem_ld_cols<kCols>(taddr + kCols * (c + 1), r[(c + 1) & 1]);
                     } else {
+                        done = ptx::mbar_test(bar(&bar_tfull[buf ^ 2]), a ? pa ^ 1u : pa);
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_read(lead(bar(&bar_tempty[a])));
+                        if (lane == 0) arrive_read(lead(bar(&bar_tempty[buf])));
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        fma2(acc[8 * c + i], pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2);
+                    for (int i = 0; i < kCols / 2; ++i)
+                        fma2(acc[kCols / 2 * c + i], pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]),
+                             c < 64 / kCols ? two0 : two1);
+                }
+                if (j == kScaleBlocks - 1 || kb == p.nkb - 1) {   // (the warp has met since it read the scales)
+                    if (lane == 0) ptx::mbar_arrive(bar(&bar_sempty[sc]));
+                    sc ^= 1;
+                    if (sc == 0) psc ^= 1u;
                 }
                 a ^= 1;
                 if (a == 0) pa ^= 1u;
             }
+            const Unit t = unit_of(u);
+            const int local = static_cast<int>(rank) * 128 + 32 * q + lane;   // this lane's row of the unit
+            const int64_t row = t.row0 + local;
             if constexpr (MODE == LINEAR) {
                 if (!ok) {
                     if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
                     *abort_flag = 1;
                     break;
                 }
-                // 32 columns at a time through shared memory, 16 bytes of a row at (their place ^ row) % 8
+                const int col0 = t.f * 256 + half * 128;
+                auto store = [&](auto *y) {
+                    using T = typename std::remove_reference<decltype(*y)>::type;
+                    constexpr int N = 32 / sizeof(T);   // columns of a full sector
+                    T *to = y + row * p.out + col0;
+                    const T *from = static_cast<const T *>(p.res) + row * p.out + col0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 128; c += N) {
+                        float v[N];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float v[4];
-                        unpack2(acc[16 * c + 2 * j], v[0], v[1]);
-                        unpack2(acc[16 * c + 2 * j + 1], v[2], v[3]);
-                        sts128(own + lane * 128 + ((j ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+                        for (int i = 0; i < N; i += 2) unpack2(acc[(c + i) / 2], v[i], v[i + 1]);
+                        store_sector<T>(to + c, p.res ? from + c : nullptr, v, p.out - col0 - c);
                     }
-                    __syncwarp();
-                    const int col = t.f * 256 + part * 128 + c * 32 + (lane & 7) * 4;
-                    auto store = [&](auto *y) {
-                        using T = typename std::remove_reference<decltype(*y)>::type;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int row = 4 * i + (lane >> 3), at_row = static_cast<int>(rank) * 128 + 32 * q + row;
-                            const float4 f = lds128(own + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                            if (at_row >= t.valid || col >= p.out) continue;   // (out is a multiple of 8)
-                            const int64_t at = static_cast<int64_t>(t.row0 + at_row) * p.out + col;
-                            float v[4] = {f.x, f.y, f.z, f.w};
-                            struct alignas(4 * sizeof(T)) Four {
-                                T e[4];
-                            } o;
-                            if (p.res) {
-                                const Four r4 = *reinterpret_cast<const Four *>(static_cast<const T *>(p.res) + at);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) v[e] += to_f32(r4.e[e]);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o.e[e] = from_f32<T>(v[e]);
-                            *reinterpret_cast<Four *>(y + at) = o;
-                        }
-                    };
+                };
+                if (local < t.valid) {
                     if (p.dt == DT_BF16) store(static_cast<__nv_bfloat16 *>(p.y));
                     else if (p.dt == DT_F16) store(static_cast<__half *>(p.y));
                     else store(static_cast<float *>(p.y));
-                    __syncwarp();
                 }
             } else {
-                // The two warps of a lane's row meet (named barrier 1 + q): the gate's
-                // finishes features 0-63 of the block, the up's 64-127.
-                auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory"); };
+                // The two warps of a lane's row, 64 features each, meet (named barrier 1 + q).
                 int both;
                 asm volatile(
                     "{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\tbar.red.and.pred b, %2, 64, a;\n\t"
@@ -378,70 +457,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *abort_flag = 1;
                     break;
                 }
-                const uint32_t other = out_base + static_cast<uint32_t>((warp - 4) ^ 4) * 4096u;
+                const int f0 = t.f * 128 + half * 64;
                 float h[64];
                 uint32_t m = 0u;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {   // 32 features
+                for (int i = 0; i < 32; ++i) {
+                    float g[2], v[2];
+                    unpack2(acc[i], g[0], g[1]);
+                    unpack2(acc[32 + i], v[0], v[1]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float v[4];
-                        unpack2(part ? acc[16 * c + 2 * j] : acc[32 + 16 * c + 2 * j], v[0], v[1]);
-                        unpack2(part ? acc[16 * c + 2 * j + 1] : acc[32 + 16 * c + 2 * j + 1], v[2], v[3]);
-                        sts128(own + j * 512 + lane * 16, v[0], v[1], v[2], v[3]);
+                    for (int e = 0; e < 2; ++e) {
+                        h[2 * i + e] = e4::swiglu(g[e], v[e]);
+                        if (f0 + 2 * i + e >= p.out) h[2 * i + e] = 0.f;   // (the next expert's rows)
+                        m = max(m, abs_bits(h[2 * i + e]));
                     }
-                    meet();
+                }
+                s_amax[half][32 * q + lane] = m;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+                m = max(m, s_amax[half ^ 1][32 * q + lane]);   // (read before the next unit's vote, written after it)
+                const float amax = floor_amax(__uint_as_float(m)), k = kE4m3Max / amax;
+                if (local < t.valid) {
+                    if (half == 0) p.ys[row * p.nf + t.f] = amax / kE4m3Max;
+                    uint8_t *to = static_cast<uint8_t *>(p.y) + row * p.out + f0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 f = lds128(other + j * 512 + lane * 16);
-                        const float theirs[4] = {f.x, f.y, f.z, f.w};
-                        float mine[4];
-                        unpack2(part ? acc[32 + 16 * c + 2 * j] : acc[16 * c + 2 * j], mine[0], mine[1]);
-                        unpack2(part ? acc[32 + 16 * c + 2 * j + 1] : acc[16 * c + 2 * j + 1], mine[2], mine[3]);
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = 32 * c + 4 * j + e;
-                            h[i] = e4::swiglu(part ? theirs[e] : mine[e], part ? mine[e] : theirs[e]);
-                            if (t.f * 128 + 64 * part + i >= p.out) h[i] = 0.f;   // (the next expert's rows)
-                            m = max(m, abs_bits(h[i]));
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = e4m3x4(h[c + 4 * i] * k, h[c + 4 * i + 1] * k, h[c + 4 * i + 2] * k,
+                                          h[c + 4 * i + 3] * k);
+                        if ((reinterpret_cast<uintptr_t>(to) & 31) == 0 && f0 + c + 32 <= p.out) {
+                            st_sector(to + c, w);
+                        } else {   // rows of whole 8 bytes
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (f0 + c + 8 * i < p.out)
+                                    *reinterpret_cast<uint2 *>(to + c + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
                         }
                     }
-                    if (c == 1) s_amax[part][32 * q + lane] = m;
-                    meet();
                 }
-                m = max(m, s_amax[part ^ 1][32 * q + lane]);
-                const float amax = floor_amax(__uint_as_float(m)), k = kE4m3Max / amax;
-                if (part == 0 && local < t.valid) p.ys[static_cast<int64_t>(t.row0 + local) * p.nf + t.f] = amax / kE4m3Max;
-                // codes: 128 bytes a row, both warps' in the gate's place, turned as in linear
-                const uint32_t codes = out_base + static_cast<uint32_t>(q) * 4096u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 16 * j + 4 * e;
-                        w[e] = e4m3x4(h[i] * k, h[i + 1] * k, h[i + 2] * k, h[i + 3] * k);
-                    }
-                    sts128(codes + lane * 128 + (((4 * part + j) ^ (lane & 7)) << 4), __uint_as_float(w[0]),
-                           __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
-                }
-                meet();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * part + 4 * i + (lane >> 3),
-                              at_row = static_cast<int>(rank) * 128 + 32 * q + row;
-                    const float4 f = lds128(codes + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                    const int col = t.f * 128 + (lane & 7) * 16;
-                    if (at_row >= t.valid || col >= p.out) continue;
-                    uint8_t *to = static_cast<uint8_t *>(p.y) + static_cast<int64_t>(t.row0 + at_row) * p.out + col;
-                    if ((p.out & 15) == 0) {
-                        *reinterpret_cast<float4 *>(to) = f;
-                    } else {   // rows of whole 8 bytes
-                        *reinterpret_cast<float2 *>(to) = make_float2(f.x, f.y);
-                        if (col + 8 < p.out) *reinterpret_cast<float2 *>(to + 8) = make_float2(f.z, f.w);
-                    }
-                }
-                meet();
             }
         }
     }
@@ -451,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // loads still in flight (only after an abandoned wait) land before shared memory is released
         for (uint32_t s = 0; s < kStages; ++s)
             if (produced > s)
-                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + kStages - 1) / kStages - 1) & 1u, never, e4::kWaitNs);
+                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + kStages - 1) / kStages - 1) & 1u, never,
+                               e4::kWaitNs);
     }
     __syncthreads();
     ptx::cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
@@ -462,8 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-bool map_codes(CUtensorMap *m, const void *ptr, int64_t in, int64_t rows) {
-    return encode_tma_2d(m, ptr, CU_TENSOR_MAP_DATA_TYPE_UINT8, in, rows, in, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+bool map_codes(CUtensorMap *m, const void *ptr, int64_t in, int64_t rows, uint32_t box_rows) {
+    return encode_tma_2d(m, ptr, CU_TENSOR_MAP_DATA_TYPE_UINT8, in, rows, in, 128, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int MODE>
@@ -502,7 +558,7 @@ cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64
     }
     CUtensorMap m0, m1, mx;
     const int64_t wrows = static_cast<int64_t>(p.experts) * p.out;
-    if (!map_codes(&m0, w0, in, wrows) || !map_codes(&m1, w1, in, wrows) || !map_codes(&mx, x, in, p.rows))
+    if (!map_codes(&m0, w0, in, wrows, 64) || !map_codes(&m1, w1, in, wrows, 64) || !map_codes(&mx, x, in, p.rows, 128))
         return cudaErrorInvalidValue;
     const int64_t most = moe::max_tiles(p.rows, p.experts, kRows) * ((p.out + kFeatures - 1) / kFeatures);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(slots, most)));
