@@ -80,6 +80,7 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
 // x codes [rows x in], w codes [experts x out x in]; p but nf, nkb, err filled in
 cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
                                 e4::Params p, cudaStream_t s);
+// wide: tiles of 128 rows (linear only), else 32
 cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8_t *x, const uint8_t *w0,
                                const uint8_t *w1, int64_t in, const e4::Params &p, cudaStream_t s);
 cudaError_t launch_e4m3_pair(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,

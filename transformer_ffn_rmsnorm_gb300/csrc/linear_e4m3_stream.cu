@@ -11,12 +11,13 @@
 // nor a second launch.
 //
 // Two widths: tiles of 32 rows leave room for two CTAs on an SM, whose starts
-// and ends overlap; tiles of 128 rows take one.
+// and ends overlap; tiles of 128 rows (linear only: with two matrices the pairs are
+// faster from there on) take one.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-11 read each block's sums
-// and add them up in registers (lane = weight row, column = row of x; gate/up:
-// four warps a matrix, linear: every second 16 columns).  The columns' scales,
-// times the weight's, go through shared memory.  Every wait is bounded (1 s).
+// Roles: warp 0 loads, warp 1 issues the MMAs, the warps from 4 on read each block's
+// sums and add them up in registers (lane = weight row, column = row of x; gate/up:
+// four warps a matrix, linear: each four every second or fourth 16 columns).  The
+// columns' scales, times the weight's, go through shared memory.  Every wait is bounded (1 s).
 // Tensor memory is given back before a CTA waits for its cluster.
 #include <cudaTypedefs.h>
 
@@ -33,16 +34,16 @@ using e4::GATEUP;
 using e4::LINEAR;
 using e4::Params;
 
-constexpr int kThreads = 32 * 12, kEpiWarps = 8;
-
 template <int MODE, int TILE> struct Config {
     static constexpr int kMats = MODE == GATEUP ? 2 : 1;
+    static constexpr int kParts = MODE == LINEAR && TILE == 128 ? 4 : 2;    // of four warps each
+    static constexpr int kEpiWarps = 4 * kParts, kThreads = 32 * (4 + kEpiWarps);
     static constexpr uint32_t kStageBytes = kMats * e4::kTileBytes + TILE * 128;
     static constexpr int kCtas = TILE == 32 ? 2 : 1;   // on an SM
     static constexpr int kStages = static_cast<int>((kCtas == 2 ? 108 * 1024 : 200 * 1024) / kStageBytes);
-    static constexpr int kBufs = (TILE == 128 && MODE == GATEUP) ? 2 : 4;   // accumulators in tensor memory
+    static constexpr int kBufs = 4;                                         // accumulators in tensor memory
     static constexpr uint32_t kTmemCols = kMats * TILE * kBufs;
-    static constexpr int kCols = MODE == GATEUP ? TILE : TILE / 2;          // columns of a warp
+    static constexpr int kCols = MODE == GATEUP ? TILE : TILE / kParts;     // columns of a warp
     static constexpr size_t kSmem = kStages * kStageBytes + 1024;
     static constexpr uint32_t kPartBytes = kMats * TILE * 128 * 4;          // the parts a CTA receives
     static_assert(kPartBytes <= kStages * kStageBytes, "the parts take the stages' place");
@@ -89,24 +90,23 @@ template <int TILE> __device__ __forceinline__ UnitInfo find_unit(const Params &
     return u;
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ float ld_shared(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 
 template <int MODE, int TILE>
-__global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
+__global__ void __launch_bounds__((Config<MODE, TILE>::kThreads), (Config<MODE, TILE>::kCtas))
     e4m3_stream_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                        const __grid_constant__ moe::RowMaps maps_x, const Params p, const int splits) {
     using C = Config<MODE, TILE>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
     __shared__ __align__(8) uint64_t bar_tfull[C::kBufs], bar_tempty[C::kBufs], bar_drain;
-    __shared__ __align__(16) float s_scale[kEpiWarps][2][C::kCols];
+    __shared__ __align__(16) float s_scale[C::kEpiWarps][2][C::kCols];
     __shared__ uint32_t s_amax[TILE], s_all[8][TILE];
     __shared__ UnitInfo s_unit;
     __shared__ uint32_t s_tmem_base;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
         }
         for (int a = 0; a < C::kBufs; ++a) {
             ptx::mbar_init(bar(&bar_tfull[a]), 1);
-            ptx::mbar_init(bar(&bar_tempty[a]), kEpiWarps);
+            ptx::mbar_init(bar(&bar_tempty[a]), C::kEpiWarps);
         }
         ptx::mbar_init(bar(&bar_drain), 1);
         s_abort = 0;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
         for (int i = 0; i < 4; ++i) ptx::tma_prefetch_map(&maps_x.m[i]);
     }
     if (MODE == GATEUP)
-        for (int i = threadIdx.x; i < TILE; i += kThreads) s_amax[i] = 0u;
+        for (int i = threadIdx.x; i < TILE; i += C::kThreads) s_amax[i] = 0u;
     ptx::griddep_wait();   // x, its scales, offsets (and the weights, where they were just quantised)
     if (warp == 0) {
         const UnitInfo u = find_unit<TILE>(p, static_cast<int>(blockIdx.x) / splits, lane);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
 #pragma unroll
     for (int i = 0; i < C::kCols; ++i) acc[i] = 0.f;
     const int q = warp & 3, part = (warp - 4) >> 2;   // of the epilogue warps
-    auto column = [&](int j) { return MODE == GATEUP ? j : 32 * (j >> 4) + 16 * part + (j & 15); };
+    auto column = [&](int j) { return MODE == GATEUP ? j : 16 * C::kParts * (j >> 4) + 16 * part + (j & 15); };
 
     if (warp == 0) {
         // ------------------------------------------------------ producer
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
         int s = 0, a = 0;
         uint32_t ph = 0, pa = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
-            bool got = ptx::mbar_wait(bar(&bar_tempty[a]), pa ^ 1u, abort_flag, e4::kWaitNs);
-            got = got && ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, e4::kWaitNs);
+            bool got = ptx::mbar_wait(bar(&bar_full[s]), ph, abort_flag, e4::kWaitNs);
+            got = got && ptx::mbar_wait(bar(&bar_tempty[a]), pa ^ 1u, abort_flag, e4::kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
     } else if (warp >= 4) {
         // ---------------------------------------------------------- sums
         constexpr int kPer = (C::kCols + 31) / 32;   // scales of a lane
-        const float *ws = (MODE == GATEUP && part ? p.ws[1] : p.ws[0]) + (static_cast<int64_t>(t.expert) * p.nf + t.f) * p.nkb;
+        const float *ws = (MODE == GATEUP && part ? p.ws[1] : p.ws[0]) +
+                          (static_cast<int64_t>(t.expert) * p.nf + t.f) * p.nkb;
         const float *xs[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -309,70 +310,88 @@ __global__ void __launch_bounds__(kThreads, (Config<MODE, TILE>::kCtas))
 
     // ------------------------------------------ the parts to their features' CTA
     const int rows = 128 / splits;   // features that a CTA finishes
-    // part [source][matrix][column][feature]
-    auto part_at = [&](int src, int mat, int col, int r) {
-        return base + 4u * static_cast<uint32_t>(((src * C::kMats + mat) * TILE + col) * rows + r);
+    // part [source][matrix][column / 4][feature], four columns together
+    auto part_at = [&](int src, int mat, int col4, int r) {
+        return 16u * static_cast<uint32_t>(((src * C::kMats + mat) * (TILE / 4) + col4) * rows + r);
     };
     if (warp >= 4) {
         const int row = 32 * q + lane, dst = row / rows, r = row - dst * rows;
-        const uint32_t to = ptx::mapa_shared(part_at(rank, MODE == GATEUP ? part : 0, 0, r), dst);
+        const uint32_t to = ptx::mapa_shared(base + part_at(rank, MODE == GATEUP ? part : 0, 0, r), dst);
 #pragma unroll
-        for (int j = 0; j < C::kCols; ++j)
-            if (column(j) < t.valid) st_cluster(to + 4u * static_cast<uint32_t>(column(j) * rows), acc[j]);
+        for (int j = 0; j < C::kCols; j += 4)
+            if (column(j) < t.valid)
+                st_cluster4(to + part_at(0, 0, column(j) >> 2, 0), acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     }
     ptx::cluster_sync();
 
+    // four columns of a feature a thread
+    float4 *parts = reinterpret_cast<float4 *>(smem_raw + (base - ptx::smem_u32(smem_raw)));
     const int f0 = t.f * 128 + rank * rows;
-    const int items = t.valid * rows;
-    for (int i0 = 32 * warp; i0 < items; i0 += kThreads) {   // whole warps (rows is 16 or more, items a multiple of it)
-        const int i = i0 + lane;
-        const int r = i & (rows - 1), c = i / rows;
+    const int items = (t.valid + 3) / 4 * rows;
+    for (int i0 = 32 * warp; i0 < items; i0 += C::kThreads) {   // whole warps
+        const int i = i0 + lane, r = i & (rows - 1), c4 = i / rows;
         const bool in = i < items && f0 + r < p.out;
-        float v[C::kMats];
+        float v[C::kMats][4];
 #pragma unroll
         for (int m = 0; m < C::kMats; ++m) {
-            v[m] = 0.f;
+            v[m][0] = v[m][1] = v[m][2] = v[m][3] = 0.f;
             if (i < items)
-                for (int src = 0; src < splits; ++src) v[m] += ld_shared(part_at(src, m, c, r));
+                for (int src = 0; src < splits; ++src) {
+                    const float4 f = parts[part_at(src, m, c4, r) >> 4];
+                    v[m][0] += f.x;
+                    v[m][1] += f.y;
+                    v[m][2] += f.z;
+                    v[m][3] += f.w;
+                }
         }
         if constexpr (MODE == LINEAR) {
             if (!in) continue;
-            const int64_t at = static_cast<int64_t>(t.row0 + c) * p.out + f0 + r;
             auto store = [&](auto *y) {
                 using T = typename std::remove_reference<decltype(*y)>::type;
-                if (p.res) v[0] += to_f32(static_cast<const T *>(p.res)[at]);
-                y[at] = from_f32<T>(v[0]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (4 * c4 + e >= t.valid) break;
+                    const int64_t at = static_cast<int64_t>(t.row0 + 4 * c4 + e) * p.out + f0 + r;
+                    if (p.res) v[0][e] += to_f32(static_cast<const T *>(p.res)[at]);
+                    y[at] = from_f32<T>(v[0][e]);
+                }
             };
             if (p.dt == DT_BF16) store(static_cast<__nv_bfloat16 *>(p.y));
             else if (p.dt == DT_F16) store(static_cast<__half *>(p.y));
             else store(static_cast<float *>(p.y));
         } else {
-            const float h = in ? e4::swiglu(v[0], v[1]) : 0.f;
-            uint32_t m = abs_bits(h);
-            const int seg = min(rows, 32);
-            for (int o = seg >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (i < items && (lane & (seg - 1)) == 0) atomicMax(&s_amax[c], m);
-            if (i < items) st_cluster(ptx::mapa_shared(part_at(0, 0, c, r), rank), h);   // in its own part's place
+            float h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h[e] = in ? e4::swiglu(v[0][e], v[C::kMats - 1][e]) : 0.f;
+                uint32_t m = abs_bits(h[e]);
+                const int seg = min(rows, 32);
+                for (int o = seg >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (i < items && (lane & (seg - 1)) == 0) atomicMax(&s_amax[4 * c4 + e], m);
+            }
+            if (i < items) parts[part_at(0, 0, c4, r) >> 4] = make_float4(h[0], h[1], h[2], h[3]);   // (only it read them)
         }
     }
     if constexpr (MODE == GATEUP) {
         __syncthreads();
-        for (int i = threadIdx.x; i < t.valid * splits; i += kThreads) {
+        for (int i = threadIdx.x; i < t.valid * splits; i += C::kThreads) {
             const int c = i / splits, dst = i - c * splits;
-            st_cluster(ptx::mapa_shared(ptx::smem_u32(&s_all[rank][c]), dst), __uint_as_float(s_amax[c]));
+            st_cluster(ptx::mapa_shared(ptx::smem_u32(&s_all[rank][c]), dst), s_amax[c]);
         }
         ptx::cluster_sync();
-        for (int i = 4 * threadIdx.x; i < items; i += 4 * kThreads) {
+        // four features of a row a thread
+        const float *h = reinterpret_cast<const float *>(parts);
+        for (int i = 4 * threadIdx.x; i < t.valid * rows; i += 4 * C::kThreads) {
             const int r = i & (rows - 1), c = i / rows;
             uint32_t m = 0u;
             for (int src = 0; src < splits; ++src) m = max(m, s_all[src][c]);
             const float amax = floor_amax(__uint_as_float(m)), k = kE4m3Max / amax;
             const int64_t row = t.row0 + c;
             if (rank == 0 && r == 0) p.ys[row * p.nf + t.f] = amax / kE4m3Max;
+            const float *from = h + (part_at(0, 0, c >> 2, r) >> 2) + (c & 3);
             if (f0 + r < p.out)   // (out is a multiple of 8)
                 *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + row * p.out + f0 + r) =
-                    e4m3x4(ld_shared(part_at(0, 0, c, r)) * k, ld_shared(part_at(0, 0, c, r + 1)) * k,
-                           ld_shared(part_at(0, 0, c, r + 2)) * k, ld_shared(part_at(0, 0, c, r + 3)) * k);
+                    e4m3x4(from[0] * k, from[4] * k, from[8] * k, from[12] * k);
         }
     }
 }
@@ -412,7 +431,7 @@ cudaError_t launch(int splits, const uint8_t *x, const uint8_t *w0, const uint8_
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -426,22 +445,45 @@ cudaError_t launch(int splits, const uint8_t *x, const uint8_t *w0, const uint8_
 
 cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8_t *x, const uint8_t *w0,
                                const uint8_t *w1, int64_t in, const Params &p, cudaStream_t s) {
-    if (mode == GATEUP)
-        return wide ? launch<GATEUP, 128>(splits, x, w0, w1, in, p, s) : launch<GATEUP, 32>(splits, x, w0, w1, in, p, s);
+    if (mode == GATEUP) return launch<GATEUP, 32>(splits, x, w0, w1, in, p, s);
     return wide ? launch<LINEAR, 128>(splits, x, w0, w1, in, p, s) : launch<LINEAR, 32>(splits, x, w0, w1, in, p, s);
 }
 
+// Which kernel, from the sizes alone (of the experts' rows only the mean is known
+// here).  Up to 32 rows an expert the stream of weights: dense 4096 -> 14336
+// gate/up, 32 rows 27.9 us, pairs 34.0, 48 rows (two tiles) 40 and 34; over 64
+// experts of 2048 x 1408 with 24 rows 79 and 90, with 48 rows 111 and 92.  Beyond
+// that gate/up runs on the pairs, linear there or in tiles of 128 rows, which cut
+// the reduction where few units leave the pairs idle: by the estimates below, us.
+// Linear 14336 -> 4096, pairs / tiles of 128: 48 rows 50.6 / 15.2, 128 rows 51.7 /
+// 21.5, 256 rows 51.7 / 35.9, 512 rows 52.3 / 65.2; 4096 -> 14336, 64 rows 19.1 /
+// 18.3, 128 rows 20.5 / 27.3; 64 experts 1408 -> 2048, 48 rows 53.6 / 77.7.
 cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
                                 Params p, cudaStream_t s) {
     p.nf = (p.out + 127) / 128;
     p.nkb = static_cast<int>((in + 127) / 128);
     p.err = device_status_word();
     if (!p.err) return cudaErrorUnknown;
-    if (p.rows > 128 * static_cast<int64_t>(p.experts)) return launch_e4m3_pair(mode, x, w0, w1, in, p, s);
-    const bool wide = p.rows > 32 * static_cast<int64_t>(p.experts);
-    int splits = 8;
-    while (splits > 1 && 2 * splits > p.nkb) splits >>= 1;
-    return launch_e4m3_stream(mode, wide, splits, x, w0, w1, in, p, s);
+    const int64_t sms = sm_count(), used = std::min<int64_t>(p.rows, p.experts), mean = (p.rows + used - 1) / used;
+    auto units = [&](int tile) { return used * ((mean + tile - 1) / tile) * p.nf; };
+    // The most parts of the reduction whose CTAs all run at once, two blocks each: 4096 ->
+    // 14336 gate/up, 1 row, 112 units in 1, 2, 4, 8 parts 25.1, 23.8, 28.5, 40.8 us;
+    // linear 14336 -> 4096, 32 units 37.2, 21.0, 13.0, 11.9.
+    auto parts = [&](int tile, int64_t slots) {
+        int n = 8;
+        while (n > 1 && (n * units(tile) > slots || 2 * n > p.nkb)) n >>= 1;
+        return n;
+    };
+    if (mean <= 32) return launch_e4m3_stream(mode, false, parts(32, 2 * sms), x, w0, w1, in, p, s);
+    if (mode == LINEAR) {
+        const int n = parts(128, sms);
+        const double block = 0.13 + 0.0027 * static_cast<double>(std::min<int64_t>(mean, 128));
+        const double wide = 2. + static_cast<double>((units(128) * n + sms - 1) / sms) * (p.nkb / n * block + 6.);
+        const int64_t pairs = used * ((mean + 255) / 256) * ((p.out + 255) / 256);
+        const double pair = 4. + static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * p.nkb * 0.45;
+        if (wide < pair) return launch_e4m3_stream(mode, true, n, x, w0, w1, in, p, s);
+    }
+    return launch_e4m3_pair(mode, x, w0, w1, in, p, s);
 }
 
 }  // namespace ffn
