@@ -558,8 +558,9 @@ cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64
     }
     CUtensorMap m0, m1, mx;
     const int64_t wrows = static_cast<int64_t>(p.experts) * p.out;
-    if (!map_codes(&m0, w0, in, wrows, 64) || !map_codes(&m1, w1, in, wrows, 64) || !map_codes(&mx, x, in, p.rows, 128))
-        return cudaErrorInvalidValue;
+    if (!map_codes(&m0, w0, in, wrows, 64) || !map_codes(&mx, x, in, p.rows, 128)) return cudaErrorInvalidValue;
+    m1 = m0;
+    if (MODE == GATEUP && !map_codes(&m1, w1, in, wrows, 64)) return cudaErrorInvalidValue;
     const int64_t most = moe::max_tiles(p.rows, p.experts, kRows) * ((p.out + kFeatures - 1) / kFeatures);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(slots, most)));
     cfg.stream = s;

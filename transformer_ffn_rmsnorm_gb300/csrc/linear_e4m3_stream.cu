@@ -418,8 +418,14 @@ cudaError_t launch(int splits, const uint8_t *x, const uint8_t *w0, const uint8_
     CUtensorMap m0, m1;
     moe::RowMaps mx;
     const int64_t wrows = static_cast<int64_t>(p.experts) * p.out;
-    bool good = map_codes(&m0, w0, in, wrows, 128) && map_codes(&m1, w1, in, wrows, 128);
-    for (int i = 0; i < 4; ++i) good = good && map_codes(&mx.m[i], x, in, p.rows, 128u >> i);
+    // (a map takes the host about a microsecond: none that the kernel does not use)
+    bool good = map_codes(&m0, w0, in, wrows, 128);
+    if (MODE == GATEUP) good = good && map_codes(&m1, w1, in, wrows, 128);
+    else m1 = m0;
+    for (int i = 3; i >= 0; --i) {   // boxes of 16, 32, ... rows up to the tile
+        if ((128 >> i) <= TILE) good = good && map_codes(&mx.m[i], x, in, p.rows, 128u >> i);
+        else mx.m[i] = mx.m[i + 1];
+    }
     if (!good) return cudaErrorInvalidValue;
     const int64_t units = moe::max_tiles(p.rows, p.experts, TILE) * p.nf;
     cudaLaunchAttribute attr[2];

@@ -11,8 +11,8 @@
 // goes to k places; or the k rows are read together and added in fp32.
 //
 // The order is stable, whatever the number of CTAs: a pair's rank among its
-// expert's is counted, not dealt out by atomics.  Up to 256 pairs each CTA counts
-// the pairs before its token's k for itself, one launch in all.  More take three:
+// expert's is counted, not dealt out by atomics.  Up to 1024 pairs each CTA counts
+// the pairs before its token's k for itself, one launch in all (384 pairs 2.9 us, 7.1 in three).  More take three:
 // a CTA a chunk of pairs (ranks inside a warp by comparing lanes, warps and pieces
 // of 1024 pairs one after the other), a scan over the chunks' counts, the copy.
 #include <algorithm>
@@ -24,7 +24,7 @@
 namespace ffn {
 namespace {
 
-constexpr int kSmallPairs = 256;
+constexpr int kSmallPairs = 1024;
 constexpr int kCountThreads = 1024, kMaxChunks = 512;
 constexpr int kRowThreads = 128;
 
@@ -70,10 +70,10 @@ __device__ __forceinline__ void copy_row(const SortParams &p, int64_t t, const i
     }
 }
 
-// Few pairs: CTA (piece, t) counts the places of token t's pairs and copies a
-// piece of its row; the row of CTAs after the last token's writes pos and offsets.
+// Few pairs, a thread each: CTA (piece, t) counts the places of token t's pairs and copies
+// a piece of its row; the row of CTAs after the last token's writes offsets.
 __global__ void __launch_bounds__(kSmallPairs) moe_sort_small_kernel(const SortParams p) {
-    __shared__ __align__(16) int s_e[kSmallPairs];
+    __shared__ int s_count[moe::kMaxExperts];
     __shared__ int s_at[32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -90,31 +90,49 @@ __global__ void __launch_bounds__(kSmallPairs) moe_sort_small_kernel(const SortP
             if (i == 0) s_at[j] = mine < p.experts ? before : -1;
         }
         __syncthreads();
-        copy_row(p, t, s_at, blockIdx.x * kSmallPairs + i, gridDim.x * kSmallPairs, blockIdx.x == 0);
+        if (blockIdx.x == 0 && i < p.k) p.pos[t * p.k + i] = s_at[i];
+        copy_row(p, t, s_at, blockIdx.x * blockDim.x + i, gridDim.x * blockDim.x, blockIdx.x == 0);
         return;
     }
     if (blockIdx.x) return;
-    s_e[i] = e;
+    for (int f = i; f < p.experts; f += blockDim.x) s_count[f] = 0;
     __syncthreads();
-    const int4 *all = reinterpret_cast<const int4 *>(s_e);
-    auto count = [&](int expert, int pair) {   // pairs of experts before it, and of it before the pair
-        int n = 0;
-        for (int j = 0; j < kSmallPairs / 4; ++j) {
-            const int4 o = all[j];
-            const int v[4] = {o.x, o.y, o.z, o.w};
+    if (e < p.experts) atomicAdd(&s_count[e], 1);
+    __syncthreads();
+    if (i >= 32) return;
+    int before = 0;
+    for (int f0 = 0; f0 < p.experts; f0 += 32) {
+        const int f = f0 + i;
+        int incl = f < p.experts ? s_count[f] : 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) n += v[q] < expert || (v[q] == expert && 4 * j + q < pair);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (i >= o) incl += v;
         }
-        return n;
-    };
-    if (i < p.pairs) p.pos[i] = e < p.experts ? count(e, i) : -1;
-    for (int f = i; f <= p.experts; f += kSmallPairs) p.offsets[f] = count(f, 0);
+        if (f < p.experts) p.offsets[f + 1] = before + incl;
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (i == 0) p.offsets[0] = 0;
+}
+
+// The sum of an expert's counts in the warps before `before`.
+__device__ __forceinline__ int count_before(const uint8_t *counts, int before) {
+    const uint4 lo = reinterpret_cast<const uint4 *>(counts)[0], hi = reinterpret_cast<const uint4 *>(counts)[1];
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t n = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int left = before - 4 * i;   // bytes of the word that count
+        const uint32_t ones = left >= 4 ? 0x01010101u : left <= 0 ? 0u : 0x01010101u & ((1u << (8 * left)) - 1u);
+        n = __dp4a(w[i], ones, n);
+    }
+    return static_cast<int>(n);
 }
 
 // A chunk of pairs: counts by expert to hist, each pair's rank among the
 // chunk's of its expert to pos (-1: none).
 __global__ void __launch_bounds__(kCountThreads) moe_sort_count_kernel(const SortParams p) {
-    extern __shared__ uint8_t s_count[];   // [experts][32 warps], then the chunk's counts so far
+    extern __shared__ __align__(16) uint8_t s_count[];   // [experts][32 warps]
     __shared__ int s_run[moe::kMaxExperts];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -132,18 +150,12 @@ __global__ void __launch_bounds__(kCountThreads) moe_sort_count_kernel(const Sor
         if (e >= 0 && ahead == 0) s_count[e * 32 + warp] = static_cast<uint8_t>(__popc(same));
         __syncthreads();
         if (e >= 0) {
-            int rank = s_run[e] + ahead;
-            for (int w = 0; w < warp; ++w) rank += s_count[e * 32 + w];
-            p.pos[i] = rank;
+            p.pos[i] = s_run[e] + ahead + count_before(s_count + e * 32, warp);
         } else if (i < p.pairs) {
             p.pos[i] = -1;
         }
         __syncthreads();
-        for (int f = threadIdx.x; f < p.experts; f += kCountThreads) {
-            int n = 0;
-            for (int w = 0; w < 32; ++w) n += s_count[f * 32 + w];
-            s_run[f] += n;
-        }
+        for (int f = threadIdx.x; f < p.experts; f += kCountThreads) s_run[f] += count_before(s_count + f * 32, 32);
         __syncthreads();
     }
     for (int e = threadIdx.x; e < p.experts; e += kCountThreads)
@@ -390,10 +402,10 @@ cudaError_t launch_moe_sort(const void *x, const float *x_scales, const int32_t 
     p.nscales = static_cast<int>(nscales);
     cudaError_t e;
     if (p.pairs <= kSmallPairs) {
-        const dim3 grid(static_cast<unsigned>((p.nvec + kSmallPairs - 1) / kSmallPairs),
-                        static_cast<unsigned>(rows + 1));
+        const int threads = std::max(128, (p.pairs + 31) / 32 * 32);
+        const dim3 grid(static_cast<unsigned>((p.nvec + threads - 1) / threads), static_cast<unsigned>(rows + 1));
         LaunchScope scope(K_MOE_SORT, s);
-        e = launch_dependent(moe_sort_small_kernel, grid, dim3(kSmallPairs), 0, s, p);
+        e = launch_dependent(moe_sort_small_kernel, grid, dim3(static_cast<unsigned>(threads)), 0, s, p);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     {

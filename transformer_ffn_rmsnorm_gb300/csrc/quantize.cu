@@ -24,6 +24,26 @@ struct QuantParams {
     int d, group, ngroups;
 };
 
+// The largest magnitude of a vector (max_of), or of several (max of those), as bits
+// that order magnitudes: a 16-bit type's own, two at a time, widened only at the end.
+template <typename T> struct Magnitude {
+    __device__ static __forceinline__ uint32_t max_of(const uint4 &v) {
+        const uint32_t k = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+        return max(m >> 16, m & 0xffffu);
+    }
+    __device__ static __forceinline__ float value(uint32_t bits) {
+        const unsigned short b = static_cast<unsigned short>(bits);
+        return to_f32(*reinterpret_cast<const T *>(&b));
+    }
+};
+template <> struct Magnitude<float> {
+    __device__ static __forceinline__ uint32_t max_of(const uint4 &v) {
+        const uint32_t k = 0x7fffffffu;
+        return max(max(v.x & k, v.y & k), max(v.z & k, v.w & k));
+    }
+    __device__ static __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+};
+
 template <int EPV> __device__ __forceinline__ void store_codes(uint8_t *to, const float (&f)[EPV], float k) {
     if constexpr (EPV == 8)
         __stcs(reinterpret_cast<uint2 *>(to), make_uint2(e4m3x4(f[0] * k, f[1] * k, f[2] * k, f[3] * k),
@@ -61,15 +81,13 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantP
     }
 #pragma unroll
     for (int b = 0; b < kRowVecs; ++b) {
-        float f[EPV];
-        Vec16<T>::unpack(v[b], f);
-        uint32_t m = 0u;
-#pragma unroll
-        for (int j = 0; j < EPV; ++j) m = max(m, abs_bits(f[j]));
+        uint32_t m = Magnitude<T>::max_of(v[b]);
         for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float a = floor_amax(__uint_as_float(m));
+        const float a = floor_amax(Magnitude<T>::value(m));
         const int64_t i = i0 + b * kRowThreads;
         if (i < p.total && (lane & (lanes - 1)) == 0) p.scales[i / lanes] = a / kE4m3Max;
+        float f[EPV];
+        Vec16<T>::unpack(v[b], f);
         if (at[b] >= 0) store_codes<EPV>(p.q + at[b], f, kE4m3Max / a);
     }
 }
@@ -129,18 +147,13 @@ __global__ void __launch_bounds__(kBlockThreads) quantize_blocks_kernel(const Qu
     }
     uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float f[EPV];
-        Vec16<T>::unpack(v[i], f);
-#pragma unroll
-        for (int j = 0; j < EPV; ++j) m = max(m, abs_bits(f[j]));
-    }
+    for (int i = 0; i < N; ++i) m = max(m, Magnitude<T>::max_of(v[i]));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kBlockThreads / 32; ++w) m = max(m, s_max[w]);
-    const float a = floor_amax(__uint_as_float(m)), k = kE4m3Max / a;
+    const float a = floor_amax(Magnitude<T>::value(m)), k = kE4m3Max / a;
     if (threadIdx.x == 0)
         p.scales[mat * nbr * p.ngroups + (TRANSPOSE ? bc * nbr + br : in_mat)] = a / kE4m3Max;
 #pragma unroll
