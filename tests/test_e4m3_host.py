@@ -35,8 +35,8 @@ def test_quantize_refusals(lib):
         assert call(**{name: None}) == NULL
     assert call(dtype=_lib.FFN_E4M3) == DTYPE and call(dtype=9) == DTYPE
     assert call(flags=2) == FLAGS and call(flags=1) == FLAGS     # (only blocks are transposed)
-    for bad in ({"rows": -1}, {"batch": -1}, {"d": 0}, {"block_rows": 2}, {"block_rows": 64}, {"group": 0}, {"group": 16},
-                {"block_rows": 128, "group": 64}, {"block_rows": 128, "d": 72}, {"d": 1 << 30},
+    for bad in ({"rows": -1}, {"batch": -1}, {"d": 0}, {"block_rows": 2}, {"block_rows": 64}, {"group": 0},
+                {"group": 16}, {"block_rows": 128, "group": 64}, {"block_rows": 128, "d": 72}, {"d": 1 << 30},
                 {"block_rows": 128, "flags": 1, "rows": 8}, {"rows": 1 << 31}, {"rows": 1 << 25, "d": 1 << 13},
                 {"batch": 1 << 20, "rows": 1 << 20}):
         assert call(**bad) == SHAPE, bad
@@ -108,7 +108,8 @@ def test_sort_refusals(lib):
         assert call(**{name: off(p, 8)}) == ALIGN, name
     for name, p in (("sc", P[1]), ("idx", P[2]), ("xsc", P[4]), ("pos", P[5]), ("offs", P[6])):
         assert call(**{name: off(p, 2)}) == ALIGN, name
-    for bad in ({"xs": P[0]}, {"pos": P[2]}, {"offs": off(P[5], 16)}, {"xsc": P[1]}, {"ws": P[3]}, {"ws": off(P[2], 16)}):
+    for bad in ({"xs": P[0]}, {"pos": P[2]}, {"offs": off(P[5], 16)}, {"xsc": P[1]}, {"ws": P[3]},
+                {"ws": off(P[2], 16)}):
         assert call(**bad) == ALIAS, bad
 
 
