@@ -12,9 +12,9 @@
 // and reads its accumulators at 75 % of tensor memory's rate, the epilogue warps'
 // loads are the other 25 %, their additions 256 cycles of the FMA pipe (two an
 // instruction); but the way of a half -- instructions issued, sums done, seen,
-// read and added, their leave sent back across the pair, seen -- is about 1500
-// cycles, of which two halves' 512 are hidden: 890 cycles a block.  (4096 tokens,
-// 4096 -> 11008 gate/up: 284 us; without reading and adding 228, with one such
+// read and added, their leave sent back across the pair, seen -- is about 1300
+// cycles, of which two halves' 512 are hidden: 790 cycles a block.  (4096 tokens,
+// 4096 -> 11008 gate/up: 274 us; without reading and adding about 220, with one such
 // handshake in 16 blocks 195.  Two accumulators of N = 256 took 349; 16 warps of 64
 // columns, whose sums do not fit beside what else the registers hold, 441; one warp
 // issuing both halves' MMAs 387.)
@@ -24,9 +24,10 @@
 // which the operands fill.
 //
 // Roles: warp 0 loads, warps 1 and 2 issue the MMAs of a half each (the even CTA's),
-// warp 3 brings the scales of the CTA's rows to shared memory four blocks at a time,
-// warps 4-11 add the sums (lane = row of x; four warps for each half) and finish the
-// unit while the next one's first blocks run.  Every wait is bounded (1 s).
+// warp 3 brings the scales of the CTA's rows to shared memory four blocks at a time
+// (and what the unit is), warps 4-11 add the sums (lane = row of x; four warps for
+// each half) and finish the unit while the next one's first blocks run.  Every wait
+// is bounded (1 s).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -116,6 +117,12 @@ template <typename T> __device__ __forceinline__ void store_sector(T *to, const 
     }
 }
 
+// max(a, |b|), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     e4m3_pair_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
@@ -125,10 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages], bar_tfull[4], bar_tempty[4], bar_drain;
     __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2];
     __shared__ float s_xs[2][kScaleBlocks][128], s_ws[2][kScaleBlocks][2];
+    __shared__ int4 s_unit[2];   // f, row0, valid of the unit that the slot of scales begins
     // the experts' first tiles and rows, and the rows of their last tiles less one
     __shared__ int s_first[moe::kMaxExperts + 1], s_row0[moe::kMaxExperts];
     __shared__ uint8_t s_last[moe::kMaxExperts];
-    __shared__ uint32_t s_amax[MODE == GATEUP ? 2 : 1][128];
+    __shared__ float s_amax[MODE == GATEUP ? 2 : 1][128];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort, s_never;
 
@@ -347,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane < 2) s_ws[s][j0 + j][lane] = w[j];
                         }
                     }
+                    if (lane == 0 && k0 == 0) s_unit[s] = make_int4(t.f, t.row0, t.valid, 0);
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(&bar_sfull[s]));
                     s ^= 1;
@@ -362,30 +371,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---------------------------------------------------------- sums
         const int q = warp & 3, half = (warp - 4) >> 2;
-        int a = 0, sc = 0;
-        uint32_t pa = 0, psc = 0;
+        // addresses of the half's two accumulators and their barriers lie 256 columns and 16 bytes apart
+        const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+        const uint32_t tfull = bar(&bar_tfull[half]), tempty = lead(bar(&bar_tempty[half]));
+        const uint32_t sfull = bar(&bar_sfull[0]), sempty = bar(&bar_sempty[0]);
+        const float *my_xs = &s_xs[0][0][32 * q + lane], *my_ws = &s_ws[0][0][MODE == GATEUP ? 0 : half];
+        uint32_t a = 0, pa = 0;             // of the next block: accumulator, its parity
+        uint32_t ring = 0, pring = 0;       // its place in the ring of scales, the ring's parity
         for (int u = u0; u < units; u += ustep) {
             uint64_t acc[64];   // two columns each; gate/up: 64 of gate, then 64 of up
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
             bool ok = true, done = false;   // done: this block's sums are known to be there
-            for (int kb = 0; kb < p.nkb; ++kb) {
-                const int j = kb & (kScaleBlocks - 1);
+            int tf = 0, trow0 = 0, tvalid = 0;
+            for (int kb = p.nkb; kb > 0; --kb) {
                 bool got = true;
-                if (j == 0) got = ptx::mbar_wait(bar(&bar_sfull[sc]), psc, abort_flag, e4::kWaitNs);
-                const float x = s_xs[sc][j][32 * q + lane];
-                const float w0 = s_ws[sc][j][MODE == GATEUP ? 0 : half];
+                if ((ring & (kScaleBlocks - 1)) == 0)
+                    got = ptx::mbar_wait(sfull + 8 * (ring / kScaleBlocks), pring, abort_flag, e4::kWaitNs);
+                if (kb == p.nkb) {
+                    const int4 t = s_unit[ring / kScaleBlocks];
+                    tf = t.x;
+                    trow0 = t.y;
+                    tvalid = t.z;
+                }
+                const float x = my_xs[ring * 128], w0 = my_ws[ring * 2];
                 const uint32_t s0 = __float_as_uint(x * w0),
-                               s1 = MODE == GATEUP ? __float_as_uint(x * s_ws[sc][j][1]) : s0;
+                               s1 = MODE == GATEUP ? __float_as_uint(x * my_ws[ring * 2 + 1]) : s0;
                 const uint64_t two0 = pack2(s0, s0), two1 = pack2(s1, s1);
-                const int buf = 2 * a + half;
-                got = got && (done || ptx::mbar_wait(bar(&bar_tfull[buf]), pa, abort_flag, e4::kWaitNs));
+                got = got && (done || ptx::mbar_wait(tfull + 16 * a, pa, abort_flag, e4::kWaitNs));
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 128;
+                const uint32_t taddr = trow + 256 * a;
                 // 16 columns at a time (gate/up: 32, which linear's registers do not hold), loaded
                 // under the additions before
                 constexpr int kCols = MODE == GATEUP ? 32 : 16;
@@ -397,34 +416,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c < 128 / kCols - 1) {
                         ptx::tmem_ld_cols<kCols>(taddr + kCols * (c + 1), r[(c + 1) & 1]);
                     } else {
-                        done = ptx::mbar_test(bar(&bar_tfull[buf ^ 2]), a ? pa ^ 1u : pa);
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_read(lead(bar(&bar_tempty[buf])));
+                        if (lane == 0) arrive_read(tempty + 16 * a);
+                        pa ^= a;
+                        a ^= 1u;
+                        done = ptx::mbar_test(tfull + 16 * a, pa);
                     }
 #pragma unroll
                     for (int i = 0; i < kCols / 2; ++i)
                         fma2(acc[kCols / 2 * c + i], pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]),
                              c < 64 / kCols ? two0 : two1);
                 }
-                if (j == kScaleBlocks - 1 || kb == p.nkb - 1) {   // (the warp has met since it read the scales)
-                    if (lane == 0) ptx::mbar_arrive(bar(&bar_sempty[sc]));
-                    sc ^= 1;
-                    if (sc == 0) psc ^= 1u;
+                const uint32_t slot = ring / kScaleBlocks;
+                ++ring;
+                if (kb == 1) ring = (ring + kScaleBlocks - 1) & ~static_cast<uint32_t>(kScaleBlocks - 1);
+                if ((ring & (kScaleBlocks - 1)) == 0) {   // (the warp has met since it read the scales)
+                    if (lane == 0) ptx::mbar_arrive(sempty + 8 * slot);
+                    if (ring == 2 * kScaleBlocks) {
+                        ring = 0;
+                        pring ^= 1u;
+                    }
                 }
-                a ^= 1;
-                if (a == 0) pa ^= 1u;
             }
-            const Unit t = unit_of(u);
             const int local = static_cast<int>(rank) * 128 + 32 * q + lane;   // this lane's row of the unit
-            const int64_t row = t.row0 + local;
+            const int64_t row = trow0 + local;
             if constexpr (MODE == LINEAR) {
                 if (!ok) {
                     if (lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
                     *abort_flag = 1;
                     break;
                 }
-                const int col0 = t.f * 256 + half * 128;
+                const int col0 = tf * 256 + half * 128;
                 auto store = [&](auto *y) {
                     using T = typename std::remove_reference<decltype(*y)>::type;
                     constexpr int N = 32 / sizeof(T);   // columns of a full sector
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         store_sector<T>(to + c, p.res ? from + c : nullptr, v, p.out - col0 - c);
                     }
                 };
-                if (local < t.valid) {
+                if (local < tvalid) {
                     if (p.dt == DT_BF16) store(static_cast<__nv_bfloat16 *>(p.y));
                     else if (p.dt == DT_F16) store(static_cast<__half *>(p.y));
                     else store(static_cast<float *>(p.y));
@@ -457,27 +480,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *abort_flag = 1;
                     break;
                 }
-                const int f0 = t.f * 128 + half * 64;
-                float h[64];
-                uint32_t m = 0u;
+                const int f0 = tf * 128 + half * 64;
+                float h[64], m = 0.f;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float g[2], v[2];
                     unpack2(acc[i], g[0], g[1]);
                     unpack2(acc[32 + i], v[0], v[1]);
+                    h[2 * i] = e4::swiglu(g[0], v[0]);
+                    h[2 * i + 1] = e4::swiglu(g[1], v[1]);
+                    m = max_nan(max_nan(m, h[2 * i]), h[2 * i + 1]);
+                }
+                if (f0 + 64 > p.out) {   // features that are the next expert's rows, or none
+                    m = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        h[2 * i + e] = e4::swiglu(g[e], v[e]);
-                        if (f0 + 2 * i + e >= p.out) h[2 * i + e] = 0.f;   // (the next expert's rows)
-                        m = max(m, abs_bits(h[2 * i + e]));
+                    for (int i = 0; i < 64; ++i) {
+                        h[i] = f0 + i < p.out ? h[i] : 0.f;
+                        m = max_nan(m, h[i]);
                     }
                 }
                 s_amax[half][32 * q + lane] = m;
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-                m = max(m, s_amax[half ^ 1][32 * q + lane]);   // (read before the next unit's vote, written after it)
-                const float amax = floor_amax(__uint_as_float(m)), k = kE4m3Max / amax;
-                if (local < t.valid) {
-                    if (half == 0) p.ys[row * p.nf + t.f] = amax / kE4m3Max;
+                m = max_nan(m, s_amax[half ^ 1][32 * q + lane]);   // (read before the next unit's vote)
+                const float amax = floor_amax(m), k = kE4m3Max / amax;
+                if (local < tvalid) {
+                    if (half == 0) p.ys[row * p.nf + tf] = amax / kE4m3Max;
                     uint8_t *to = static_cast<uint8_t *>(p.y) + row * p.out + f0;
 #pragma unroll
                     for (int c = 0; c < 64; c += 32) {

@@ -369,7 +369,8 @@ __global__ void __launch_bounds__((Config<MODE, TILE>::kThreads), (Config<MODE, 
                 for (int o = seg >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 if (i < items && (lane & (seg - 1)) == 0) atomicMax(&s_amax[4 * c4 + e], m);
             }
-            if (i < items) parts[part_at(0, 0, c4, r) >> 4] = make_float4(h[0], h[1], h[2], h[3]);   // (only it read them)
+            if (i < items)   // (in the place that only this thread read)
+                parts[part_at(0, 0, c4, r) >> 4] = make_float4(h[0], h[1], h[2], h[3]);
         }
     }
     if constexpr (MODE == GATEUP) {
