@@ -477,8 +477,9 @@ ffn_status ffn_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t b
  *   offsets NULL: w is one matrix, experts 1.  Else offsets [experts + 1] int32
  *   on the device, read when the call runs: rows offsets[e] .. offsets[e + 1] - 1
  *   are multiplied with expert e's matrix (ffn_moe_sort's offsets); rows of no
- *   expert, and their places in y, are not touched.  Offsets beyond 0 .. rows
- *   count as the nearest of the two, an end before its start as the start.
+ *   expert, and their places in y, are not touched.  Offsets do not fall; what is
+ *   beyond 0 .. rows counts as the nearest of the two, and an offset below one
+ *   before it as that one.
  *   res [rows x out] of `dtype` or NULL; y may equal res and overlaps nothing else.
  *   in % 16 == 0, out % 8 == 0, both at most 2^24, 1 <= experts <= 1024, rows and
  *   experts * out at most 2^30, (rows / 32 + min(rows, experts)) * ceil(out / 128)

@@ -38,11 +38,28 @@ struct Params {
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kTileBytes = 128 * 128;   // 128 rows of 128 codes
 
-// The rows of expert e, whatever offsets holds: inside 0 .. rows.
-__device__ __forceinline__ int2 expert_rows(const Params &p, int e) {
-    if (!p.offsets) return make_int2(0, p.rows);
-    const int a = min(max(__ldcg(p.offsets + e), 0), p.rows);
-    return make_int2(a, min(max(__ldcg(p.offsets + e + 1), a), p.rows));
+// Rows first .. end - 1 of expert e0 + lane (a converged warp; `before`: where the
+// experts before e0 end, carried from one call to the next).  Whatever offsets holds,
+// they are inside 0 .. rows and no row is two experts'.
+__device__ __forceinline__ int2 expert_rows(const Params &p, int e0, int lane, int &before) {
+    if (!p.offsets) return make_int2(0, lane == 0 ? p.rows : 0);
+    const int e = e0 + lane;
+    int first = 0, end = 0;
+    if (e < p.experts) {
+        first = min(max(__ldcg(p.offsets + e), 0), p.rows);
+        end = min(max(__ldcg(p.offsets + e + 1), first), p.rows);
+    }
+    int most = end;   // of the experts up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, most, o);
+        if (lane >= o) most = max(most, v);
+    }
+    most = max(most, before);
+    const int ahead = __shfl_up_sync(0xffffffffu, most, 1);
+    first = max(first, lane ? ahead : before);
+    before = __shfl_sync(0xffffffffu, most, 31);
+    return make_int2(first, max(first, end));
 }
 
 // Instruction descriptor, kind::f8f6f4: e4m3 operands, K-major, fp32 sums.

@@ -173,11 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::griddep_wait();   // x, its scales, offsets (and the weights, where they were just quantised)
     if (warp == 0) {       // the experts' tiles
-        int before = 0;
+        int before = 0, rows_before = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
-            int2 r = make_int2(0, 0);
-            if (e < p.experts) r = e4::expert_rows(p, e);
+            const int2 r = e4::expert_rows(p, e0, lane, rows_before);
             const int tiles = (r.y - r.x + kRows - 1) / kRows;
             int incl = tiles;
 #pragma unroll

@@ -48,6 +48,7 @@ template <int MODE, int TILE> struct Config {
     static constexpr uint32_t kPartBytes = kMats * TILE * 128 * 4;          // the parts a CTA receives
     static_assert(kPartBytes <= kStages * kStageBytes, "the parts take the stages' place");
     static_assert(kTmemCols * kCtas <= 512, "tensor memory");
+    static_assert(kCtas * (kSmem + 4608) <= 228 * 1024 && (kCtas + 1) * kSmem > 228 * 1024, "CTAs on an SM");
 };
 
 struct UnitInfo {
@@ -57,11 +58,9 @@ struct UnitInfo {
 // The unit's place (one warp): an expert's units run through its tiles of rows first.
 template <int TILE> __device__ __forceinline__ UnitInfo find_unit(const Params &p, int unit, int lane) {
     UnitInfo u{0, 0, 0, 0, 0};
-    int tiles_before = 0;
+    int tiles_before = 0, rows_before = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        const int e = e0 + lane;
-        int2 r = make_int2(0, 0);
-        if (e < p.experts) r = e4::expert_rows(p, e);
+        const int2 r = e4::expert_rows(p, e0, lane, rows_before);
         const int tiles = (r.y - r.x + TILE - 1) / TILE;
         int incl = tiles;
 #pragma unroll
