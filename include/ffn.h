@@ -515,7 +515,7 @@ ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_wei
  *   topk_idx [rows x k] as ffn_moe_route writes it.  1 <= experts <= 1024, 1 <= k <=
  *   32, rows * k and d at most 2^30, nscales at most d.  Index and scale lists are
  *   aligned to 4 bytes.  Nothing overlaps.
- *   workspace: ffn_moe_sort_workspace_bytes(...), at most 2 MB (0 up to 1024 pairs);
+ *   workspace: ffn_moe_sort_workspace_bytes(...), at most 2 MB (0 up to 8192 pairs);
  *   the answer never falls as rows grow.  The whole call is on `stream` and never
  *   waits for the device.  rows == 0 writes offsets alone.
  *   Its gradient, dx[t] = the sum of dxs over t's pairs, is ffn_moe_unsort of dxs

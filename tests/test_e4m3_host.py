@@ -84,11 +84,11 @@ def test_gateup_refusals(lib):
 
 
 def test_sort_refusals(lib):
-    def need(rows=600, experts=8, k=2):
+    def need(rows=20000, experts=8, k=2):
         out = ctypes.c_size_t(0)
         return lib.ffn_moe_sort_workspace_bytes(rows, experts, k, ctypes.byref(out)), out.value
 
-    def call(x=P[0], sc=P[1], idx=P[2], xs=P[3], xsc=P[4], pos=P[5], offs=P[6], rows=600, d=64, ns=1, experts=8, k=2,
+    def call(x=P[0], sc=P[1], idx=P[2], xs=P[3], xsc=P[4], pos=P[5], offs=P[6], rows=20000, d=64, ns=1, experts=8, k=2,
              dtype=_lib.FFN_E4M3, ws=P[7], nb=1 << 21):
         return lib.ffn_moe_sort(x, sc, idx, xs, xsc, pos, offs, rows, d, ns, experts, k, dtype, ws, nb, None)
     assert need()[0] == OK and need()[1] > 0 and need(rows=1) == (OK, 0) and need(rows=0) == (OK, 0)

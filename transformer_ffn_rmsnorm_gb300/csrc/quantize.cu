@@ -8,7 +8,7 @@
 // operand of dX = dY W, whose blocks are the same ones.
 //
 // Bound by HBM: x is read once and held in registers between its maximum and its
-// codes.  A row's block is 4 to 32 neighbouring lanes with one 16-byte vector each,
+// codes.  A row's block is 2 to 16 neighbouring lanes with two 16-byte vectors each,
 // its maximum a few shuffles, and a thread has four vectors in flight.  A 128 x 128
 // block is one CTA's.
 #include "e4m3.cuh"
@@ -20,7 +20,7 @@ struct QuantParams {
     const void *x;
     uint8_t *q;
     float *scales;
-    int64_t rows, total;   // total: vectors, each row filled up to whole groups
+    int64_t rows, total;   // total: pairs of vectors, each row filled up to whole groups
     int d, group, ngroups;
 };
 
@@ -52,43 +52,52 @@ template <int EPV> __device__ __forceinline__ void store_codes(uint8_t *to, cons
         __stcs(reinterpret_cast<uint32_t *>(to), e4m3x4(f[0] * k, f[1] * k, f[2] * k, f[3] * k));
 }
 
-constexpr int kRowThreads = 256, kRowVecs = 4;
+constexpr int kRowThreads = 256, kRowPairs = 2;
 
-// Rows of whole vectors.  FLAT: of whole groups too, so that the matrix is one
-// run of groups; else a row's vectors are counted up to whole groups.
+// Rows of whole vectors, a thread two in a row at a time (one at a time, the divisions and
+// shuffles for a block kept the schedulers busy 70 % of the time).  FLAT: rows of whole
+// groups too, so that the matrix is one run of groups; else a row's pairs of vectors are
+// counted up to whole groups.
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p) {
     constexpr int EPV = 16 / sizeof(T);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, lanes = p.group / EPV;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kRowThreads * kRowVecs) + threadIdx.x;
+    const int lane = threadIdx.x & 31, lanes = p.group / (2 * EPV);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kRowThreads * kRowPairs) + threadIdx.x;
     const int per_row = p.ngroups * lanes;
-    uint4 v[kRowVecs];
-    int64_t at[kRowVecs];   // first element, or -1
+    uint4 v[kRowPairs][2];
+    int64_t at[kRowPairs];   // first element
+    int have[kRowPairs];     // vectors of the pair that are the row's
 #pragma unroll
-    for (int b = 0; b < kRowVecs; ++b) {
+    for (int b = 0; b < kRowPairs; ++b) {
         const int64_t i = i0 + b * kRowThreads;
         if (FLAT) {
-            at[b] = i < p.total ? i * EPV : -1;
+            at[b] = i * (2 * EPV);
+            have[b] = i < p.total ? 2 : 0;
         } else {
             const int64_t row = i / per_row;
-            const int c = static_cast<int>(i - row * per_row) * EPV;
-            at[b] = i < p.total && c < p.d ? row * p.d + c : -1;
+            const int c = static_cast<int>(i - row * per_row) * (2 * EPV);
+            at[b] = row * p.d + c;
+            have[b] = i < p.total ? min(max((p.d - c) / EPV, 0), 2) : 0;
         }
-        v[b] = at[b] >= 0 ? __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + at[b]))
-                          : make_uint4(0, 0, 0, 0);
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + at[b]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) v[b][j] = j < have[b] ? __ldcs(x + j) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int b = 0; b < kRowVecs; ++b) {
-        uint32_t m = Magnitude<T>::max_of(v[b]);
+    for (int b = 0; b < kRowPairs; ++b) {
+        uint32_t m = max(Magnitude<T>::max_of(v[b][0]), Magnitude<T>::max_of(v[b][1]));
         for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float a = floor_amax(Magnitude<T>::value(m));
+        const float a = floor_amax(Magnitude<T>::value(m)), k = kE4m3Max / a;
         const int64_t i = i0 + b * kRowThreads;
         if (i < p.total && (lane & (lanes - 1)) == 0) p.scales[i / lanes] = a / kE4m3Max;
-        float f[EPV];
-        Vec16<T>::unpack(v[b], f);
-        if (at[b] >= 0) store_codes<EPV>(p.q + at[b], f, kE4m3Max / a);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float f[EPV];
+            Vec16<T>::unpack(v[b][j], f);
+            if (j < have[b]) store_codes<EPV>(p.q + at[b] + j * EPV, f, k);
+        }
     }
 }
 
@@ -203,8 +212,8 @@ cudaError_t launch_typed(QuantParams p, int64_t batch, bool blocks, bool transpo
         const dim3 grid(static_cast<unsigned>((p.rows * p.ngroups + 7) / 8));
         e = launch_dependent(quantize_any_kernel<T>, grid, dim3(256), 0, s, p);
     } else {
-        p.total = p.rows * p.ngroups * (p.group / EPV);
-        const dim3 grid(static_cast<unsigned>((p.total + kRowThreads * kRowVecs - 1) / (kRowThreads * kRowVecs)));
+        p.total = p.rows * p.ngroups * (p.group / (2 * EPV));
+        const dim3 grid(static_cast<unsigned>((p.total + kRowThreads * kRowPairs - 1) / (kRowThreads * kRowPairs)));
         e = p.d % p.group == 0
                 ? launch_dependent(quantize_rows_kernel<T, true>, grid, dim3(kRowThreads), 0, s, p)
                 : launch_dependent(quantize_rows_kernel<T, false>, grid, dim3(kRowThreads), 0, s, p);
