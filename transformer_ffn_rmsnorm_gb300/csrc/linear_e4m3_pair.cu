@@ -90,9 +90,10 @@ __device__ __forceinline__ void st_sector(void *at, const uint32_t (&w)[8]) {
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-// 32 bytes of y, v rounded to T (plus res's, if there is one), of which `left`
+// 32 bytes of y, v (plus res's, if there is one) rounded to T, of which `left`
 // elements, a multiple of 8, are y's.  Rows begin on multiples of 16 bytes.
-template <typename T> __device__ __forceinline__ void store_sector(T *to, const T *res, float *v, int left) {
+template <typename T>
+__device__ __forceinline__ void store_sector(T *to, const uint4 *res, bool add, float *v, int left) {
     constexpr int N = 32 / sizeof(T);
     uint4 o[2];
 #pragma unroll
@@ -100,9 +101,9 @@ template <typename T> __device__ __forceinline__ void store_sector(T *to, const 
         float f[N / 2];
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) f[e] = v[i * N / 2 + e];
-        if (res && i * N / 2 < left) {
+        if (add) {
             float r[N / 2];
-            Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(res + i * N / 2), r);
+            Vec16<T>::unpack(res[i], r);
 #pragma unroll
             for (int e = 0; e < N / 2; ++e) f[e] += r[e];
         }
@@ -392,6 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tf = t.x;
                     trow0 = t.y;
                     tvalid = t.z;
+                    if (MODE == LINEAR && p.res) {   // its lines of this lane's row on the way to L2
+                        const int r = static_cast<int>(rank) * 128 + 32 * q + lane, es = p.dt == DT_F32 ? 4 : 2;
+                        const int col0 = tf * 256 + half * 128, cols = min(128, p.out - col0);
+                        const char *line = static_cast<const char *>(p.res) +
+                                           (static_cast<int64_t>(trow0 + r) * p.out + col0) * es;
+                        for (int b = 0; r < tvalid && b < cols * es; b += 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
+                    }
                 }
                 const float x = my_xs[ring * 128], w0 = my_ws[ring * 2];
                 const uint32_t s0 = __float_as_uint(x * w0),
@@ -448,15 +457,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int col0 = tf * 256 + half * 128;
                 auto store = [&](auto *y) {
                     using T = typename std::remove_reference<decltype(*y)>::type;
-                    constexpr int N = 32 / sizeof(T);   // columns of a full sector
+                    constexpr int N = 32 / sizeof(T), kAhead = 4;   // columns of a sector; sectors requested together
                     T *to = y + row * p.out + col0;
                     const T *from = static_cast<const T *>(p.res) + row * p.out + col0;
+                    const int left = p.out - col0;
 #pragma unroll
-                    for (int c = 0; c < 128; c += N) {
-                        float v[N];
+                    for (int c0 = 0; c0 < 128; c0 += kAhead * N) {
+                        uint4 r[2 * kAhead];
 #pragma unroll
-                        for (int i = 0; i < N; i += 2) unpack2(acc[(c + i) / 2], v[i], v[i + 1]);
-                        store_sector<T>(to + c, p.res ? from + c : nullptr, v, p.out - col0 - c);
+                        for (int i = 0; i < 2 * kAhead; ++i)
+                            r[i] = p.res && c0 + i * (N / 2) < left
+                                       ? *reinterpret_cast<const uint4 *>(from + c0 + i * (N / 2))
+                                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const int c = c0 + i * N;
+                            float v[N];
+#pragma unroll
+                            for (int e = 0; e < N; e += 2) unpack2(acc[(c + e) / 2], v[e], v[e + 1]);
+                            store_sector<T>(to + c, r + 2 * i, p.res != nullptr, v, left - c);
+                        }
                     }
                 };
                 if (local < tvalid) {

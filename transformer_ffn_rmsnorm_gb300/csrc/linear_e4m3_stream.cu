@@ -234,6 +234,14 @@ __global__ void __launch_bounds__((Config<MODE, TILE>::kThreads), (Config<MODE, 
         }
         if (ptx::elect_one()) ptx::tc_commit(bar(&bar_drain));   // every MMA ends before TMEM is freed
         ptx::mbar_wait(bar(&bar_drain), 0, never, e4::kWaitNs);
+    } else if (MODE == LINEAR && warp == 2 && p.res) {
+        // the residual that this CTA will add, on its way to L2
+        const int es = p.dt == DT_F32 ? 4 : 2, rows = 128 / splits, f0 = t.f * 128 + rank * rows;
+        for (int c = lane; c < t.valid && f0 < p.out; c += 32) {
+            const char *line = static_cast<const char *>(p.res) + (static_cast<int64_t>(t.row0 + c) * p.out + f0) * es;
+            for (int b = 0; b < min(rows, p.out - f0) * es; b += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b));
+        }
     } else if (warp >= 4) {
         // ---------------------------------------------------------- sums
         constexpr int kPer = (C::kCols + 31) / 32;   // scales of a lane
@@ -486,7 +494,7 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
         const double block = 0.13 + 0.0027 * static_cast<double>(std::min<int64_t>(mean, 128));
         const double wide = 2. + static_cast<double>((units(128) * n + sms - 1) / sms) * (p.nkb / n * block + 6.);
         const int64_t pairs = used * ((mean + 255) / 256) * ((p.out + 255) / 256);
-        const double pair = 4. + static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * p.nkb * 0.45;
+        const double pair = 3. + static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * (p.nkb * 0.42 + 2.);
         if (wide < pair) return launch_e4m3_stream(mode, true, n, x, w0, w1, in, p, s);
     }
     return launch_e4m3_pair(mode, x, w0, w1, in, p, s);
