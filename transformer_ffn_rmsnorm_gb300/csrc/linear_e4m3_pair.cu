@@ -14,8 +14,8 @@
 // instruction); but the way of a half -- instructions issued, sums done, seen,
 // read and added, their leave sent back across the pair, seen -- is about 1300
 // cycles, of which two halves' 512 are hidden: 790 cycles a block.  (4096 tokens,
-// 4096 -> 11008 gate/up: 274 us; without reading and adding about 220, with one such
-// handshake in 16 blocks 195.  Two accumulators of N = 256 took 349; 16 warps of 64
+// 4096 -> 11008 gate/up: 274 to 283 us.  An earlier form took 349; with nothing read or
+// added 252, with one such handshake in 16 blocks 195.  16 warps of 64
 // columns, whose sums do not fit beside what else the registers hold, 441; one warp
 // issuing both halves' MMAs 387.)
 //
