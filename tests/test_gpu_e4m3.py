@@ -241,3 +241,42 @@ def test_rows_in_pieces(env, start, end):
     s = torch.zeros(333, 7, device="cuda")
     q, _ = ffn.ffn_quantize_e4m3(h[start:end], scales=s[start:end])
     u.check_quantized(torch, q, s[start:end], h[start:end].double(), torch.zeros(end - start, 880, device="cuda"))
+
+
+SKEWED = [[0] * 20 + [500, 3] + [0] * 10, [1] * 40 + [333], [0, 0, 700, 0], [90] + [0] * 63]
+
+
+@pytest.mark.parametrize("counts", SKEWED, ids=lambda c: f"{len(c)}e{max(c)}")
+def test_one_expert_has_most_rows(env, counts):
+    """The mean alone chooses the kernel: few rows an expert, but many of one."""
+    torch, ffn = env
+    rows = sum(counts)
+    x, (wg, wu) = u.make(torch, rows, 400, [264, 264], len(counts), rows)
+    off = offsets_of(torch, counts)
+    ref, mag = u.product(torch, x, wg, off)
+    u.check_linear(torch, ffn.ffn_linear_e4m3(*x, wg, offsets=off), ref, mag, 400)
+    q, s = ffn.ffn_gateup_e4m3(*x, wg, wu, offsets=off)
+    u.check_gateup(torch, q, s, x, wg, wu, 400, off)
+    ffn.ffn_device_status()
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 5, 1], [40, 0, 61], [300, 0, 1, 257], [0, 90] + [0] * 62],
+                         ids=lambda c: f"{len(c)}e{sum(c)}")
+@pytest.mark.parametrize("out", [136, 384])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_residual_by_expert(env, counts, out, dtype):
+    """Elsewhere and in place; rows of no expert keep what they hold, the residual or not."""
+    torch, ffn = env
+    dt, n, more = getattr(torch, dtype), sum(counts), 6
+    x, (w,) = u.make(torch, n + more, 272, [out], len(counts), n)
+    off = offsets_of(torch, counts)
+    ref, mag = u.product(torch, x, w, off)
+    res = torch.randn(n + more, out, device="cuda").to(dt)
+    y = torch.full_like(res, 7.0)
+    ffn.ffn_linear_e4m3(*x, w, offsets=off, res=res, out=y)
+    u.check_linear(torch, y[:n], ref[:n], mag[:n], 272, res[:n])
+    assert bool((y[n:] == 7).all())
+    z = res.clone()
+    ffn.ffn_linear_e4m3(*x, w, offsets=off, res=z, out=z)
+    assert torch.equal(z[:n], y[:n]) and torch.equal(z[n:], res[n:])
+    ffn.ffn_device_status()
