@@ -280,3 +280,21 @@ def test_residual_by_expert(env, counts, out, dtype):
     ffn.ffn_linear_e4m3(*x, w, offsets=off, res=z, out=z)
     assert torch.equal(z[:n], y[:n]) and torch.equal(z[n:], res[n:])
     ffn.ffn_device_status()
+
+
+@pytest.mark.parametrize("rows,inn,out", [(257, 2048, 264), (300, 1296, 392), (512, 4096, 1024), (511, 144, 72),
+                                          (640, 4096, 4096), (1500, 1024, 4104)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_linear_of_few_and_many_units(env, rows, inn, out, dtype):
+    """Units of 128 and of 256 features, whole and cut at the edges, with and without a residual."""
+    torch, ffn = env
+    dt = getattr(torch, dtype)
+    x, (w,) = u.make(torch, rows, inn, [out], 0, rows + out)
+    ref, mag = u.product(torch, x, w)
+    room = torch.full((rows + 8, out), 7.0, device="cuda", dtype=dt)
+    ffn.ffn_linear_e4m3(*x, w, out=room[:rows])
+    u.check_linear(torch, room[:rows], ref, mag, inn)
+    assert bool((room[rows:] == 7).all())
+    res = torch.randn(rows, out, device="cuda").to(dt)
+    u.check_linear(torch, ffn.ffn_linear_e4m3(*x, w, res=res), ref, mag, inn, res)
+    ffn.ffn_device_status()

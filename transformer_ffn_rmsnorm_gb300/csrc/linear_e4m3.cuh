@@ -115,8 +115,9 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
 // wide: tiles of 128 rows (linear only), else 32
 cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8_t *x, const uint8_t *w0,
                                const uint8_t *w1, int64_t in, const e4::Params &p, cudaStream_t s);
-cudaError_t launch_e4m3_pair(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
-                             const e4::Params &p, cudaStream_t s);
+// narrow: units of 128 features (linear only), else 256 (gate/up: 128 of both)
+cudaError_t launch_e4m3_pair(e4::Mode mode, bool narrow, const uint8_t *x, const uint8_t *w0, const uint8_t *w1,
+                             int64_t in, const e4::Params &p, cudaStream_t s);
 
 cudaError_t launch_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t batch, int64_t rows, int64_t d,
                                  int64_t group, bool blocks, bool transpose, int dt, cudaStream_t s);

@@ -6,6 +6,8 @@
 // from the odd one's).  A block of 128 values is multiplied in two halves of N = 128,
 // each into one of four accumulators, which together are all of tensor memory; a
 // gate/up half holds 64 features' gate and up columns, so that they meet in a thread.
+// Linear with few units takes narrow ones, of 128 features in halves of N = 64 on
+// eight accumulators: 0.31 us a block against 0.42, for half the work.
 //
 // What bounds it: each block's sums have to leave tensor memory before the block
 // after next may use their place.  The tensor pipe needs 512 cycles a block and SM
@@ -45,12 +47,19 @@ using e4::LINEAR;
 using e4::Params;
 
 constexpr int kRows = 256;                                 // of x in a unit
-constexpr uint32_t kStageBytes = 2 * e4::kTileBytes;       // one CTA's rows of x and of the weights
-constexpr int kStages = 6;
 constexpr int kEpiWarps = 8, kThreads = 32 * (4 + kEpiWarps);
-constexpr size_t kSmem = kStages * kStageBytes + 1024;
-static_assert(kSmem > 114 * 1024 && kSmem < 210 * 1024, "one CTA per SM: each allocates all of tensor memory");
 constexpr uint32_t kTmemCols = 512;
+// What follows from N, the columns of a half (64: linear's narrow units).
+template <int MODE, int N> struct Config {
+    static_assert(N == 128 || (MODE == LINEAR && N == 64), "a half");
+    static constexpr int kFeatures = MODE == GATEUP ? 128 : 2 * N;   // of a unit
+    static constexpr int kDepth = static_cast<int>(kTmemCols) / (2 * N);   // accumulators of a half
+    static constexpr uint32_t kHalfBytes = N / 2 * 128;                // one CTA's weight rows of a half
+    static constexpr uint32_t kStageBytes = e4::kTileBytes + 2 * kHalfBytes;
+    static constexpr int kStages = static_cast<int>(12 * e4::kTileBytes / kStageBytes);
+    static constexpr size_t kSmem = kStages * kStageBytes + 1024;
+    static_assert(kSmem > 114 * 1024 && kSmem < 210 * 1024, "one CTA per SM: each allocates all of tensor memory");
+};
 // Registers of a thread after the warpgroups have shared them out: 168 at launch.  (Where a
 // role spilled, the issuers at 56 and the sums at 208, a block took up to twice the time.)
 constexpr int kFewRegs = 72, kManyRegs = 216;
@@ -124,13 +133,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
     return r;
 }
-template <int MODE>
+template <int MODE, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     e4m3_pair_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                      const __grid_constant__ CUtensorMap map_x, const Params p) {
-    constexpr int kFeatures = MODE == GATEUP ? 128 : 256;   // of a unit
+    using C = Config<MODE, N>;
+    constexpr int kFeatures = C::kFeatures, kStages = C::kStages, kDepth = C::kDepth;
+    constexpr uint32_t kStageBytes = C::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages], bar_tfull[4], bar_tempty[4], bar_drain;
+    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
+    __shared__ __align__(8) uint64_t bar_tfull[2 * kDepth], bar_tempty[2 * kDepth], bar_drain;
     __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2];
     __shared__ float s_xs[2][kScaleBlocks][128], s_ws[2][kScaleBlocks][2];
     __shared__ int4 s_unit[2];   // f, row0, valid of the unit that the slot of scales begins
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(&bar_full[s]), 1);
             ptx::mbar_init(bar(&bar_empty[s]), 2);   // both halves
         }
-        for (int a = 0; a < 4; ++a) {   // accumulator 2 * (block % 2) + half
+        for (int a = 0; a < 2 * kDepth; ++a) {   // accumulator 2 * (block % kDepth) + half
             ptx::mbar_init(bar(&bar_tfull[a]), 1);
             ptx::mbar_init(bar(&bar_tempty[a]), kEpiWarps);   // half of the warps, of both CTAs
         }
@@ -241,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = u0; u < units && ok; u += ustep) {
                 const Unit t = unit_of(u);
                 const int xrow = t.row0 + static_cast<int>(rank) * 128;
-                // 64 weight rows of each half: gate/up: the CTA's matrix's next; linear: the CTA's part of 128
+                // N / 2 weight rows of each half: gate/up: the CTA's matrix's next; linear: the CTA's part of N
                 const int wrow =
-                    t.expert * p.out + t.f * kFeatures + (MODE == GATEUP ? 0 : static_cast<int>(rank) * 64);
+                    t.expert * p.out + t.f * kFeatures + (MODE == GATEUP ? 0 : static_cast<int>(rank) * (N / 2));
                 const CUtensorMap *mw = MODE == GATEUP && rank ? &map_w1 : &map_w0;
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     const bool got = ptx::mbar_wait(bar(&bar_empty[s]), ph ^ 1u, abort_flag, e4::kWaitNs);
@@ -256,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (leader) ptx::mbar_arrive_expect_tx(bar(&bar_full[s]), 2 * kStageBytes);
                         ptx::tma_load_2d_pair(at, &map_x, full, kb * 128, xrow);
                         ptx::tma_load_2d_pair(at + e4::kTileBytes, mw, full, kb * 128, wrow);
-                        ptx::tma_load_2d_pair(at + e4::kTileBytes + 64 * 128, mw, full, kb * 128,
-                                              wrow + (MODE == GATEUP ? 64 : 128));
+                        ptx::tma_load_2d_pair(at + e4::kTileBytes + C::kHalfBytes, mw, full, kb * 128,
+                                              wrow + (MODE == GATEUP ? 64 : N));
                     }
                     __syncwarp();
                     ++produced;
@@ -275,10 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- MMA issuers
             // One warp for each half of a block.  What a block needs besides its accumulator is
             // looked at before that, so that the instructions follow its release at once.
-            constexpr uint32_t idesc = e4::idesc_e4m3(256, 128);
+            constexpr uint32_t idesc = e4::idesc_e4m3(256, N);
             const int half = warp - 1;
             const uint64_t ad0 = ptx::sdesc_k_sw128(base),
-                           bd0 = ptx::sdesc_k_sw128(base + e4::kTileBytes + half * 64 * 128);
+                           bd0 = ptx::sdesc_k_sw128(base + e4::kTileBytes + half * C::kHalfBytes);
             bool ok = true;
             int s = 0, a = 0;
             uint32_t ph = 0, pa = 0;
@@ -296,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ptx::elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 bytes of k further: 2 in the address field
-                            e4::mma_e4m3_pair(tmem + acc * 128, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                            e4::mma_e4m3_pair(tmem + acc * N, ad + 2 * k, bd + 2 * k, idesc, k != 0);
                         ptx::tc_commit_pair(bar(&bar_tfull[acc]), 0x3);
                         ptx::tc_commit_pair(bar(&bar_empty[s]), 0x3);
                     }
@@ -305,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s = 0;
                         ph ^= 1u;
                     }
-                    a ^= 1;
+                    if (kDepth == 2) a ^= 1;
+                    else a = (a + 1) & (kDepth - 1);
                     if (a == 0) pa ^= 1u;
                 }
             }
@@ -329,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) at[i] = min(first + 32 * i, last) * p.nkb;
                 // lane 0: gate or the first half's block, lane 1: up or the second's
-                const int nb = MODE == GATEUP ? t.f : min(2 * t.f + (lane & 1), p.nf - 1);
+                const int nb = MODE == GATEUP ? t.f : min(N == 128 ? 2 * t.f + (lane & 1) : t.f, p.nf - 1);
                 const float *ws = (MODE == GATEUP && (lane & 1) ? p.ws[1] : p.ws[0]) +
                                   (static_cast<int64_t>(t.expert) * p.nf + nb) * p.nkb;
                 for (int k0 = 0; k0 < p.nkb; k0 += kScaleBlocks) {
@@ -371,17 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---------------------------------------------------------- sums
         const int q = warp & 3, half = (warp - 4) >> 2;
-        // addresses of the half's two accumulators and their barriers lie 256 columns and 16 bytes apart
-        const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+        // addresses of the half's accumulators and their barriers lie 2 N columns and 16 bytes apart
+        const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * N;
         const uint32_t tfull = bar(&bar_tfull[half]), tempty = lead(bar(&bar_tempty[half]));
         const uint32_t sfull = bar(&bar_sfull[0]), sempty = bar(&bar_sempty[0]);
         const float *my_xs = &s_xs[0][0][32 * q + lane], *my_ws = &s_ws[0][0][MODE == GATEUP ? 0 : half];
         uint32_t a = 0, pa = 0;             // of the next block: accumulator, its parity
         uint32_t ring = 0, pring = 0;       // its place in the ring of scales, the ring's parity
         for (int u = u0; u < units; u += ustep) {
-            uint64_t acc[64];   // two columns each; gate/up: 64 of gate, then 64 of up
+            uint64_t acc[N / 2];   // two columns each; gate/up: 64 of gate, then 64 of up
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+            for (int i = 0; i < N / 2; ++i) acc[i] = 0ull;
             bool ok = true, done = false;   // done: this block's sums are known to be there
             int tf = 0, trow0 = 0, tvalid = 0;
             for (int kb = p.nkb; kb > 0; --kb) {
@@ -395,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tvalid = t.z;
                     if (MODE == LINEAR && p.res) {   // its lines of this lane's row on the way to L2
                         const int r = static_cast<int>(rank) * 128 + 32 * q + lane, es = p.dt == DT_F32 ? 4 : 2;
-                        const int col0 = tf * 256 + half * 128, cols = min(128, p.out - col0);
+                        const int col0 = tf * kFeatures + half * N, cols = min(N, p.out - col0);
                         const char *line = static_cast<const char *>(p.res) +
                                            (static_cast<int64_t>(trow0 + r) * p.out + col0) * es;
                         for (int b = 0; r < tvalid && b < cols * es; b += 128)
@@ -412,22 +425,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = trow + 256 * a;
+                const uint32_t taddr = trow + 2 * N * a;
                 // 32 columns at a time, loaded under the additions before (of 16: gate/up 279 -> 301 us)
                 constexpr int kCols = 32;
                 uint32_t r[2][kCols];
                 ptx::tmem_ld_cols<kCols>(taddr, r[0]);
 #pragma unroll
-                for (int c = 0; c < 128 / kCols; ++c) {
+                for (int c = 0; c < N / kCols; ++c) {
                     ptx::tmem_ld_wait();
-                    if (c < 128 / kCols - 1) {
+                    if (c < N / kCols - 1) {
                         ptx::tmem_ld_cols<kCols>(taddr + kCols * (c + 1), r[(c + 1) & 1]);
                     } else {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_read(tempty + 16 * a);
-                        pa ^= a;
-                        a ^= 1u;
+                        if (kDepth == 2) {   // (a comparison here: gate/up 274 -> 278 us)
+                            pa ^= a;
+                            a ^= 1u;
+                        } else {
+                            a = (a + 1) & (kDepth - 1);
+                            pa ^= a == 0 ? 1u : 0u;
+                        }
                         done = ptx::mbar_test(tfull + 16 * a, pa);
                     }
 #pragma unroll
@@ -454,27 +472,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *abort_flag = 1;
                     break;
                 }
-                const int col0 = tf * 256 + half * 128;
+                const int col0 = tf * kFeatures + half * N;
                 auto store = [&](auto *y) {
                     using T = typename std::remove_reference<decltype(*y)>::type;
-                    constexpr int N = 32 / sizeof(T), kAhead = 4;   // columns of a sector; sectors requested together
+                    constexpr int M = 32 / sizeof(T), kAhead = 4;   // columns of a sector; sectors requested together
                     T *to = y + row * p.out + col0;
                     const T *from = static_cast<const T *>(p.res) + row * p.out + col0;
                     const int left = p.out - col0;
 #pragma unroll
-                    for (int c0 = 0; c0 < 128; c0 += kAhead * N) {
+                    for (int c0 = 0; c0 < N; c0 += kAhead * M) {
                         uint4 r[2 * kAhead];
 #pragma unroll
                         for (int i = 0; i < 2 * kAhead; ++i)
-                            r[i] = p.res && c0 + i * (N / 2) < left
-                                       ? *reinterpret_cast<const uint4 *>(from + c0 + i * (N / 2))
+                            r[i] = p.res && c0 + i * (M / 2) < left
+                                       ? *reinterpret_cast<const uint4 *>(from + c0 + i * (M / 2))
                                        : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int i = 0; i < kAhead; ++i) {
-                            const int c = c0 + i * N;
-                            float v[N];
+                            const int c = c0 + i * M;
+                            float v[M];
 #pragma unroll
-                            for (int e = 0; e < N; e += 2) unpack2(acc[(c + e) / 2], v[e], v[e + 1]);
+                            for (int e = 0; e < M; e += 2) unpack2(acc[(c + e) / 2], v[e], v[e + 1]);
                             store_sector<T>(to + c, r + 2 * i, p.res != nullptr, v, left - c);
                         }
                     }
@@ -567,11 +585,11 @@ bool map_codes(CUtensorMap *m, const void *ptr, int64_t in, int64_t rows, uint32
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE>
+template <int MODE, int N>
 cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in, const Params &p,
                    cudaStream_t s) {
-    constexpr int kFeatures = MODE == GATEUP ? 128 : 256;
-    const auto kern = &e4m3_pair_kernel<MODE>;
+    using C = Config<MODE, N>;
+    const auto kern = &e4m3_pair_kernel<MODE, N>;
     static std::atomic<int> configured_device{-1}, pair_slots{0};   // (host threads may call at the same time)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -585,13 +603,13 @@ cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.attrs = attr;
     int slots = 0;   // co-resident CTA pairs
     if (configured_device.load(std::memory_order_acquire) == dev) {
         slots = pair_slots.load(std::memory_order_relaxed);
     } else {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
         cfg.numAttrs = 1;
@@ -603,10 +621,10 @@ cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64
     }
     CUtensorMap m0, m1, mx;
     const int64_t wrows = static_cast<int64_t>(p.experts) * p.out;
-    if (!map_codes(&m0, w0, in, wrows, 64) || !map_codes(&mx, x, in, p.rows, 128)) return cudaErrorInvalidValue;
+    if (!map_codes(&m0, w0, in, wrows, N / 2) || !map_codes(&mx, x, in, p.rows, 128)) return cudaErrorInvalidValue;
     m1 = m0;
-    if (MODE == GATEUP && !map_codes(&m1, w1, in, wrows, 64)) return cudaErrorInvalidValue;
-    const int64_t most = moe::max_tiles(p.rows, p.experts, kRows) * ((p.out + kFeatures - 1) / kFeatures);
+    if (MODE == GATEUP && !map_codes(&m1, w1, in, wrows, N / 2)) return cudaErrorInvalidValue;
+    const int64_t most = moe::max_tiles(p.rows, p.experts, kRows) * ((p.out + C::kFeatures - 1) / C::kFeatures);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(slots, most)));
     cfg.stream = s;
     cfg.numAttrs = 2;
@@ -617,9 +635,10 @@ cudaError_t launch(const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64
 
 }  // namespace
 
-cudaError_t launch_e4m3_pair(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
-                             const Params &p, cudaStream_t s) {
-    return mode == GATEUP ? launch<GATEUP>(x, w0, w1, in, p, s) : launch<LINEAR>(x, w0, w1, in, p, s);
+cudaError_t launch_e4m3_pair(e4::Mode mode, bool narrow, const uint8_t *x, const uint8_t *w0, const uint8_t *w1,
+                             int64_t in, const Params &p, cudaStream_t s) {
+    if (mode == GATEUP) return launch<GATEUP, 128>(x, w0, w1, in, p, s);
+    return narrow ? launch<LINEAR, 64>(x, w0, w1, in, p, s) : launch<LINEAR, 128>(x, w0, w1, in, p, s);
 }
 
 }  // namespace ffn

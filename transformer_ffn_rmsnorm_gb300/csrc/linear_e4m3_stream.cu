@@ -471,7 +471,10 @@ cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8
 // the reduction where few units leave the pairs idle: by the estimates below, us.
 // Linear 14336 -> 4096, pairs / tiles of 128: 48 rows 50.6 / 15.2, 128 rows 51.7 /
 // 21.5, 256 rows 51.7 / 35.9, 512 rows 52.3 / 65.2; 4096 -> 14336, 64 rows 19.1 /
-// 18.3, 128 rows 20.5 / 27.3; 64 experts 1408 -> 2048, 48 rows 53.6 / 77.7.
+// 18.3, 128 rows 20.5 / 27.3; 64 experts 1408 -> 2048, 48 rows 53.6 / 77.7.  The pairs'
+// units have 256 features, or 128 where that takes as few rounds: 14336 -> 4096, 512
+// rows 50.2 / 38.5, 640 rows 54.3 / 75.6, 1024 rows 52.1 / 72.9; 512 rows of 2048 ->
+// 2048 12.5 / 9.6; 777 rows of 1024 -> 520 10.9 / 8.3.
 cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
                                 Params p, cudaStream_t s) {
     p.nf = (p.out + 127) / 128;
@@ -493,11 +496,15 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
         const int n = parts(128, sms);
         const double block = 0.13 + 0.0027 * static_cast<double>(std::min<int64_t>(mean, 128));
         const double wide = 2. + static_cast<double>((units(128) * n + sms - 1) / sms) * (p.nkb / n * block + 6.);
-        const int64_t pairs = used * ((mean + 255) / 256) * ((p.out + 255) / 256);
-        const double pair = 3. + static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * (p.nkb * 0.42 + 2.);
-        if (wide < pair) return launch_e4m3_stream(mode, true, n, x, w0, w1, in, p, s);
+        auto pairs = [&](int features, double block, double end) {
+            const int64_t u = used * ((mean + 255) / 256) * ((p.out + features - 1) / features);
+            return 3. + static_cast<double>((u + sms / 2 - 1) / (sms / 2)) * (p.nkb * block + end);
+        };
+        const double full = pairs(256, 0.42, 2.), narrow = pairs(128, 0.31, 1.5);
+        if (wide < std::min(full, narrow)) return launch_e4m3_stream(mode, true, n, x, w0, w1, in, p, s);
+        return launch_e4m3_pair(mode, narrow < full, x, w0, w1, in, p, s);
     }
-    return launch_e4m3_pair(mode, x, w0, w1, in, p, s);
+    return launch_e4m3_pair(mode, false, x, w0, w1, in, p, s);
 }
 
 }  // namespace ffn
