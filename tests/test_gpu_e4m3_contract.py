@@ -1,0 +1,49 @@
+"""What include/ffn.h says of the e4m3 operators beyond their formulas' tolerances: the codes' bits,
+falling offsets, where scales and pointers may lie."""
+
+import pytest
+
+import e4m3_util as u
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    from transformer_ffn_rmsnorm_gb300 import ffn
+    return torch, ffn
+
+
+# ------------------------------------------------------------------ bits
+def quantized(torch, x, block_rows, group):
+    """(codes, scales) of x [rows, d] by the formula in 32 bits on the host, each step rounded to nearest even."""
+    v = x.float().cpu().numpy()
+    rows, d = v.shape
+    q, s = v.copy(), []
+    for r in range(0, rows, block_rows):
+        line = []
+        for c in range(0, d, group):
+            b = v[r:r + block_rows, c:c + group]
+            one = b.dtype.type
+            a = max(abs(b).max(), one(2.0 ** -100))
+            line.append(a / one(448))
+            q[r:r + block_rows, c:c + group] = b * (one(448) / a)
+        s.append(line)
+    q = torch.from_numpy(q).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    return q.view(torch.uint8).cuda(), torch.tensor(s, dtype=torch.float32, device="cuda")
+
+
+@pytest.mark.parametrize("rows,d,block_rows,group", [(300, 1000, 1, 128), (77, 130, 1, 128), (129, 264, 1, 64),
+                                                     (65, 96, 1, 32), (400, 656, 128, 128)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_quantize_bit_for_bit(env, rows, d, block_rows, group, dtype):
+    """Values of 16 bits lie on ties between codes, where the last bit of 448 / a decides: the quotient is the
+    nearest one, not 448 times a rounded reciprocal."""
+    torch, ffn = env
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn(rows, d, generator=gen, device="cuda") * 3).to(getattr(torch, dtype))
+    q, s = ffn.ffn_quantize_e4m3(x, block_rows=block_rows, group=group)
+    want, scales = quantized(torch, x, block_rows, group)
+    assert torch.equal(s, scales)
+    assert torch.equal(q.view(torch.uint8), want)
