@@ -401,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool got = true;
                 if ((ring & (kScaleBlocks - 1)) == 0)
                     got = ptx::mbar_wait(sfull + 8 * (ring / kScaleBlocks), pring, abort_flag, e4::kWaitNs);
-                if (kb == p.nkb) {
+                if (kb == p.nkb) {   // (after an abandoned wait the unit is not known, and not used)
                     const int4 t = s_unit[ring / kScaleBlocks];
                     tf = t.x;
                     trow0 = t.y;
                     tvalid = t.z;
-                    if (MODE == LINEAR && p.res) {   // its lines of this lane's row on the way to L2
+                    if (MODE == LINEAR && p.res && got) {   // its lines of this lane's row on the way to L2
                         const int r = static_cast<int>(rank) * 128 + 32 * q + lane, es = p.dt == DT_F32 ? 4 : 2;
                         const int col0 = tf * kFeatures + half * N, cols = min(N, p.out - col0);
                         const char *line = static_cast<const char *>(p.res) +
