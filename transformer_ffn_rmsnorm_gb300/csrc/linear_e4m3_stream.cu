@@ -190,12 +190,11 @@ __global__ void __launch_bounds__((Config<MODE, TILE>::kThreads), (Config<MODE, 
             }
         }
         if (!ok) *abort_flag = 1;
-        // every load has landed before the stages' place is used again (it has, unless a wait was abandoned)
-        if (!ok || *abort_flag)
-            for (int i = 0; i < C::kStages; ++i)
-                if (issued > i)
-                    ptx::mbar_wait(bar(&bar_full[i]), ((issued - i + C::kStages - 1) / C::kStages - 1) & 1u, never,
-                                   e4::kWaitNs);
+        // Every load has landed before the stages' place is used again, whoever else gives up and when.
+        for (int i = 0; i < C::kStages; ++i)
+            if (issued > i)
+                ptx::mbar_wait(bar(&bar_full[i]), ((issued - i + C::kStages - 1) / C::kStages - 1) & 1u, never,
+                               e4::kWaitNs);
     } else if (warp == 1) {
         // -------------------------------------------------- MMA issuer
         const uint32_t idesc = e4::idesc_e4m3(128, t.n);
