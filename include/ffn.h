@@ -672,6 +672,18 @@ ffn_status ffn_device_status(void);
  * usable.  Returns FFN_OK when launched, FFN_ERR_CUDA if the launch failed. */
 ffn_status ffn_selftest_bounded_wait(uint64_t limit_ns, void *stream);
 
+/* The end of a pair of multiprocessors after one of them has given up: two CTAs,
+ * of which the even one has issued `even` loads into a ring of 4 slots and the odd one
+ * `odd`, and nothing takes them; the library's own end of such kernels then waits until all have
+ * landed.  Load i of CTA r brings 4096 bytes of src from 4096 (2 i + r) on (src holds
+ * 8192 max(even, odd) bytes, 16-byte aligned); wrong [2] int32, zeroed by the
+ * caller, counts for each CTA the bytes of its last loads that had not landed.
+ * 0 <= even, odd <= 64 and no slot filled more than once more by one CTA than
+ * by the other, as where both stop at releases of the ring: max(even, odd) <=
+ * 4 (min(even, odd) / 4 + 1), else FFN_ERR_SHAPE.  A wait that the loads do not end within a
+ * second records FFN_ERR_TIMEOUT. */
+ffn_status ffn_selftest_pair_end(const uint8_t *src, int32_t *wrong, int64_t even, int64_t odd, void *stream);
+
 /* Number of kernels this library has launched since it was loaded (host count). */
 uint64_t ffn_launch_count(void);
 

@@ -905,6 +905,16 @@ ffn_status ffn_selftest_bounded_wait(uint64_t limit_ns, void *stream) {
     return from_cuda(launch_bounded_wait_probe(limit_ns, static_cast<cudaStream_t>(stream)));
 }
 
+ffn_status ffn_selftest_pair_end(const uint8_t *src, int32_t *wrong, int64_t even, int64_t odd, void *stream) {
+    if (!src || !wrong) return FFN_ERR_NULL;
+    const int64_t least = std::min(even, odd), most = std::max(even, odd);
+    if (least < 0 || most > 64 || most > kPairProbeSlots * (least / kPairProbeSlots + 1)) return FFN_ERR_SHAPE;
+    if (!aligned16(src) || !aligned(wrong, 4)) return FFN_ERR_ALIGN;
+    if (overlaps({wrong, 8}, {src, static_cast<size_t>(most) * 2 * kPairProbeBytes})) return FFN_ERR_ALIAS;
+    return from_cuda(launch_pair_end_probe(src, wrong, static_cast<int>(even), static_cast<int>(odd),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
 ffn_status ffn_prepare_weights(const void *src, void *dst, int64_t count, ffn_dtype src_dtype,
                                void *stream) {
     if (count != 0 && (!src || !dst)) return FFN_ERR_NULL;

@@ -118,6 +118,9 @@ cudaError_t launch_swiglu(const void *gate, const void *up, void *h, int64_t cou
 // One CTA whose bounded wait on a never-completed barrier gives up after
 // limit_ns and records DEVERR_TIMEOUT (selftest.cu).
 cudaError_t launch_bounded_wait_probe(uint64_t limit_ns, cudaStream_t s);
+// One CTA pair that ends after its even CTA has issued `even` loads and its odd one `odd` (selftest.cu).
+constexpr int kPairProbeSlots = 4, kPairProbeBytes = 4096;
+cudaError_t launch_pair_end_probe(const uint8_t *src, int32_t *wrong, int even, int odd, cudaStream_t s);
 
 // fp32 G, U -> 16-bit h = silu(G) * U * out_scale, and its residual h_lo
 // when non-null (unfused arm of the tensor-core path)
@@ -231,6 +234,10 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                  "r"(bytes)
                  : "memory");
+}
+// Takes `bytes` off what the barrier still expects, without a copy.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

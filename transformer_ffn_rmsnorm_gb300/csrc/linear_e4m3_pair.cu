@@ -38,6 +38,7 @@
 
 #include "linear_e4m3.cuh"
 #include "moe.cuh"
+#include "pair_end.cuh"
 
 namespace ffn {
 namespace {
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint8_t s_last[moe::kMaxExperts];
     __shared__ float s_amax[MODE == GATEUP ? 2 : 1][128];
     __shared__ uint32_t s_tmem_base;
+    __shared__ PairEnd s_end;
     __shared__ int s_abort, s_never;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -563,16 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    __syncthreads();
-    if (warp == 0 && lane == 0 && leader) {
-        // loads still in flight (only after an abandoned wait) land before shared memory is released
-        for (uint32_t s = 0; s < kStages; ++s)
-            if (produced > s)
-                ptx::mbar_wait(bar(&bar_full[s]), ((produced - s + kStages - 1) / kStages - 1) & 1u, never,
-                               e4::kWaitNs);
-    }
-    __syncthreads();
-    ptx::cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
+    end_pair<kStages>(s_end, rank, produced, abort_flag, never, e4::kWaitNs, [&](int s) { return bar(&bar_full[s]); },
+                      [](int) { return kStageBytes; });
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after();

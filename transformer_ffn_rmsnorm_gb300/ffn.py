@@ -761,6 +761,19 @@ def ffn_selftest_bounded_wait(limit_ns: int = 2_000_000, stream=None):
     _check(_lib.load().ffn_selftest_bounded_wait(int(limit_ns), _stream(stream)), "ffn_selftest_bounded_wait")
 
 
+def ffn_selftest_pair_end(src: torch.Tensor, even: int, odd: int, stream=None) -> torch.Tensor:
+    """The bytes that had not landed when a CTA pair ended whose CTAs had issued `even` and `odd` loads, int32 [2];
+    src: 8192 * max(even, odd) bytes."""
+    if stream is not None:   # the result belongs to that stream
+        with torch.cuda.stream(stream):
+            return ffn_selftest_pair_end(src, even, odd)
+    dev = src.get_device()
+    _expect("src", src, (8192 * max(even, odd),), torch.uint8, dev)
+    wrong = torch.zeros(2, dtype=torch.int32, device=src.device)
+    _launch(_LIB.ffn_selftest_pair_end, "ffn_selftest_pair_end", dev, src.data_ptr(), wrong.data_ptr(), even, odd)
+    return wrong
+
+
 def ffn_launch_count() -> int:
     return int(_lib.load().ffn_launch_count())
 
