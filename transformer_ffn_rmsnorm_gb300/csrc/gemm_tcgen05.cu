@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "ffn_internal.cuh"
+#include "pair_end.cuh"
 
 namespace ffn {
 namespace {
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
     __shared__ uint32_t s_tmem_base;
+    __shared__ PairEnd s_end;
     __shared__ int s_abort, s_never;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -552,24 +554,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     }
 
-    __syncthreads();
-    if (warp == 0 && lane == 0 && leader) {
-        // TMA loads still in flight (only after an abandoned wait) must land
-        // before shared memory is released; the even CTA's ring barriers
-        // count the bytes of both CTAs of a pair.
-        for (uint32_t s = 0; s < STAGES; ++s) {
-            if (produced > s) {
-                const uint64_t armed = (produced - s + STAGES - 1) / STAGES;
-                ptx::mbar_wait(full(s), static_cast<uint32_t>((armed - 1) & 1), never, limit);
-            }
-        }
-    }
     if constexpr (PAIR) {
         // neither CTA of the pair leaves (or frees TMEM) while the other may
         // still copy into its shared memory, arrive on its barriers or
         // read the accumulators
+        end_pair<STAGES>(s_end, rank, static_cast<uint32_t>(produced), abort_flag, never, limit, full,
+                         [](int, int) { return STAGE_BYTES; });
+    } else {
         __syncthreads();
-        ptx::cluster_sync();
+        if (warp == 0 && lane == 0) {
+            // TMA loads still in flight (only after an abandoned wait) must land
+            // before shared memory is released
+            for (uint32_t s = 0; s < STAGES; ++s) {
+                if (produced > s) {
+                    const uint64_t armed = (produced - s + STAGES - 1) / STAGES;
+                    ptx::mbar_wait(full(s), static_cast<uint32_t>((armed - 1) & 1), never, limit);
+                }
+            }
+        }
     }
     if (warp == 1) {
         __syncwarp();

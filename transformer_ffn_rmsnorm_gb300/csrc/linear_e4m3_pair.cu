@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     end_pair<kStages>(s_end, rank, produced, abort_flag, never, e4::kWaitNs, [&](int s) { return bar(&bar_full[s]); },
-                      [](int) { return kStageBytes; });
+                      [](int, int) { return kStageBytes; });
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after();

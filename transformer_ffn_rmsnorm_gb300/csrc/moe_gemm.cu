@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "moe.cuh"
+#include "pair_end.cuh"
 
 namespace ffn {
 namespace {
@@ -75,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
     __shared__ __align__(8) uint64_t bar_tfull[2], bar_tempty[2], bar_drain;
     __shared__ float s_swap[MODE == GATEUP ? kEpiWarps / 4 : 1][MODE == GATEUP ? 2 : 1][2][8][64];
-    __shared__ uint32_t s_tmem_base;
+    __shared__ uint32_t s_tmem_base, s_bytes[kStages];   // s_bytes: of the CTA's last load into a stage
+    __shared__ PairEnd s_end;
     __shared__ int s_abort, s_never;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ptx::elect_one()) {
                     const uint32_t bar = lead(full(s));
-                    if (leader)
-                        ptx::mbar_arrive_expect_tx(full(s), kSub * (2 * kABytes + t.n * (kBK * 2)));
+                    const uint32_t bytes = kSub * (kABytes + half * (kBK * 2));
+                    s_bytes[s] = bytes;
+                    if (leader) ptx::mbar_arrive_expect_tx(full(s), 2 * bytes);
 #pragma unroll
                     for (int j = 0; j < kSub; ++j) {
                         const int k0 = (ks * kSub + j) * kBK;   // a block past K is zero fill
@@ -279,15 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    __syncthreads();
-    if (warp == 0 && lane == 0 && leader) {
-        // loads still in flight (only after an abandoned wait) land before shared memory is released
-        for (uint32_t s = 0; s < kStages; ++s)
-            if (produced > s)
-                ptx::mbar_wait(full(s), ((produced - s + kStages - 1) / kStages - 1) & 1u, never, kWaitNs);
-    }
-    __syncthreads();
-    ptx::cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
+    end_pair<kStages>(s_end, rank, produced, abort_flag, never, kWaitNs, full, [&](int s, int r) {
+        return ld_cluster(ptx::mapa_shared(ptx::smem_u32(&s_bytes[s]), r));
+    });
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after();

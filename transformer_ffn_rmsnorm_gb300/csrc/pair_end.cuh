@@ -20,10 +20,16 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Called by every thread of both CTAs when its role has ended; thread 0 knows the CTA's
-// `produced`, the slots that it has filled one after the other.  `full`: the address of slot
-// s's barrier; bytes(s): what this CTA's last load into slot s brings, or, where it has
-// issued one less than the other CTA, what the other's did (the two parts are alike in size).
+// `produced`, the slots that it has filled one after the other.  full(s): the address of slot s's
+// barrier; bytes(s, r): what CTA r's last load into slot s brings (the two parts are alike in
+// size).
 template <int STAGES, typename Full, typename Bytes>
 __device__ __forceinline__ void end_pair(PairEnd &end, uint32_t rank, uint32_t produced, const volatile int *abort_flag,
                                          volatile int *never, uint64_t limit_ns, const Full &full, const Bytes &bytes) {
@@ -45,8 +51,8 @@ __device__ __forceinline__ void end_pair(PairEnd &end, uint32_t rank, uint32_t p
             const uint32_t first = static_cast<uint32_t>(s);
             auto fills = [&](uint32_t n) { return n > first ? (n - first + STAGES - 1) / STAGES : 0u; };
             const uint32_t mine = fills(end.produced[0]), theirs = fills(end.produced[1]);
-            if (mine < theirs) ptx::mbar_arrive_expect_tx(full(s), bytes(s));   // armed for their part alone
-            if (mine > theirs) ptx::mbar_complete_tx(full(s), bytes(s));        // their part is not to come
+            if (mine < theirs) ptx::mbar_arrive_expect_tx(full(s), bytes(s, 1));   // armed for their part alone
+            if (mine > theirs) ptx::mbar_complete_tx(full(s), bytes(s, 0));        // their part is not to come
             const uint32_t last = max(mine, theirs);
             if (last) ptx::mbar_wait(full(s), (last - 1) & 1u, never, limit_ns);
         }

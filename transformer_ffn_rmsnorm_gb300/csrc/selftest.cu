@@ -85,7 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128)
         __syncwarp();
         ptx::cluster_sync();
     }
-    end_pair<kSlots>(s_end, rank, produced, &s_abort, &s_never, 1000000000ull, full, [](int) { return kBytes; });
+    end_pair<kSlots>(s_end, rank, produced, &s_abort, &s_never, 1000000000ull, full, [](int, int) { return kBytes; });
     int bad = 0;
     for (int s = 0; s < kSlots && s < loads; ++s) {
         const int i = s + (loads - 1 - s) / kSlots * kSlots;   // the last load into the slot
