@@ -459,9 +459,12 @@ typedef struct {
  *   codes and scales of each matrix are written transposed, [d x rows] and
  *   [ceil(d / 128) x ceil(rows / 128)] (rows % 16 == 0): the same values as the
  *   weight of dX = dY W for ffn_linear_e4m3.
- *   x of `dtype`; x, q and scales do not overlap.  A NaN in a block makes its
- *   scale NaN; an infinity makes it infinite, itself NaN and the block's other
- *   values 0.  FFN_ERR_FLAGS for another flag or a transposed block of rows,
+ *   x of `dtype`; x, q and scales do not overlap.  Any rows of a batch will do: x and q
+ *   are aligned to 16 bytes where d % 16 == 0; other rows of whole 16-byte vectors
+ *   begin on 16 bytes in x and on 8 (FFN_F32: 4) in q; else x is aligned to its
+ *   type's size.  A NaN in a block makes its scale NaN; an infinity makes it
+ *   infinite, itself NaN and the block's other values 0.  FFN_ERR_FLAGS for another
+ *   flag or a transposed block of rows,
  *   FFN_ERR_SHAPE for another block, or more than 2^30 scales.
  * ---------------------------------------------------------------------- */
 #define FFN_QUANT_TRANSPOSE 1u

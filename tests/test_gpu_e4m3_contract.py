@@ -47,3 +47,25 @@ def test_quantize_bit_for_bit(env, rows, d, block_rows, group, dtype):
     want, scales = quantized(torch, x, block_rows, group)
     assert torch.equal(s, scales)
     assert torch.equal(q.view(torch.uint8), want)
+
+
+# ------------------------------------------------------------------ rows of a batch
+@pytest.mark.parametrize("d", [1, 7, 130, 132, 136, 264, 1001])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_quantize_any_rows_of_a_batch(env, d, dtype):
+    """x and q begin where a row does, or where an element does if rows are read one by one; what is around stays."""
+    torch, ffn = env
+    dt = getattr(torch, dtype)
+    x = torch.randn(10, d, device="cuda").to(dt)
+    for first, rows in ((1, 4), (3, 7), (9, 1)):
+        part = x[first:first + rows]
+        room = torch.full((10, d), 3.0, device="cuda").to(torch.float8_e4m3fn)
+        q = room[first:first + rows]
+        _, s = ffn.ffn_quantize_e4m3(part, out=q)
+        u.check_quantized(torch, q, s, part.double(), torch.zeros(rows, d, device="cuda", dtype=torch.float64))
+        assert bool((room[:first].float() == 3).all()) and bool((room[first + rows:].float() == 3).all())
+    if d * x.element_size() % 16:
+        flat = torch.randn(4 * d + 1, device="cuda").to(dt)[1:].view(4, d)
+        q = torch.zeros(4 * d + 3, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[3:].view(4, d)
+        _, s = ffn.ffn_quantize_e4m3(flat, out=q)
+        u.check_quantized(torch, q, s, flat.double(), torch.zeros(4, d, device="cuda", dtype=torch.float64))

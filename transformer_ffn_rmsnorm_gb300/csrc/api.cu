@@ -1090,9 +1090,14 @@ ffn_status ffn_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t b
     const int64_t ng = (d + group - 1) / group, nr = blocks ? (rows + 127) / 128 : rows;
     if (batch * nr > kMostElements || batch * nr * ng > kMostElements) return FFN_ERR_SHAPE;   // launched blocks
     if (rows == 0 || batch == 0) return FFN_OK;
-    if (!aligned16(x) || !aligned16(q) || !aligned(scales, 4)) return FFN_ERR_ALIGN;
+    // as any rows of a batch are: those of whole vectors begin on 16 bytes, their codes on a vector's; others are
+    // read one by one
+    const size_t es = dtype_size(dtype);
+    const bool vectors = d * es % 16 == 0;
+    if (!aligned(x, vectors ? 16 : es) || !aligned(q, d % 16 == 0 ? 16 : vectors ? 16 / es : 1) || !aligned(scales, 4))
+        return FFN_ERR_ALIGN;
     const size_t n = static_cast<size_t>(batch) * rows * d;
-    const Range rx{x, n * dtype_size(dtype)}, rq{q, n}, rs{scales, static_cast<size_t>(batch * nr * ng) * 4};
+    const Range rx{x, n * es}, rq{q, n}, rs{scales, static_cast<size_t>(batch * nr * ng) * 4};
     if (overlaps(rq, rx) || overlaps(rs, rx) || overlaps(rq, rs)) return FFN_ERR_ALIAS;
     return from_cuda(launch_quantize_e4m3(x, q, scales, batch, rows, d, group, blocks, transpose, dtype,
                                           static_cast<cudaStream_t>(stream)));
