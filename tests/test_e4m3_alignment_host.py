@@ -40,3 +40,16 @@ def test_quantize_blocks(flags):
         return lib.ffn_quantize_e4m3(x, q, x, 1, 32, 48, 128, 128, _lib.FFN_BF16, flags, None)
     assert call(P[0], P[1]) == ALIAS and call(P[0] + 48 * 2, P[1] + 48) == ALIAS
     assert call(P[0] + 8, P[1]) == ALIGN and call(P[0], P[1] + 8) == ALIGN
+
+
+@pytest.mark.parametrize("ffn", [8, 128, 264, 1000])
+def test_gateup_rows_of_a_batch(ffn):
+    lib = _lib.load()
+
+    def call(q):
+        return lib.ffn_gateup_e4m3(P[0], P[1], weight(P[2], P[3]), weight(P[4], P[5]), P[6], q, P[1], 3, 64, ffn, 2,
+                                   None)   # the scales overlap x's
+    for row in range(1, 5):
+        assert call(P[7] + row * ffn) == ALIAS, row
+    assert call(P[7] + 8) == ALIAS
+    assert call(P[7] + 4) == ALIGN and call(P[7] + 1) == ALIGN

@@ -69,3 +69,19 @@ def test_quantize_any_rows_of_a_batch(env, d, dtype):
         q = torch.zeros(4 * d + 3, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[3:].view(4, d)
         _, s = ffn.ffn_quantize_e4m3(flat, out=q)
         u.check_quantized(torch, q, s, flat.double(), torch.zeros(4, d, device="cuda", dtype=torch.float64))
+
+
+@pytest.mark.parametrize("start,end", [(1, 30), (3, 4), (37, 333)])
+@pytest.mark.parametrize("out", [264, 136])
+def test_gateup_into_any_rows_of_a_batch(env, start, end, out):
+    """Codes whose rows begin on 8 bytes; what is around stays."""
+    torch, ffn = env
+    x, (wg, wu) = u.make(torch, 333, 400, [out, out], 0, 4)
+    p = (x[0][start:end], x[1][start:end])
+    room = torch.full((333, out), 3.0, device="cuda").to(torch.float8_e4m3fn)
+    q, s = ffn.ffn_gateup_e4m3(*p, wg, wu, out=room[start:end])
+    u.check_gateup(torch, q, s, p, wg, wu, 400)
+    assert bool((room[:start].float() == 3).all()) and bool((room[end:].float() == 3).all())
+    whole, scales = ffn.ffn_gateup_e4m3(*p, wg, wu)
+    assert torch.equal(whole.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s, scales)
+    ffn.ffn_device_status()

@@ -1131,7 +1131,7 @@ ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_wei
     const ffn_status st = check_e4m3(x, x_scales, w, 2, offsets, rows, d, ffn, experts);
     if (st != FFN_OK) return st;
     if (rows == 0) return FFN_OK;
-    if (!aligned16(q) || !aligned(scales, 4)) return FFN_ERR_ALIGN;
+    if (!aligned(q, 8) || !aligned(scales, 4)) return FFN_ERR_ALIGN;   // (rows of whole 8 bytes)
     const Range rq{q, static_cast<size_t>(rows) * ffn}, rs{scales, static_cast<size_t>(rows) * ((ffn + 127) / 128) * 4};
     for (const Range &o : {rq, rs})
         if (overlaps_e4m3(o, x, x_scales, w, 2, offsets, rows, d, ffn, experts)) return FFN_ERR_ALIAS;
