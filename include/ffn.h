@@ -498,7 +498,8 @@ ffn_status ffn_linear_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_wei
  * with a scale for each 128 of its features: q [rows x ffn], scales [rows x
  * ceil(ffn / 128)], what ffn_linear_e4m3 takes as x where ffn % 16 == 0.
  * w_gate, w_up [experts x ffn x d]; offsets, limits (in = d, out = ffn) and
- * untouched rows as there.  q and scales overlap nothing.
+ * untouched rows as there.  q and scales overlap nothing; q is aligned to 8
+ *   bytes, as any rows of a batch are.
  * ---------------------------------------------------------------------- */
 ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w_gate, ffn_e4m3_weight w_up,
                            const int32_t *offsets, uint8_t *q, float *scales, int64_t rows, int64_t d, int64_t ffn,
