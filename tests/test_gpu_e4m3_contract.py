@@ -85,3 +85,47 @@ def test_gateup_into_any_rows_of_a_batch(env, start, end, out):
     whole, scales = ffn.ffn_gateup_e4m3(*p, wg, wu)
     assert torch.equal(whole.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s, scales)
     ffn.ffn_device_status()
+
+
+# ------------------------------------------------------------------ offsets that fall
+def falling(rows):
+    """Offsets and where each expert's rows begin and end: an offset below one before it counts as that one, and what
+    is beyond 0 .. rows as the nearest of the two."""
+    few = [-5, 9, 4, 20, rows + 1000, 30]
+    many = [min(e * 2, rows - 8) for e in range(71)]
+    many[31], many[32], many[33] = rows - 20, 3, rows - 18        # falls from the 32nd expert on, and rises
+    many[63], many[64], many[65] = rows - 6, -100, rows - 7        # the same at the 64th
+    for e in range(34, 63):
+        many[e] = rows - 30 + e // 3                               # (below what came before, then beyond it)
+    for off in (few, many):
+        top, at = 0, []
+        for v in off:
+            top = max(top, min(max(v, 0), rows))
+            at.append(top)
+        yield off, at
+
+
+@pytest.mark.parametrize("rows", [40, 240, 900, 5000])
+@pytest.mark.parametrize("experts", [5, 70])
+@pytest.mark.parametrize("out", [136, 384])
+def test_offsets_that_fall(env, rows, experts, out):
+    """Every row is its one expert's, also across the groups of 32 experts that are looked at together; rows of no
+    expert stay."""
+    torch, ffn = env
+    (off, at), = [c for c in falling(rows) if len(c[0]) == experts + 1]
+    x, (wg, wu) = u.make(torch, rows, 256, [out, out], experts, rows)
+    given = torch.tensor(off, dtype=torch.int32, device="cuda")
+    counts = torch.tensor(at, dtype=torch.int32, device="cuda")
+    first, end = at[0], at[-1]
+    room = torch.full((rows + 64, out), 7.0, device="cuda")
+    ffn.ffn_linear_e4m3(*x, wg, offsets=given, out=room[:rows])
+    ref, mag = u.product(torch, x, wg, counts)
+    s = slice(first, end)
+    u.check_linear(torch, room[s], ref[s], mag[s], 256)
+    assert bool((room[:first] == 7).all()) and bool((room[end:] == 7).all())
+    codes = torch.full((rows + 64, out), 3.0, device="cuda").to(torch.float8_e4m3fn)
+    sc = torch.full((rows + 64, -(-out // 128)), 5.0, device="cuda")
+    ffn.ffn_gateup_e4m3(*x, wg, wu, offsets=given, out=codes[:rows], scales=sc[:rows])
+    u.check_gateup(torch, codes[:rows], sc[:rows], x, wg, wu, 256, counts, s)
+    assert bool((codes[end:].float() == 3).all()) and bool((sc[end:] == 5).all())
+    ffn.ffn_device_status()
