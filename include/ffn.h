@@ -476,7 +476,10 @@ ffn_status ffn_quantize_e4m3(const void *x, uint8_t *q, float *scales, int64_t b
  *   x_scales[r, b] * w.scales[o / 128, b] * sum_{i in b} x[r, i] * w.codes[o, i]
  *   The products of codes are exact and added in fp32 block by block, the blocks
  *   in fp32 (for few rows in up to 8 parts, added in a fixed order: the same bits
- *   every run), res last; one rounding to `dtype` (any).
+ *   every run), res last; one rounding to `dtype` (any).  A block's two scales are
+ *   multiplied first, in fp32: their product is 0 or from 2^-126 to below 2^128 in
+ *   size.  A smaller one loses bits (below 2^-149 the block counts nothing), a
+ *   larger one is infinite, and NaN times a sum of 0.
  *   offsets NULL: w is one matrix, experts 1.  Else offsets [experts + 1] int32
  *   on the device, read when the call runs: rows offsets[e] .. offsets[e + 1] - 1
  *   are multiplied with expert e's matrix (ffn_moe_sort's offsets); rows of no

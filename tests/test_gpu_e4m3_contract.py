@@ -129,3 +129,23 @@ def test_offsets_that_fall(env, rows, experts, out):
     u.check_gateup(torch, codes[:rows], sc[:rows], x, wg, wu, 256, counts, s)
     assert bool((codes[end:].float() == 3).all()) and bool((sc[end:] == 5).all())
     ffn.ffn_device_status()
+
+
+# ------------------------------------------------------------------ range of scales
+@pytest.mark.parametrize("rows", [1, 24, 48, 200, 700])
+@pytest.mark.parametrize("ex,ew", [(-63, -63), (-126, 0), (0, -126), (-90, -36), (60, 60), (110, 10)])
+def test_scales_whose_product_is_at_the_end_of_its_range(env, rows, ex, ew):
+    """Powers of two whose product is a normal fp32 number, the smallest among them, times whole numbers: exact."""
+    torch, ffn = env
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+
+    def whole(*shape):
+        return torch.randint(-1, 2, shape, generator=gen, device="cuda").float().to(torch.float8_e4m3fn)
+    xq, wq = whole(rows, 400), whole(264, 400)
+    xs = torch.full((rows, 4), 2.0, device="cuda", dtype=torch.float64).pow(ex).float()
+    ws = torch.full((3, 4), 2.0, device="cuda", dtype=torch.float64).pow(ew).float()
+    xq.view(torch.uint8)[:, 60:] = 0      # |sums| <= 60 in the first block, 0 in the others
+    y = ffn.ffn_linear_e4m3(xq, xs, (wq, ws), dtype=torch.float32)
+    want = (xq.double() @ wq.double().T) * 2.0 ** (ex + ew)
+    assert torch.equal(y.double(), want)
+    ffn.ffn_device_status()
