@@ -497,12 +497,13 @@ ffn_status ffn_linear_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_wei
 
 /* ------------------------------------------------------------------------
  * ffn_gateup_e4m3 -- the block's first half: h = silu(W_gate x) * (W_up x), both
- * products as in ffn_linear_e4m3, h in fp32 and quantised as ffn_quantize_e4m3 does
- * with a scale for each 128 of its features: q [rows x ffn], scales [rows x
+ * products as in ffn_linear_e4m3, h in fp32 (silu of less than -87.3, 1e-36 and
+ * smaller, counts 0) and quantised as ffn_quantize_e4m3 does with a scale for each
+ * 128 of its features: q [rows x ffn], scales [rows x
  * ceil(ffn / 128)], what ffn_linear_e4m3 takes as x where ffn % 16 == 0.
  * w_gate, w_up [experts x ffn x d]; offsets, limits (in = d, out = ffn) and
- * untouched rows as there.  q and scales overlap nothing; q is aligned to 8
- *   bytes, as any rows of a batch are.
+ * untouched rows as there.  q and scales overlap nothing; q is aligned to 8 bytes,
+ * as any rows of a batch are.
  * ---------------------------------------------------------------------- */
 ffn_status ffn_gateup_e4m3(const uint8_t *x, const float *x_scales, ffn_e4m3_weight w_gate, ffn_e4m3_weight w_up,
                            const int32_t *offsets, uint8_t *q, float *scales, int64_t rows, int64_t d, int64_t ffn,

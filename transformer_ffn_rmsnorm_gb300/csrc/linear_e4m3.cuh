@@ -19,7 +19,6 @@ namespace ffn {
 namespace e4 {
 
 enum Mode { LINEAR = 0, GATEUP = 1 };
-enum Out { Y_F32 = DT_F32, Y_F16 = DT_F16, Y_BF16 = DT_BF16 };
 
 struct Params {
     const float *xs;          // [rows x nkb]
@@ -97,11 +96,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 // silu(gate) * up = gate / (1 + 2^(-gate log2 e)) * up, within (5 + |gate|) 2^-23 of
-// the value (the exponent is off by an ulp of itself), 2e-6 where silu is not
-// vanishing, |gate| < 16, next to half a step of e4m3, 6e-2; 0 below gate = -87,
-// where silu is under 1e-36.  (With the forms that keep subnormals, whose fix-ups
-// are as many instructions again, gate/up of 4096 tokens 4096 -> 11008 took 279 us
-// instead of 274.)
+// the value (the exponent is off by an ulp of itself), 2.5e-6 where silu is not
+// vanishing, |gate| < 16, next to half a step of e4m3, 6e-2; 0 below gate = -87.3
+// (a denominator beyond 2^126), where |silu| is 1e-36 and less.  (With the forms
+// that keep subnormals, whose fix-ups are as many instructions again, gate/up of
+// 4096 tokens 4096 -> 11008 took 279 us instead of 274.)
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float swiglu(float gate, float up) {
     return gate * rcp_approx(1.0f + exp2_approx(gate * -kLog2e)) * up;

@@ -81,7 +81,7 @@ template <int TILE> __device__ __forceinline__ UnitInfo find_unit(const Params &
             u.f = local / nt;
             u.row0 = a + tt * width;
             u.valid = min(width, b - u.row0);
-            u.n = (max(u.valid, 1) + 15) & ~15;   // (widths rounded up may leave the last tile empty)
+            u.n = (u.valid + 15) & ~15;   // (nt - 1 tiles of at most TILE rows leave the last one some)
             return u;
         }
         tiles_before += __shfl_sync(0xffffffffu, incl, 31);

@@ -112,7 +112,7 @@ __device__ __forceinline__ void for_row_boxes(const RowMaps &maps, int rows, F l
 }
 
 // silu(gate) * up * scale in fp32.  The division is the approximate one (2 ulp,
-// and 0 for a denominator beyond 2^126, where silu is below 1e-36), and so is the
+// and 0 for a denominator beyond 2^126, where |silu| is about 1e-36), and so is the
 // exponential (2 + 1.17 |gate| ulp, 105 at the end of its range): together at
 // most 1.3e-5 of the value, a fortieth of fp16's half step, and a third of the
 // instructions of the accurate forms in epilogues that the MMAs wait for.

@@ -20,7 +20,6 @@
 // copy.  (1026 pairs 7.1 us by a cluster, 8.8 by chunks; 24576, three pieces a CTA of a
 // cluster, 27.6 and 24.6.)
 #include <algorithm>
-#include <atomic>
 
 #include "moe.cuh"
 #include "moe_sort.cuh"
