@@ -149,3 +149,26 @@ def test_scales_whose_product_is_at_the_end_of_its_range(env, rows, ex, ew):
     want = (xq.double() @ wq.double().T) * 2.0 ** (ex + ew)
     assert torch.equal(y.double(), want)
     ffn.ffn_device_status()
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_silu_that_vanishes(env, rows):
+    """Gates of -80, -88 and -96 beside an up of 2^100: the last two count 0, the first does not."""
+    torch, ffn = env
+    codes = torch.zeros(24, 16, device="cuda")
+    codes[:, 0] = torch.tensor([-320.0, -352.0, -384.0], device="cuda").repeat_interleave(8)
+    x = torch.zeros(rows, 16, device="cuda")
+    x[:, 0] = 1
+    one = torch.ones(1, 1, device="cuda")
+    up = torch.zeros(24, 16, device="cuda")
+    up[:, 0] = 1
+
+    def e4m3(v):
+        return v.to(torch.float8_e4m3fn)
+    q, s = ffn.ffn_gateup_e4m3(e4m3(x), torch.ones(rows, 1, device="cuda"), (e4m3(codes), one * 0.25),
+                               (e4m3(up), one * 2.0 ** 100))
+    g = torch.tensor(-80.0, dtype=torch.float64)
+    h = (g * torch.sigmoid(g) * 2.0 ** 100).abs()
+    assert bool(((s.double().cpu() - h / 448).abs() <= h / 448 * (6 + 1.17 * 80) * 2.0 ** -23).all())
+    assert bool((q[:, :8].float() == -448).all()) and bool((q[:, 8:].float() == 0).all())
+    ffn.ffn_device_status()
