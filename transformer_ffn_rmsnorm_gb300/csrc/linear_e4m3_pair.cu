@@ -10,13 +10,14 @@
 // eight accumulators: 0.31 us a block against 0.42, for half the work.
 //
 // What bounds it: each block's sums have to leave tensor memory before the block
-// after next may use their place.  The tensor pipe needs 512 cycles a block and SM
-// and reads its accumulators at 75 % of tensor memory's rate, the epilogue warps'
-// loads are the other 25 %, their additions 256 cycles of the FMA pipe (two an
-// instruction); but the way of a half -- instructions issued, sums done, seen,
-// read and added, their leave sent back across the pair, seen -- is about 1300
-// cycles, of which two halves' 512 are hidden: 790 cycles a block.  (4096 tokens,
-// 4096 -> 11008 gate/up: 274 to 283 us.  An earlier form took 349; with nothing read or
+// after next may use their place.  The tensor pipe needs 512 cycles a block and SM,
+// the additions 256 of the FMA pipe (two an instruction); but the way of a half --
+// instructions issued, sums done, seen, read and added, their leave sent back across
+// the pair, seen -- is about 1300 cycles, of which two halves' 512 are hidden: 790
+// cycles a block.  Nothing else is near its limit: of the cycles the tensor pipe is
+// active in 60 %, instructions issue in 52, the FMA pipe works in 24, and tensor memory
+// is read at 30 % of its peak, three quarters of it the pipe's own accumulators.
+// (4096 tokens, 4096 -> 11008 gate/up: 273 to 283 us.  An earlier form took 349; with nothing read or
 // added 252, with one such handshake in 16 blocks 195.  16 warps of 64
 // columns, whose sums do not fit beside what else the registers hold, 441; one warp
 // issuing both halves' MMAs 387.)

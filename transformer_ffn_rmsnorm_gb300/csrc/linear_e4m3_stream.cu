@@ -463,17 +463,19 @@ cudaError_t launch_e4m3_stream(e4::Mode mode, bool wide, int splits, const uint8
 }
 
 // Which kernel, from the sizes alone (of the experts' rows only the mean is known
-// here).  Up to 32 rows an expert the stream of weights: dense 4096 -> 14336
-// gate/up, 32 rows 27.9 us, pairs 34.0, 48 rows (two tiles) 40 and 34; over 64
-// experts of 2048 x 1408 with 24 rows 79 and 90, with 48 rows 111 and 92.  Beyond
-// that gate/up runs on the pairs, linear there or in tiles of 128 rows, which cut
-// the reduction where few units leave the pairs idle: by the estimates below, us.
-// Linear 14336 -> 4096, pairs / tiles of 128: 48 rows 50.6 / 15.2, 128 rows 51.7 /
-// 21.5, 256 rows 51.7 / 35.9, 512 rows 52.3 / 65.2; 4096 -> 14336, 64 rows 19.1 /
-// 18.3, 128 rows 20.5 / 27.3; 64 experts 1408 -> 2048, 48 rows 53.6 / 77.7.  The pairs'
+// here: 64 experts of 2048 x 1408, 626 rows evenly or 500 of them one expert's, which
+// reads its weights 16 times, 72.6 and 72.8 us gate/up; 1536 rows, 24 each or 1473 of
+// one, 81.4 and 96.7).  Up to 32 rows an expert the stream of weights: dense 4096 ->
+// 14336 gate/up, 32 rows 27.3 us, pairs 32.7, 48 rows (two tiles) 37.5 and 32.8; over
+// 64 experts of 2048 x 1408 with 24 rows 80.6 and 83.5, with 48 rows 110 and 84.4.
+// Beyond that gate/up runs on the pairs, linear there or in tiles of 128 rows, which
+// cut the reduction where few units leave the pairs idle: by the estimates below, us.
+// Linear 14336 -> 4096, pairs / tiles of 128: 48 rows 47.3 / 15.0, 128 rows 48.4 /
+// 21.2, 256 rows 48.8 / 35.5, 512 rows 49.4 / 64.5; 4096 -> 14336, 64 rows 18.3 /
+// 18.2, 128 rows 19.8 / 27.1; 64 experts 1408 -> 2048, 48 rows 46.4 / 77.8.  The pairs'
 // units have 256 features, or 128 where that takes as few rounds: 14336 -> 4096, 512
-// rows 50.2 / 38.5, 640 rows 54.3 / 75.6, 1024 rows 52.1 / 72.9; 512 rows of 2048 ->
-// 2048 12.5 / 9.6; 777 rows of 1024 -> 520 10.9 / 8.3.
+// rows 49.5 / 38.5, 640 rows 50.9 / 72.5, 1024 rows 51.5 / 72.9; 512 rows of 2048 ->
+// 2048 12.0 / 9.5; 777 rows of 1024 -> 520 8.9 / 7.0.
 cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *w0, const uint8_t *w1, int64_t in,
                                 Params p, cudaStream_t s) {
     p.nf = (p.out + 127) / 128;
@@ -483,8 +485,8 @@ cudaError_t launch_e4m3_product(e4::Mode mode, const uint8_t *x, const uint8_t *
     const int64_t sms = sm_count(), used = std::min<int64_t>(p.rows, p.experts), mean = (p.rows + used - 1) / used;
     auto units = [&](int tile) { return used * ((mean + tile - 1) / tile) * p.nf; };
     // The most parts of the reduction whose CTAs all run at once, two blocks each: 4096 ->
-    // 14336 gate/up, 1 row, 112 units in 1, 2, 4, 8 parts 25.1, 23.8, 28.5, 40.8 us;
-    // linear 14336 -> 4096, 32 units 37.2, 21.0, 13.0, 11.9.
+    // 14336 gate/up, 1 row, 112 units in 1, 2, 4, 8 parts 24.9, 23.5, 29.3, 42.2 us;
+    // linear 14336 -> 4096, 32 units 36.8, 20.7, 12.7, 11.7.
     auto parts = [&](int tile, int64_t slots) {
         int n = 8;
         while (n > 1 && (n * units(tile) > slots || 2 * n > p.nkb)) n >>= 1;
