@@ -1,4 +1,4 @@
-"""README.md's examples, to be run as they stand there."""
+"""The documented examples, to be run as they stand."""
 
 import os
 import re

@@ -1,4 +1,4 @@
-"""README.md's gradient of the routed 8-bit layer, run as it stands there: each step against its formula in 64 bits on
+"""The documented gradient of the routed 8-bit layer, run as it stands: each step against its formula in 64 bits on
 what the step before wrote (tolerances: e4m3_util; the chain itself: test_layer_gradient_host)."""
 
 import pytest

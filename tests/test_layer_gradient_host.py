@@ -1,4 +1,4 @@
-"""README.md's gradient of the routed 8-bit layer is the layer's gradient: the examples, run as they stand on a plain
+"""The documented gradient of the routed 8-bit layer is the layer's gradient: the examples, run as they stand on a plain
 64-bit implementation of the entry points that rounds nothing, against autograd and against differences (CPU)."""
 
 import pytest
