@@ -42,6 +42,8 @@ __global__ void __launch_bounds__(64) bounded_wait_probe_kernel(uint64_t limit_n
     __syncthreads();
 }
 
+constexpr uint64_t kProbeWaitNs = 1000000000ull;
+
 // Load number i of CTA r brings rows 32 (2 i + r) .. of src (rows of 128 bytes) to slot i %
 // kPairProbeSlots.  Whole rounds that both CTAs load are waited for, as the MMAs would; what the
 // last slots hold when the pair ends is compared with src, byte for byte, into wrong[r].
@@ -81,11 +83,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128)
         if (i0 == rounds * kSlots) break;
         if (rank == 0 && threadIdx.x == 0)
             for (int s = 0; s < kSlots; ++s)
-                if (!ptx::mbar_wait(full(s), (i0 / kSlots) & 1u, &s_never, 1000000000ull)) atomicOr(err, DEVERR_TIMEOUT);
+                if (!ptx::mbar_wait(full(s), (i0 / kSlots) & 1u, &s_never, kProbeWaitNs)) atomicOr(err, DEVERR_TIMEOUT);
         __syncwarp();
         ptx::cluster_sync();
     }
-    end_pair<kSlots>(s_end, rank, produced, &s_abort, &s_never, 1000000000ull, full, [](int, int) { return kBytes; });
+    end_pair<kSlots>(s_end, rank, produced, &s_abort, &s_never, kProbeWaitNs, full, [](int, int) { return kBytes; });
     int bad = 0;
     for (int s = 0; s < kSlots && s < loads; ++s) {
         const int i = s + (loads - 1 - s) / kSlots * kSlots;   // the last load into the slot
